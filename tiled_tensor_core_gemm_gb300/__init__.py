@@ -16,12 +16,23 @@ raises.
         torch-tensor convenience: row-major CUDA tensors in, FP32 C out.
     gemm_ex(A, B, C=None, alpha=1, beta=0, bias=None, act="none", out="f32", ...) -> C
         the same with the fused epilogue.
+
+The operators of an expert layer (include/gemm_ops.h; ops.py has their
+documentation):
+
+    quantize_block(x, block) -> (q, scale)              FP8 with a scale for each block of 128
+    gemm_scaled(A, a_scale, B, b_scale) -> C            their product
+    gemm_experts(A, a_scale, W, w_scale, offsets) -> C  one product per expert, sizes on the device
+    route(logits, top_k) -> Routing, route_backward     tokens to experts, and the logits' gradient
+    combine(Y, slots, weights) -> out, combine_backward the weighted sum of the experts' rows
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+
+from . import ops
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libtcgemm.so")
@@ -44,7 +55,8 @@ OUT_TYPES = {"f32": GEMM_OUT_F32, "bf16": GEMM_OUT_BF16, "f16": GEMM_OUT_F16}
 
 EXPORTED = ("gemm_run", "gemm_last_error", "gemm_get_status", "gemm_set_option",
             "gemm_get_option", "gemm_plan", "gemm_version", "gemm_run_tf32_static", "gemm_run_ex",
-            "gemm_run_grouped")
+            "gemm_run_grouped", "gemm_quantize_block", "gemm_run_scaled", "gemm_run_experts", "gemm_route",
+            "gemm_route_backward", "gemm_combine", "gemm_combine_backward")
 TF32_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024   # GEMM_TF32_STATIC_SCRATCH_BYTES in include/gemm.h
 
 
@@ -125,6 +137,7 @@ def load_library():
         lib.gemm_run_ex.restype = ctypes.c_int
         lib.gemm_run_grouped.argtypes = [ctypes.c_int, i64, ctypes.POINTER(GemmGroup), ctypes.POINTER(GemmEpilogue), p]
         lib.gemm_run_grouped.restype = ctypes.c_int
+        ops.declare(lib)
         _lib = lib
         return lib
 
@@ -325,3 +338,7 @@ def gemm_grouped(As, Bs, Cs=None, biases=None, alpha=1.0, beta=0.0, act="none", 
     if rc != GEMM_OK:
         raise GemmError(rc, gemm_last_error())
     return Cs
+
+
+from .ops import (Routing, combine, combine_backward, gemm_experts, gemm_scaled, quantize_block, route,  # noqa: E402
+                  route_backward)

@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "ops.h"
 
 namespace tcgemm {
 namespace {
@@ -692,10 +693,11 @@ int gemm_get_status(struct CUstream_st *stream_) {
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaStreamSynchronize: %s", cudaGetErrorString(e));
     uint32_t w[4] = {0, 0, 0, 0};
     e = tc_read_and_clear_status(w);
+    if (e == cudaSuccess && w[0] == 0) e = scaled_read_and_clear_status(w);
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
     if (w[0] != 0) {
-        static const char *roles[] = {"?", "producer", "mma", "epilogue", "drain"};
-        return fail((int)w[0], "kernel wait expired: role=%s tile=%d block=%u", roles[w[1] < 5 ? w[1] : 0],
+        static const char *roles[] = {"?", "producer", "mma", "epilogue", "drain", "scales"};
+        return fail((int)w[0], "kernel wait expired: role=%s tile=%d block=%u", roles[w[1] < 6 ? w[1] : 0],
                     (int)w[2], w[3]);
     }
     return GEMM_OK;

@@ -1,0 +1,114 @@
+// What the expert-layer operators' translation units share: the argument checks
+// of their C entries, and loads and stores of FP32 / BF16 / FP16 vectors.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cstdio>
+
+#include "gemm_ops.h"
+#include "internal.h"
+
+namespace tcgemm {
+
+// --------------------------------------------------------------- C entries ---
+// A span of device memory an entry point reads or writes.
+struct OpSpan {
+    const char *name;
+    const void *p;
+    uint64_t bytes;   // 0: nothing is touched, the pointer is not looked at
+    int align;        // its element's size
+    bool written;
+};
+
+// The last byte touched + 1 of `rows` rows of `cols` elements, `ld` apart.
+inline uint64_t op_extent(int64_t rows, int64_t cols, int64_t ld, int elem) {
+    return rows > 0 && cols > 0 ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * (uint64_t)elem : 0;
+}
+
+// Checks the spans (NULL, alignment, a written span overlapping another) before
+// any CUDA call, then that the current device is one this library serves and
+// that every span is its memory.  Returns a gemm_status_t; *sms as asked.
+int op_check(const OpSpan *spans, int count, int *sms);
+
+inline int op_type_bytes(int type) { return type == GEMM_OUT_F32 ? 4 : 2; }
+inline bool op_type_ok(int type) { return type == GEMM_OUT_F32 || type == GEMM_OUT_BF16 || type == GEMM_OUT_F16; }
+inline int op_launched(const char *what, cudaError_t e) {
+    if (e == cudaSuccess) return GEMM_OK;
+    char msg[192];
+    std::snprintf(msg, sizeof msg, "%s: %s", what, cudaGetErrorString(e));
+    return api_error(GEMM_ERR_CUDA, msg);
+}
+
+// Reads and clears the status word of the block-scaled product's kernel.
+cudaError_t scaled_read_and_clear_status(uint32_t words[4]);
+
+#ifdef __CUDACC__
+// ----------------------------------------------------------------- vectors ---
+template <typename T> struct OpType;
+template <> struct OpType<float> {
+    static __device__ __forceinline__ float up(float x) { return x; }
+    static __device__ __forceinline__ float down(float x) { return x; }
+};
+template <> struct OpType<__nv_bfloat16> {
+    static __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
+};
+template <> struct OpType<__half> {
+    static __device__ __forceinline__ float up(__half x) { return __half2float(x); }
+    static __device__ __forceinline__ __half down(float x) { return __float2half_rn(x); }
+};
+
+// Eight elements as they sit in memory: 32 bytes of FP32, 16 of the 16-bit types.
+template <typename T> struct alignas(16) OpVec8 {
+    T v[8];
+};
+
+// Eight elements from p; those at `have` and beyond are 0.  `wide`: p is on a
+// 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ OpVec8<T> op_load8(const T *p, int have, bool wide) {
+    OpVec8<T> r;
+    if (wide && have >= 8) {
+        const uint4 *s = reinterpret_cast<const uint4 *>(p);
+        uint4 *d = reinterpret_cast<uint4 *>(r.v);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) * 8 / 16); ++i) d[i] = s[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.v[i] = i < have ? p[i] : OpType<T>::down(0.f);
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void op_store8(T *p, const OpVec8<T> &r, int have, bool wide) {
+    if (wide && have >= 8) {
+        uint4 *d = reinterpret_cast<uint4 *>(p);
+        const uint4 *s = reinterpret_cast<const uint4 *>(r.v);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) * 8 / 16); ++i) d[i] = s[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < have) p[i] = r.v[i];
+    }
+}
+#endif
+
+// Rows of a pitched array all start on 16 bytes.
+inline bool op_wide(const void *p, int64_t ld, int elem) {
+    return (uintptr_t)p % 16 == 0 && ((uint64_t)ld * (uint64_t)elem) % 16 == 0;
+}
+
+// Calls f with a value of the C++ type of `type` (gemm_out_t).
+template <typename F> auto op_by_type(int type, F &&f) {
+    if (type == GEMM_OUT_BF16) return f(__nv_bfloat16());
+    if (type == GEMM_OUT_F16) return f(__half());
+    return f(float());
+}
+
+}  // namespace tcgemm

@@ -1,0 +1,991 @@
+// Products of FP8 matrices with a scale for each block of 128 along K:
+//
+//   D[i][j] = sum_kb sp(i, kb) * sq(j, kb) * sum_{k in kb} P[i][k] * Q[j][k]
+//
+// for one pair of matrices (gemm_run_scaled) or one per expert
+// (gemm_run_experts).  P is the operand whose rows become Tensor Memory lanes,
+// Q the one whose rows become its columns.  With many rows of C, P is A and Q
+// is B^T; with few (a decode step) the roles are swapped, so that the 128 lanes
+// carry the weights' rows and a tile is only as wide as the tokens there are:
+// the MMA, the shared memory and the registers then go with the tokens, and the
+// kernel streams the weights.
+//
+// The scales change every 128 values of K, so an MMA may sum over one K-block
+// only: four MMAs of K = 32 write a fresh accumulator, and epilogue warps add
+// it, scaled, to sums kept in registers.  NBUF accumulators rotate, so the MMAs
+// of the next blocks run meanwhile.  Per K-block of a 128 x 256 tile the MMAs
+// take at least 512 cycles of an SM, reading the accumulator 256 and the
+// multiply-adds (paired, one scale for 128 columns) 128 issue slots a
+// sub-partition; with a scale per column the multiply by it doubles that.
+//
+// Roles: warp 0 issues the TMA loads of P and Q into a ring; warp 1 the MMAs;
+// warp 2 brings the lanes' scales and warp 3 the columns' into a second ring in
+// shared memory; the other warps hold the sums, one lane a thread, and write C.
+// Both operands are read in either major: K-major as rows of 128 bytes, or
+// MN-major in chunks of 128 rows of K by 128 bytes (as tc_gemm.cu reads B).
+// Every wait is bounded as there.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+
+#include "epilogue.cuh"
+#include "ops.h"
+#include "ptx.cuh"
+#include "ptx_ops.cuh"
+
+namespace tcgemm {
+
+__device__ uint32_t g_scaled_status[4];
+
+namespace {
+
+constexpr int kLanes = 128;
+constexpr int kBlockK = 128;
+constexpr int kSmemMax = 232448;
+constexpr int kCtrlBytes = 1024;       // barriers and flags
+constexpr int kScaleSlots = 8;
+constexpr int kMaxExperts = 1024;
+
+enum Role : uint32_t { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleDrain = 4, kRoleScales = 5 };
+
+struct ScaleView {
+    const float *p;
+    int64_t stride_k, stride_i, stride_e;
+    int shift;                 // 7: one for 128 rows, 0: one each
+};
+
+struct ScaledParams {
+    int I, J;                  // rows of P, rows of Q (experts: of the weights' side; the tokens' side is `rows`)
+    int num_kb;
+    int tiles_i, tiles_j;      // experts: of the weights' side
+    int group_i;               // raster: lane tiles taken together
+    int splits;                // CTAs of a cluster that share a tile's K
+    int kb_per_split;
+    int p_mn, q_mn;            // operands stored MN-major
+    uint32_t idesc;
+    ScaleView sp, sq;
+    void *C;
+    int64_t c_i, c_j;          // element strides of D in C
+    int swapped;               // P is B^T: C's columns are D's rows
+    int wide;                  // 16-byte stores along C's rows are aligned
+    EpiParams epi;
+    const int32_t *offsets;    // experts: rows of each
+    int experts, rows;         // 0: one product
+    int tokens_on_i;           // experts: the token rows are D's rows
+    unsigned long long timeout_ns;
+};
+
+template <int BN, bool QVEC, int EW>
+struct Cfg {
+    static constexpr int COLS = BN / (EW / 4);        // columns of a thread
+    static constexpr int CHUNK = COLS < 32 ? COLS : 32;
+    static constexpr int THREADS = 128 + EW * 32;
+    static constexpr bool SPLIT_REGS = COLS > 64;
+    static constexpr int P_BYTES = kLanes * 128;
+    static constexpr int Q_BYTES = BN * 128;
+    static constexpr int STAGE = P_BYTES + Q_BYTES;
+    static constexpr int NBUF = BN >= 256 ? 2 : 4;
+    static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
+    static constexpr int SCALES = kLanes + (QVEC ? BN : 0) + 4;      // floats of a slot: lanes, columns or one
+    static constexpr int SLOT_BYTES = (SCALES * 4 + 15) / 16 * 16;
+    static constexpr int FIXED = 1024 + kCtrlBytes + kScaleSlots * SLOT_BYTES + 2 * (kMaxExperts + 1) * 4 + 32;
+    static constexpr int FIT = (kSmemMax - FIXED) / STAGE;
+    static constexpr int STAGES = FIT > 12 ? 12 : FIT;
+    static constexpr int SMEM = FIXED + STAGES * STAGE;
+    static_assert(!SPLIT_REGS || THREADS == 384, "the register split is written for 384 threads");
+    static_assert(STAGES >= 3 && SMEM <= kSmemMax, "ring");
+    static_assert((2 * STAGES + 2 * NBUF + 2 * kScaleSlots) * 8 + 16 <= kCtrlBytes, "barrier area");
+    static_assert(kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
+};
+
+__device__ __noinline__ void record_failure(uint32_t role, int tile, volatile int *abort_flag) {
+    *abort_flag = 1;
+    if (atomicCAS(&g_scaled_status[0], 0u, (uint32_t)GEMM_ERR_TIMEOUT) == 0u) {
+        g_scaled_status[1] = role;
+        g_scaled_status[2] = (uint32_t)tile;
+        g_scaled_status[3] = blockIdx.x;
+        __threadfence();
+    }
+}
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                         unsigned long long timeout_ns) {
+    if (ptx::mbar_try_wait<false>(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (ptx::mbar_try_wait<false>(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (ptx::globaltimer_ns() - t0 > timeout_ns) return false;
+    }
+}
+
+// The wait of a role that has given up, for what it started itself.
+__device__ __noinline__ void wait_landed(uint32_t bar, uint32_t parity, unsigned long long timeout_ns) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait<false>(bar, parity))
+        if (ptx::globaltimer_ns() - t0 > timeout_ns) return;
+}
+
+// A position in a ring of n slots: its index and the parity of its lap.
+struct Ring {
+    int i = 0;
+    uint32_t phase = 0;
+    bool laps = false;         // been round once
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            phase ^= 1u;
+            laps = true;
+        }
+    }
+};
+
+// One output tile: D's rows [i0, i1) and columns [j0, j1) of expert e (0 outside
+// an expert launch), in the coordinates of the operands' tensor maps.
+struct Tile {
+    int i0, i1, j0, j1, e;
+};
+
+// Tile t of the launch.  Down `group_i` lane tiles, then across the columns:
+// tiles that run together share both operands' panels in L2.
+template <int BN>
+__device__ __forceinline__ Tile tile_at(const ScaledParams &p, const int32_t *first_tile, const int32_t *first_row,
+                                        int t) {
+    Tile T;
+    int e = 0, tiles_i = p.tiles_i, tiles_j = p.tiles_j, r = t;
+    if (p.experts) {
+        int lo = 0, hi = p.experts - 1;       // the last expert whose first tile is at or before t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first_tile[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        e = lo;
+        r = t - first_tile[e];
+        const int rows = first_row[e + 1] - first_row[e];
+        if (p.tokens_on_i) tiles_i = (rows + kLanes - 1) / kLanes;
+        else tiles_j = (rows + BN - 1) / BN;
+    }
+    const int per = p.group_i * tiles_j, g = r / per, first = g * p.group_i;
+    const int gi = min(p.group_i, tiles_i - first);
+    const int in = r - g * per;
+    const int ti = first + in % gi, tj = in / gi;
+    T.e = e;
+    T.i0 = ti * kLanes;
+    T.j0 = tj * BN;
+    T.i1 = p.I;
+    T.j1 = p.J;
+    if (p.experts) {
+        if (p.tokens_on_i) {
+            T.i0 += first_row[e];
+            T.i1 = first_row[e + 1];
+        } else {
+            T.j0 += first_row[e];
+            T.j1 = first_row[e + 1];
+        }
+    }
+    return T;
+}
+
+// The scale of row i (clamped below `end`) in K-block kb of expert e.
+__device__ __forceinline__ float scale_at(const ScaleView &v, int i, int end, int kb, int e) {
+    i = i < end ? i : end - 1;
+    return __ldg(v.p + kb * v.stride_k + (int64_t)(i >> v.shift) * v.stride_i + e * v.stride_e);
+}
+
+// acc += r * s (paired: two columns an instruction).
+template <int N>
+__device__ __forceinline__ void add_scaled(float *acc, const uint32_t (&r)[N], float s) {
+    const float2 s2 = make_float2(s, s);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const float2 v = make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+        const float2 a = __ffma2_rn(v, s2, make_float2(acc[c], acc[c + 1]));
+        acc[c] = a.x;
+        acc[c + 1] = a.y;
+    }
+}
+
+// acc += r * (s * column scale), the scales from shared memory.
+template <int N>
+__device__ __forceinline__ void add_scaled_columns(float *acc, const uint32_t (&r)[N], float s, uint32_t columns) {
+    const float2 s2 = make_float2(s, s);
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+        const float4 q = ptx::ld_shared_v4f(columns + 4u * (uint32_t)c);
+        const float2 t0 = __fmul2_rn(make_float2(q.x, q.y), s2), t1 = __fmul2_rn(make_float2(q.z, q.w), s2);
+        const float2 a0 = __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), t0,
+                                     make_float2(acc[c], acc[c + 1]));
+        const float2 a1 = __ffma2_rn(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), t1,
+                                     make_float2(acc[c + 2], acc[c + 3]));
+        acc[c] = a0.x;
+        acc[c + 1] = a0.y;
+        acc[c + 2] = a1.x;
+        acc[c + 3] = a1.y;
+    }
+}
+
+// One warp's side of the scales of a tile: COUNT of them a K-block, of the rows
+// base, base + STEP, ...  AHEAD K-blocks are loaded together, and the next ones
+// are in flight while these are handed over: a load takes about as long as one
+// K-block's MMAs.
+template <int PER, int COUNT, int STEP>
+__device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int end, int e, int kb0, int kb1, int t,
+                                             Ring &sl, uint8_t *slots, int slot_bytes, uint32_t scf0, uint32_t sce0,
+                                             volatile int *abort_flag, unsigned long long timeout_ns) {
+    constexpr int AHEAD = PER > 4 ? 2 : 4;
+    const int lane = threadIdx.x & 31;
+    float cur[AHEAD][PER], nxt[AHEAD][PER];
+    auto load = [&](int kb) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+                nxt[a][c] = kb + a < kb1 && 32 * c + lane < COUNT
+                                ? scale_at(v, base + (32 * c + lane) * STEP, end, kb + a, e) : 0.f;
+    };
+    load(kb0);
+    for (int kb = kb0; kb < kb1; kb += AHEAD) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+            for (int c = 0; c < PER; ++c) cur[a][c] = nxt[a][c];
+        load(kb + AHEAD);
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            if (kb + a >= kb1) break;
+            const bool got = wait_bar(sce0 + 8u * (uint32_t)sl.i, sl.phase ^ 1u, abort_flag, timeout_ns);
+            if (!__all_sync(0xffffffffu, got)) {
+                if (lane == 0) record_failure(kRoleScales, t, abort_flag);
+                return false;
+            }
+            float *slot = reinterpret_cast<float *>(slots + sl.i * slot_bytes);
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+                if (32 * c + lane < COUNT) slot[32 * c + lane] = cur[a][c];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(scf0 + 8u * (uint32_t)sl.i);
+            sl.next(kScaleSlots);
+        }
+    }
+    return true;
+}
+
+// C's element (row i of D, column j) from its whole sum.
+__device__ __forceinline__ void write_one(const ScaledParams &p, const Tile &T, int row, int col, float v) {
+    const int64_t i = (int64_t)T.i0 + row, j = (int64_t)T.j0 + col;
+    if (i >= T.i1 || j >= T.j1) return;
+    const int64_t n = p.swapped ? i : j;
+    epi_write(p.epi, p.C, i * p.c_i + j * p.c_j, v, epi_bias(p.epi, n, n + 1));
+}
+
+// A thread's columns of its row.
+template <int COLS>
+__device__ __forceinline__ void write_row(const ScaledParams &p, const Tile &T, int row, int col0,
+                                          const float (&acc)[COLS]) {
+    const int64_t i = (int64_t)T.i0 + row, j = (int64_t)T.j0 + col0;
+    if (p.swapped || !p.wide || j + COLS > T.j1) {
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) write_one(p, T, row, col0 + c, acc[c]);
+        return;
+    }
+    if (i >= T.i1) return;
+    const int64_t at = i * p.c_i + j;
+    const bool half = p.epi.active && p.epi.out != GEMM_OUT_F32;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 8) {
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            y[k] = acc[c + k];
+            if (p.epi.active)
+                y[k] = epi_value(p.epi, y[k], p.epi.beta != 0.f ? epi_load_old(p.C, at + c + k, p.epi.out) : 0.f,
+                                 epi_bias(p.epi, j + c + k, j + c + k + 1));
+        }
+        if (half) {
+            uint4 w;
+            w.x = epi_pack2(p.epi.out, y[0], y[1]);
+            w.y = epi_pack2(p.epi.out, y[2], y[3]);
+            w.z = epi_pack2(p.epi.out, y[4], y[5]);
+            w.w = epi_pack2(p.epi.out, y[6], y[7]);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.C) + at + c) = w;
+        } else {
+            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at + c);
+            d[0] = make_float4(y[0], y[1], y[2], y[3]);
+            d[1] = make_float4(y[4], y[5], y[6], y[7]);
+        }
+    }
+}
+
+template <int BN, bool QVEC, int EW>
+__global__ void __launch_bounds__(Cfg<BN, QVEC, EW>::THREADS, 1)
+scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const ScaledParams p) {
+    using Cf = Cfg<BN, QVEC, EW>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + Cf::STAGES * Cf::STAGE);
+    uint8_t *scales = reinterpret_cast<uint8_t *>(bars) + kCtrlBytes;
+    int32_t *first_tile = reinterpret_cast<int32_t *>(scales + kScaleSlots * Cf::SLOT_BYTES);
+    int32_t *first_row = first_tile + kMaxExperts + 1;
+    constexpr int kBars = 2 * Cf::STAGES + 2 * Cf::NBUF + 2 * kScaleSlots;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const uint32_t bar0 = ptx::smem_addr(bars);
+    auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+    auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(Cf::STAGES + s); };
+    auto accf = [&](int b) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + b); };
+    auto acce = [&](int b) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + b); };
+    auto scf = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + 2 * Cf::NBUF + s); };
+    auto sce = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + 2 * Cf::NBUF + kScaleSlots + s); };
+    const uint32_t scales0 = ptx::smem_addr(scales), scf0 = scf(0), sce0 = sce(0);
+
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t crank = p.splits > 1 ? ptx::cluster_ctarank() : 0u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cf::STAGES; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < Cf::NBUF; ++b) {
+            ptx::mbar_init(accf(b), 1);
+            ptx::mbar_init(acce(b), EW);
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            ptx::mbar_init(scf(s), 2);       // the lanes' and the columns' scale warps
+            ptx::mbar_init(sce(s), EW);
+        }
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        if (p.num_kb > 0) {
+            ptx::prefetch_tensormap(&tmP);
+            ptx::prefetch_tensormap(&tmQ);
+        }
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<1>(ptx::smem_addr(tmem_slot), Cf::TMEM_COLS);
+        ptx::tmem_relinquish<1>();
+    }
+    // Global memory from here on: the previous kernel on the stream is done.
+    ptx::pdl_wait();
+    if (threadIdx.x == 0) ptx::pdl_launch_dependents();
+    if (p.experts && warp == 2) {
+        // The experts' first rows and first tiles.  Offsets are clamped to
+        // ascending values within [0, rows].
+        int32_t row = 0, tile = 0;
+        for (int e0 = 0; e0 <= p.experts; e0 += 32) {
+            const int e = e0 + (int)lane;
+            int32_t o = e <= p.experts ? min(max(p.offsets[e], 0), p.rows) : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, o, d);
+                if ((int)lane >= d) o = max(o, y);
+            }
+            o = max(o, row);
+            if (e <= p.experts) first_row[e] = o;
+            int32_t before = __shfl_up_sync(0xffffffffu, o, 1);
+            if (lane == 0) before = e0 ? row : o;
+            // tiles of the expert that ends here (e - 1)
+            const int n = e > 0 && e <= p.experts ? o - before : 0;
+            int32_t c = p.tokens_on_i ? (n + kLanes - 1) / kLanes * p.tiles_j : (n + BN - 1) / BN * p.tiles_i;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, c, d);
+                if ((int)lane >= d) c += y;
+            }
+            c += tile;
+            if (e <= p.experts) first_tile[e] = c;
+            row = __shfl_sync(0xffffffffu, o, 31);
+            tile = __shfl_sync(0xffffffffu, c, 31);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int num_tiles = p.experts ? first_tile[p.experts] : p.tiles_i * p.tiles_j;
+    const int unit = (int)blockIdx.x / p.splits, units = (int)gridDim.x / p.splits;
+    const int kb0 = (int)crank * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
+
+    // 128 columns a thread need more than the launch's 168 registers: the first
+    // warpgroup gives the difference (128 x 72 + 256 x 216 = 384 x 168).
+    if (warp < 4) {
+        if (Cf::SPLIT_REGS) ptx::regs_give_back<72>();
+        if (warp == 0) {
+            // ------------------------------------------------------ TMA producer
+            if (lane == 0) {
+                Ring rg;
+                bool ok = true;
+                for (int t = unit; ok && t < num_tiles; t += units) {
+                    const Tile T = tile_at<BN>(p, first_tile, first_row, t);
+                    const int ep = p.tokens_on_i ? 0 : T.e, eq = p.tokens_on_i ? T.e : 0;
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!wait_bar(empty(rg.i), rg.phase ^ 1u, abort_flag, p.timeout_ns)) {
+                            record_failure(kRoleProducer, t, abort_flag);
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t fb = full(rg.i), sp = ptx::smem_addr(ring + rg.i * Cf::STAGE),
+                                       sq = sp + Cf::P_BYTES;
+                        ptx::mbar_arrive_expect_tx(fb, (uint32_t)Cf::STAGE);
+                        const int k0 = kb * kBlockK;
+                        if (p.p_mn) ptx::tma_load_3d(sp, &tmP, fb, T.i0, k0, ep);
+                        else ptx::tma_load_3d(sp, &tmP, fb, k0, T.i0, ep);
+                        if (p.q_mn) {
+#pragma unroll
+                            for (int c = 0; c < (BN + 127) / 128; ++c)
+                                ptx::tma_load_3d(sq + c * 16384, &tmQ, fb, T.j0 + c * 128, k0, eq);
+                        } else {
+                            ptx::tma_load_3d(sq, &tmQ, fb, k0, T.j0, eq);
+                        }
+                        rg.next(Cf::STAGES);
+                    }
+                }
+                // Until the MMAs have released every slot no read of this shared
+                // memory and no arrival on its barriers is outstanding.
+                const Ring last = rg;
+                for (int i = 0; ok && i < Cf::STAGES; ++i) {
+                    if (!wait_bar(empty(rg.i), rg.phase ^ 1u, abort_flag, p.timeout_ns)) {
+                        record_failure(kRoleDrain, -1, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    rg.next(Cf::STAGES);
+                }
+                // Given up: the copies already issued still land in this shared memory.
+                for (int i = 0; !ok && i < Cf::STAGES; ++i) {
+                    const uint32_t parity = i < last.i ? last.phase : last.phase ^ 1u;
+                    if (last.laps || i < last.i) wait_landed(full(i), parity, p.timeout_ns);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // -------------------------------------------------------- MMA issuer
+            if (lane == 0) {
+                Ring rg, buf;
+                bool ok = true;
+                uint32_t last_bar = 0, last_parity = 0;      // of the MMAs issued last
+                for (int t = unit; ok && t < num_tiles; t += units) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!wait_bar(acce(buf.i), buf.phase ^ 1u, abort_flag, p.timeout_ns) ||
+                            !wait_bar(full(rg.i), rg.phase, abort_flag, p.timeout_ns)) {
+                            record_failure(kRoleMma, t, abort_flag);
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t sp = ptx::smem_addr(ring + rg.i * Cf::STAGE), sq = sp + Cf::P_BYTES;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            // K-major: K advances 32 bytes inside a 128-byte row, 8-row
+                            // groups 1024 bytes apart.  MN-major: 32 rows of K further,
+                            // 128-byte chunks 16 KB apart, 8-row groups 1024.
+                            const uint64_t pd = p.p_mn ? ptx::sdesc_sw128(sp + 4096u * kk, 16384u, 1024u)
+                                                       : ptx::sdesc_sw128(sp + 32u * kk, 16u, 1024u);
+                            const uint64_t qd = p.q_mn ? ptx::sdesc_sw128(sq + 4096u * kk, 16384u, 1024u)
+                                                       : ptx::sdesc_sw128(sq + 32u * kk, 16u, 1024u);
+                            ptx::mma<1, ptx::kKindF8>(tmem + (uint32_t)(buf.i * BN), pd, qd, p.idesc, kk != 0 ? 1u : 0u);
+                        }
+                        ptx::mma_commit(empty(rg.i));
+                        ptx::mma_commit(accf(buf.i));
+                        last_bar = accf(buf.i);
+                        last_parity = buf.phase;
+                        rg.next(Cf::STAGES);
+                        buf.next(Cf::NBUF);
+                    }
+                }
+                if (!ok && last_bar) wait_landed(last_bar, last_parity, p.timeout_ns);
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ scales
+            const bool lanes_side = warp == 2;
+            Ring sl;
+            bool ok = true;
+            for (int t = unit; ok && t < num_tiles; t += units) {
+                const Tile T = tile_at<BN>(p, first_tile, first_row, t);
+                if (lanes_side)
+                    ok = bring_scales<4, kLanes, 1>(p.sp, T.i0, T.i1, p.tokens_on_i ? 0 : T.e, kb0, kb1, t, sl, scales,
+                                                    Cf::SLOT_BYTES, scf0, sce0, abort_flag, p.timeout_ns);
+                else
+                    ok = bring_scales<QVEC ? (BN + 31) / 32 : 1, QVEC ? BN : (BN + 127) / 128, QVEC ? 1 : 128>(
+                        p.sq, T.j0, T.j1, p.tokens_on_i ? T.e : 0, kb0, kb1, t, sl, scales + kLanes * 4, Cf::SLOT_BYTES,
+                        scf0, sce0, abort_flag, p.timeout_ns);
+            }
+        }
+    } else {
+        if (Cf::SPLIT_REGS) ptx::regs_take<216>();
+        // ------------------------------------------------- sums and epilogue
+        const uint32_t quarter = warp & 3, half = (warp - 4) >> 2;     // lanes it may read; its columns
+        const int row = (int)(quarter * 32 + lane), col0 = (int)half * Cf::COLS;
+        const uint32_t tbase = tmem + (quarter << 21) + (uint32_t)col0;   // lane field: quarter * 32 << 16
+        Ring buf, sl;
+        bool ok = true;
+        for (int t = unit; ok && t < num_tiles; t += units) {
+            const Tile T = tile_at<BN>(p, first_tile, first_row, t);
+            float acc[Cf::COLS];
+#pragma unroll
+            for (int c = 0; c < Cf::COLS; ++c) acc[c] = 0.f;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                bool got = wait_bar(scf(sl.i), sl.phase, abort_flag, p.timeout_ns);
+                const uint32_t slot = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES);
+                got = got && wait_bar(accf(buf.i), buf.phase, abort_flag, p.timeout_ns);
+                if (!__all_sync(0xffffffffu, got)) {
+                    if (lane == 0) record_failure(kRoleEpilogue, t, abort_flag);
+                    ok = false;
+                    break;
+                }
+                float s = ptx::ld_shared_f(slot + 4u * (uint32_t)row);
+                const uint32_t columns = slot + 4u * (uint32_t)(kLanes + col0);
+                if (!QVEC) s *= ptx::ld_shared_f(slot + 4u * (uint32_t)(kLanes + (col0 >> 7)));
+                ptx::tc_fence_after();
+                const uint32_t src = tbase + (uint32_t)(buf.i * BN);
+                constexpr int kChunks = Cf::COLS / Cf::CHUNK;
+                uint32_t r[2][Cf::CHUNK];
+                ptx::tmem_load(src, r[0]);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    ptx::tmem_wait(r[c & 1]);
+                    if (c + 1 < kChunks) {
+                        ptx::tmem_load(src + (uint32_t)((c + 1) * Cf::CHUNK), r[(c + 1) & 1]);
+                    } else {
+                        // the accumulator is read: its next K-block may be summed
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(acce(buf.i));
+                    }
+                    if (QVEC) add_scaled_columns<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s, columns + 4u * (uint32_t)(c * Cf::CHUNK));
+                    else add_scaled<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s);
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sce(sl.i));
+                buf.next(Cf::NBUF);
+                sl.next(kScaleSlots);
+            }
+            if (!ok) break;
+            if (p.splits > 1) {
+                // this CTA's K range of the tile, for the cluster to read: [column][lane]
+                float *part = reinterpret_cast<float *>(ring);
+#pragma unroll
+                for (int c = 0; c < Cf::COLS; ++c) part[(col0 + c) * kLanes + row] = acc[c];
+                break;                                   // one tile a cluster
+            }
+            write_row<Cf::COLS>(p, T, row, col0, acc);
+        }
+    }
+
+    // K ranges: every CTA of the cluster sums its share of the columns over all
+    // of them, in their order, and writes it.
+    if (p.splits > 1) {
+        __syncwarp();
+        ptx::cluster_sync();
+        if (warp >= 4 && unit < num_tiles && *abort_flag == 0) {
+            const Tile T = tile_at<BN>(p, first_tile, first_row, unit);
+            const int row = (int)(((warp - 4) & 3) * 32 + lane);
+            const uint32_t part = ptx::smem_addr(ring);
+            const int share = BN / p.splits, c0 = (int)crank * share;
+            for (int c = c0 + (int)((warp - 4) >> 2); c < c0 + share; c += EW / 4) {
+                float v = 0.f;
+                for (int s = 0; s < p.splits; ++s)
+                    v += ptx::ld_cluster_f(ptx::mapa_shared(part + 4u * (uint32_t)(c * kLanes + row), (uint32_t)s));
+                write_one(p, T, row, c, v);
+            }
+        }
+        __syncwarp();
+        ptx::cluster_sync();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc<1>(tmem, Cf::TMEM_COLS);
+}
+
+
+// ------------------------------------------------------------------- host ---
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+// `count` matrices of rows x cols bytes, in boxes of box_rows x 128 bytes.
+int encode_bytes(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld, int64_t count,
+                 int64_t stride, int box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return api_error(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)(count > 1 ? stride : ld)};
+    const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return GEMM_OK;
+    char msg[96];
+    std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return api_error(GEMM_ERR_CUDA, msg);
+}
+
+struct ScaledPlan {
+    int swap, bn, qvec, splits, grid;
+};
+
+template <int BN, bool QVEC, int EW>
+int launch(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &tq, const ScaledParams &p,
+           cudaStream_t stream) {
+    using Cf = Cfg<BN, QVEC, EW>;
+    auto kern = scaled_kernel<BN, QVEC, EW>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
+    if (e != cudaSuccess) return op_launched("cudaFuncSetAttribute", e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pl.grid, 1, 1);
+    cfg.blockDim = dim3(Cf::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Cf::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (pl.splits > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)pl.splits;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (options_snapshot().pdl != 1) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return op_launched("block-scaled product launch", cudaLaunchKernelEx(&cfg, kern, tp, tq, p));
+}
+
+int launch_plan(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &tq, const ScaledParams &p,
+                cudaStream_t stream) {
+    switch (pl.bn) {
+        case 16: return launch<16, true, 4>(pl, tp, tq, p, stream);
+        case 32: return launch<32, true, 4>(pl, tp, tq, p, stream);
+        case 64: return launch<64, true, 4>(pl, tp, tq, p, stream);
+        case 128:
+            return pl.qvec ? launch<128, true, 8>(pl, tp, tq, p, stream) : launch<128, false, 8>(pl, tp, tq, p, stream);
+        default:
+            return pl.qvec ? launch<256, true, 8>(pl, tp, tq, p, stream) : launch<256, false, 8>(pl, tp, tq, p, stream);
+    }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+// One operand as the caller gave it: `rows` x `cols` bytes in memory.
+struct Operand {
+    const char *name;
+    const void *p;
+    int64_t rows, cols, ld;
+    bool pack;               // TMA cannot address it
+    int64_t ld_use;
+};
+
+void plan_operand(Operand *o) {
+    // (the pitch of a single row is nobody's)
+    if (o->rows <= 1) o->ld = round_up(o->cols, 16);
+    o->pack = (uintptr_t)o->p % 16 != 0 || o->ld % 16 != 0;
+    o->ld_use = o->pack ? round_up(o->cols, 16) : o->ld;
+}
+
+int check_scale(const char *name, const gemm_block_scale_t *s, bool tile_ok, int64_t extent, int64_t num_kb,
+                int64_t experts, int64_t stride_e, OpSpan *span) {
+    char msg[128];
+    const int64_t kMax = 1LL << 36;
+    if (!s || !(s->block == 1 || (tile_ok && s->block == 128)) || s->stride_k < 0 || s->stride_i < 0 ||
+        s->stride_k > kMax || s->stride_i > kMax || stride_e < 0 || stride_e > (1LL << 46)) {
+        std::snprintf(msg, sizeof msg, "%s: NULL, or block or strides out of range", name);
+        return api_error(GEMM_ERR_INVALID_ARG, msg);
+    }
+    const int64_t n = s->block == 128 ? cdiv(extent, 128) : extent;
+    *span = OpSpan{name, s->scale,
+                   num_kb > 0 && n > 0 && experts > 0
+                       ? ((uint64_t)(num_kb - 1) * s->stride_k + (uint64_t)(n - 1) * s->stride_i +
+                          (uint64_t)(experts - 1) * stride_e + 1) * 4
+                       : 0,
+                   4, false};
+    return GEMM_OK;
+}
+
+ScaleView view_of(const gemm_block_scale_t *s, int64_t stride_e) {
+    return ScaleView{s->scale, s->stride_k, s->stride_i, stride_e, s->block == 128 ? 7 : 0};
+}
+
+uint32_t idesc_of(int dtype, int bn, int p_mn, int q_mn) {
+    // D f32 (bit 4), A/B format (bits 7-9, 10-12: e4m3 0, e5m2 1), A / B MN-major
+    // (bits 15, 16), N >> 3 (bits 17-22), M >> 4 (bits 24-28)
+    const uint32_t fmt = dtype == GEMM_E5M2 ? 1u : 0u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)p_mn << 15) | ((uint32_t)q_mn << 16) |
+           ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(kLanes >> 4) << 24);
+}
+
+// Tile width, roles and K ranges of one product.
+ScaledPlan plan_product(int64_t M, int64_t N, int64_t num_kb, bool a_col, bool b_tile, int sms) {
+    ScaledPlan pl = {};
+    if (M <= 64 && !a_col) {
+        pl.swap = 1;
+        pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+        pl.qvec = 1;
+    } else {
+        const int64_t tm = cdiv(M, kLanes);
+        pl.bn = tm * cdiv(N, 256) >= sms ? 256 : 128;
+        pl.qvec = !b_tile;
+    }
+    const int64_t tiles = pl.swap ? cdiv(N, kLanes) * cdiv(M, pl.bn) : cdiv(M, kLanes) * cdiv(N, pl.bn);
+    pl.splits = 1;
+    while (pl.splits < 8 && tiles * pl.splits * 2 <= sms && num_kb >= 4 * pl.splits * 2) pl.splits *= 2;
+    pl.grid = (int)(pl.splits > 1 ? tiles * pl.splits : std::min<int64_t>(tiles, sms));
+    return pl;
+}
+
+// Tile width and roles of an expert product, from the rows an expert has on average.
+ScaledPlan plan_experts(int64_t rows, int64_t N, int64_t experts, int sms) {
+    ScaledPlan pl = {};
+    const int64_t used = std::max<int64_t>(1, std::min(rows, experts)), avg = cdiv(rows, used);
+    if (avg <= 64) {
+        pl.swap = 1;
+        pl.bn = avg <= 12 ? 16 : avg <= 24 ? 32 : 64;
+        pl.qvec = 1;
+    } else {
+        pl.bn = 256;
+    }
+    const int64_t wt = pl.swap ? cdiv(N, kLanes) : cdiv(N, pl.bn), rt = pl.swap ? pl.bn : kLanes;
+    pl.splits = 1;
+    pl.grid = (int)std::min<int64_t>(sms, wt * (cdiv(rows, rt) + used));
+    return pl;
+}
+
+int check_common(int dtype, const gemm_epilogue_t *epi_in, EpiParams *epi) {
+    if (dtype != GEMM_E4M3 && dtype != GEMM_E5M2) return api_error(GEMM_ERR_INVALID_ARG, "dtype must be E4M3 or E5M2");
+    return api_epilogue(epi_in, epi);
+}
+
+// Copies the operands TMA cannot address into one workspace (returned to free).
+int pack_operands(Operand *a, Operand *b, int dev, void **ws, cudaStream_t stream) {
+    *ws = nullptr;
+    const uint64_t na = a->pack ? (uint64_t)a->rows * a->ld_use : 0, nb = b->pack ? (uint64_t)b->rows * b->ld_use : 0;
+    const uint64_t off = (na + 255) / 256 * 256;
+    if (!na && !nb) return GEMM_OK;
+    cudaError_t e = cudaMallocAsync(ws, off + nb, stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        *ws = nullptr;
+        char msg[128];
+        std::snprintf(msg, sizeof msg, "workspace of %llu bytes: %s", (unsigned long long)(off + nb),
+                      cudaGetErrorString(e));
+        return api_error(GEMM_ERR_NO_MEMORY, msg);
+    }
+    for (int i = 0; i < 2; ++i) {
+        Operand *o = i ? b : a;
+        if (!o->pack) continue;
+        uint8_t *dst = static_cast<uint8_t *>(*ws) + (i ? off : 0);
+        uint64_t lo = 0, hi = 0;
+        int rc = api_check_device_span_range(o->name, o->p, op_extent(o->rows, o->cols, o->ld, 1), dev, &lo, &hi);
+        if (rc == GEMM_OK)
+            rc = op_launched("operand pack", pack_rows_launch(o->p, o->ld, dst, o->ld_use, o->rows, o->cols, 1, lo, hi, stream));
+        if (rc) {
+            cudaFreeAsync(*ws, stream);
+            *ws = nullptr;
+            return rc;
+        }
+        o->p = dst;
+    }
+    return GEMM_OK;
+}
+
+// The two operands' tensor maps as the plan takes them, then the kernel.
+int encode_and_launch(const ScaledPlan &pl, ScaledParams &p, const Operand &a, int a_major, const Operand &b,
+                      int b_major, int64_t experts, int64_t b_expert, int dtype, cudaStream_t stream) {
+    const Operand &P = pl.swap ? b : a, &Q = pl.swap ? a : b;
+    p.p_mn = pl.swap ? !b_major : a_major;
+    p.q_mn = pl.swap ? a_major : !b_major;
+    p.idesc = idesc_of(dtype, pl.bn, p.p_mn, p.q_mn);
+    p.swapped = pl.swap;
+    p.splits = pl.splits;
+    p.kb_per_split = (int)cdiv(p.num_kb, pl.splits);
+    p.group_i = 16;
+    p.timeout_ns = (unsigned long long)options_snapshot().wait_timeout_ms * 1000000ull;
+    CUtensorMap tp, tq;
+    std::memset(&tp, 0, sizeof tp);
+    std::memset(&tq, 0, sizeof tq);
+    if (p.num_kb > 0) {
+        const int64_t pe = pl.swap ? experts : 1, qe = pl.swap ? 1 : experts;
+        int rc = encode_bytes(&tp, P.p, P.rows, P.cols, P.ld_use, pe, b_expert, kLanes);
+        if (rc == GEMM_OK)
+            rc = encode_bytes(&tq, Q.p, Q.rows, Q.cols, Q.ld_use, qe, b_expert, p.q_mn ? 128 : pl.bn);
+        if (rc) return rc;
+    }
+    return launch_plan(pl, tp, tq, p, stream);
+}
+
+}  // namespace
+
+cudaError_t scaled_read_and_clear_status(uint32_t words[4]) {
+    cudaError_t e = cudaMemcpyFromSymbol(words, g_scaled_status, sizeof(uint32_t) * 4);
+    if (e != cudaSuccess || words[0] == 0) return e;
+    static const uint32_t zero[4] = {0, 0, 0, 0};
+    return cudaMemcpyToSymbol(g_scaled_status, zero, sizeof zero);
+}
+
+}  // namespace tcgemm
+
+using namespace tcgemm;
+
+extern "C" {
+
+int gemm_run_scaled(int64_t M, int64_t N, int64_t K, int dtype, const void *A, int64_t lda, int a_major,
+                    const gemm_block_scale_t *a_scale, const void *B, int64_t ldb, int b_major,
+                    const gemm_block_scale_t *b_scale, void *C, int64_t ldc, const gemm_epilogue_t *epi_in,
+                    struct CUstream_st *stream_) {
+    api_clear_error();
+    EpiParams epi;
+    int rc = check_common(dtype, epi_in, &epi);
+    if (rc) return rc;
+    const int64_t kMax = 0x7fffffffLL - 512, kLdMax = 1LL << 36;
+    if (M < 0 || N < 0 || K < 0 || M > kMax || N > kMax || K > kMax)
+        return api_error(GEMM_ERR_INVALID_ARG, "size negative or out of range");
+    if ((a_major != 0 && a_major != 1) || (b_major != 0 && b_major != 1))
+        return api_error(GEMM_ERR_INVALID_ARG, "a_major and b_major are 0 or 1");
+    Operand a = {"A", A, a_major ? K : M, a_major ? M : K, lda, false, 0};
+    Operand b = {"B", B, b_major ? N : K, b_major ? K : N, ldb, false, 0};
+    if (lda < std::max<int64_t>(a.cols, 1) || ldb < std::max<int64_t>(b.cols, 1) || ldc < std::max<int64_t>(N, 1) ||
+        lda > kLdMax || ldb > kLdMax || ldc > kLdMax)
+        return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
+    const int64_t num_kb = cdiv(K, kBlockK);
+    const int ob = epi.active ? op_type_bytes(epi.out) : 4;
+    OpSpan spans[6] = {{"A", A, op_extent(a.rows, a.cols, lda, 1), 1, false},
+                       {"B", B, op_extent(b.rows, b.cols, ldb, 1), 1, false},
+                       {"C", C, op_extent(M, N, ldc, ob), ob, true},
+                       {"bias", epi.active ? epi.bias : nullptr, epi.active && epi.bias ? (uint64_t)N * 4 : 0, 4, false}};
+    if ((rc = check_scale("a_scale", a_scale, true, M, num_kb, 1, 0, &spans[4]))) return rc;
+    if ((rc = check_scale("b_scale", b_scale, true, N, num_kb, 1, 0, &spans[5]))) return rc;
+    if (M == 0 || N == 0) return GEMM_OK;
+    int sms = 0;
+    if ((rc = op_check(spans, 6, &sms))) return rc;
+    plan_operand(&a);
+    plan_operand(&b);
+    const ScaledPlan pl = plan_product(M, N, num_kb, a_major != 0, b_scale->block == 128, sms);
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    ScaledParams p = {};
+    p.I = (int)(pl.swap ? N : M);
+    p.J = (int)(pl.swap ? M : N);
+    p.num_kb = (int)num_kb;
+    const int64_t ti = cdiv(p.I, kLanes), tj = cdiv(p.J, pl.bn);
+    if (ti * tj * pl.splits > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
+    p.tiles_i = (int)ti;
+    p.tiles_j = (int)tj;
+    p.sp = view_of(pl.swap ? b_scale : a_scale, 0);
+    p.sq = view_of(pl.swap ? a_scale : b_scale, 0);
+    p.C = C;
+    p.c_i = pl.swap ? 1 : ldc;
+    p.c_j = pl.swap ? ldc : 1;
+    p.wide = op_wide(C, ldc, ob);
+    p.epi = epi;
+    p.tokens_on_i = !pl.swap;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    void *ws = nullptr;
+    if (num_kb > 0 && (rc = pack_operands(&a, &b, dev, &ws, stream))) return rc;
+    rc = encode_and_launch(pl, p, a, a_major, b, b_major, 1, 0, dtype, stream);
+    if (ws) {
+        const cudaError_t e = cudaFreeAsync(ws, stream);
+        if (rc == GEMM_OK) rc = op_launched("cudaFreeAsync", e);
+    }
+    return rc;
+}
+
+int gemm_run_experts(int64_t rows, int64_t N, int64_t K, int64_t experts, int dtype, const void *A, int64_t lda,
+                     const gemm_block_scale_t *a_scale, const int32_t *offsets, const void *B, int64_t ldb,
+                     int64_t b_expert, int b_major, const gemm_block_scale_t *b_scale, int64_t b_scale_expert, void *C,
+                     int64_t ldc, const gemm_epilogue_t *epi_in, struct CUstream_st *stream_) {
+    api_clear_error();
+    EpiParams epi;
+    int rc = check_common(dtype, epi_in, &epi);
+    if (rc) return rc;
+    if (epi.active && (epi.beta != 0.f || epi.bias))
+        return api_error(GEMM_ERR_INVALID_ARG, "the expert product takes beta = 0 and no bias");
+    const int64_t kMax = 0x7fffffffLL - 512, kLdMax = 1LL << 36;
+    if (rows < 0 || N < 0 || K < 0 || rows > kMax || N > kMax || K > kMax)
+        return api_error(GEMM_ERR_INVALID_ARG, "size negative or out of range");
+    if (experts < 1 || experts > kMaxExperts) return api_error(GEMM_ERR_INVALID_ARG, "experts must be in [1, 1024]");
+    if (b_major != 0 && b_major != 1) return api_error(GEMM_ERR_INVALID_ARG, "b_major is 0 or 1");
+    Operand a = {"A", A, rows, K, lda, false, 0};
+    Operand b = {"B", B, b_major ? N : K, b_major ? K : N, ldb, false, 0};
+    if (lda < std::max<int64_t>(K, 1) || ldb < std::max<int64_t>(b.cols, 1) || ldc < std::max<int64_t>(N, 1) ||
+        lda > kLdMax || ldb > kLdMax || ldc > kLdMax)
+        return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
+    if (b_expert < 0 || b_expert > (1LL << 39)) return api_error(GEMM_ERR_INVALID_ARG, "b_expert out of range");
+    const int64_t num_kb = cdiv(K, kBlockK);
+    const int ob = epi.active ? op_type_bytes(epi.out) : 4;
+    const uint64_t one = op_extent(b.rows, b.cols, ldb, 1);
+    OpSpan spans[6] = {{"A", A, op_extent(rows, K, lda, 1), 1, false},
+                       {"B", B, one ? (uint64_t)(experts - 1) * b_expert + one : 0, 1, false},
+                       {"C", C, op_extent(rows, N, ldc, ob), ob, true},
+                       {"offsets", offsets, (uint64_t)(experts + 1) * 4, 4, false}};
+    if ((rc = check_scale("a_scale", a_scale, false, rows, num_kb, 1, 0, &spans[4]))) return rc;
+    if ((rc = check_scale("b_scale", b_scale, true, N, num_kb, experts, b_scale_expert, &spans[5]))) return rc;
+    if (rows == 0 || N == 0) return GEMM_OK;
+    plan_operand(&a);
+    if (num_kb > 0 && ((uintptr_t)B % 16 != 0 || ldb % 16 != 0 || b_expert % 16 != 0))
+        return api_error(GEMM_ERR_UNSUPPORTED, "B's base, pitch and b_expert must be multiples of 16 bytes");
+    int sms = 0;
+    if ((rc = op_check(spans, 6, &sms))) return rc;
+    b.ld_use = ldb;
+    ScaledPlan pl = plan_experts(rows, N, experts, sms);
+    if (!pl.swap) pl.qvec = b_scale->block != 128;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    ScaledParams p = {};
+    p.I = (int)(pl.swap ? N : rows);
+    p.J = (int)(pl.swap ? rows : N);
+    p.num_kb = (int)num_kb;
+    p.tiles_i = pl.swap ? (int)cdiv(N, kLanes) : 0;
+    p.tiles_j = pl.swap ? 0 : (int)cdiv(N, pl.bn);
+    if ((cdiv(rows, 16) + experts) * cdiv(N, kLanes) > kMax)
+        return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
+    p.sp = view_of(pl.swap ? b_scale : a_scale, pl.swap ? b_scale_expert : 0);
+    p.sq = view_of(pl.swap ? a_scale : b_scale, pl.swap ? 0 : b_scale_expert);
+    p.C = C;
+    p.c_i = pl.swap ? 1 : ldc;
+    p.c_j = pl.swap ? ldc : 1;
+    p.wide = op_wide(C, ldc, ob);
+    p.epi = epi;
+    p.offsets = offsets;
+    p.experts = (int)experts;
+    p.rows = (int)rows;
+    p.tokens_on_i = !pl.swap;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    void *ws = nullptr;
+    if (num_kb > 0) {
+        Operand none = {"", nullptr, 0, 0, 0, false, 0};
+        if ((rc = pack_operands(&a, &none, dev, &ws, stream))) return rc;
+    }
+    rc = encode_and_launch(pl, p, a, 0, b, b_major, experts, b_expert, dtype, stream);
+    if (ws) {
+        const cudaError_t e = cudaFreeAsync(ws, stream);
+        if (rc == GEMM_OK) rc = op_launched("cudaFreeAsync", e);
+    }
+    return rc;
+}
+
+}  // extern "C"
