@@ -4,19 +4,23 @@
 //   dY[slot]     = w[t][j] * g[t]
 //   dw[t][j]     = <g[t], Y[slot]>
 //
-// Both are one pass over the rows and bound by HBM.  A block takes one token:
-// its threads walk the hidden dimension eight elements (16 or 32 bytes) at a
-// time, all top_k rows' loads of a step in flight together.  In the backward
-// pass g[t] is read once and each row's product with it is kept per thread,
-// then summed over the block in a fixed order, so results do not depend on
-// timing.
+// Both are one pass over the rows and bound by HBM.  A block takes a token (or a
+// segment of its hidden dimension): its threads hold eight elements (16 or 32
+// bytes) each of all its rows, so that up to eight loads a thread are in flight,
+// and as many blocks as fit an SM stride over the tokens.  In the backward pass
+// g[t] is read once; each row's product with it is summed over the block in a
+// fixed order, so results do not depend on timing.
 #include "ops.h"
 
 namespace tcgemm {
 namespace {
 
-constexpr int kMaxThreads = 256;
-constexpr int kChunk = 8;     // rows of a token taken together
+constexpr int kThreads = 512;  // at most
+
+// Rows of a token taken together (their loads in flight at once), and the blocks
+// of kThreads an SM is to hold: what fits the registers.
+template <typename T> constexpr int chunk_of() { return sizeof(T) == 2 ? 8 : 4; }
+template <typename T, bool WIDE> constexpr int blocks_of() { return sizeof(T) == 2 && WIDE ? 2 : 1; }
 
 struct CombineParams {
     const void *Y, *grad;
@@ -26,107 +30,160 @@ struct CombineParams {
     void *out;                // out (forward) or dY (backward)
     float *dweights;
     int top_k;
-    int wide;                 // every row of every array starts on 16 bytes
+    int64_t tokens;
+    int segments;             // of the hidden dimension, one per block and step
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kMaxThreads) combine_kernel(const CombineParams p) {
-    pdl_enter();
-    const int64_t t = blockIdx.x;
-    const int64_t h = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 8;
-    if (h >= p.hidden) return;
-    const int have = (int)(p.hidden - h < 8 ? p.hidden - h : 8);
-    const T *Y = static_cast<const T *>(p.Y);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < p.top_k; j0 += kChunk) {
-        OpVec8<T> y[kChunk];
-        float w[kChunk];
-        bool real[kChunk];
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-            const bool in = j0 + j < p.top_k;
-            const int64_t s = in ? p.slots[t * p.top_k + j0 + j] : -1;
-            real[j] = s >= 0 && s < p.rows;
-            w[j] = !real[j] ? 0.f : p.weights ? p.weights[t * p.top_k + j0 + j] : 1.f;
-            if (real[j]) y[j] = op_load8<T>(Y + s * p.ldy + h, have, p.wide);
-        }
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j)
-            if (real[j]) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[j], OpType<T>::up(y[j].v[k]), acc[k]);
-            }
+// Lane j's slot (-1 if it is none of the rows) and weight of a token's pair j0 + j.
+__device__ __forceinline__ void pair_of(const CombineParams &p, int64_t t, int j, int64_t tokens, int32_t &slot,
+                                        float &w) {
+    slot = -1;
+    w = 0.f;
+    if (j < p.top_k && t < tokens) {
+        const int32_t s = p.slots[t * p.top_k + j];
+        slot = s < p.rows ? s : -1;
+        w = p.weights ? p.weights[t * p.top_k + j] : 1.f;
     }
-    OpVec8<T> o;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o.v[k] = OpType<T>::down(acc[k]);
-    op_store8<T>(static_cast<T *>(p.out) + t * p.ldo + h, o, have, p.wide);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kMaxThreads) combine_backward_kernel(const CombineParams p) {
+// Units are (token, segment of the hidden dimension); a block strides over them
+// and has the next unit's slots and weights on their way while it sums this one.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_kernel(const CombineParams p) {
+    constexpr int kChunk = chunk_of<T>();
     pdl_enter();
-    __shared__ float s_part[kMaxThreads / 32][kChunk];
-    const int64_t t = blockIdx.x;
-    const T *Y = static_cast<const T *>(p.Y), *G = static_cast<const T *>(p.grad) + t * p.ldg;
-    T *D = static_cast<T *>(p.out);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    for (int j0 = 0; j0 < p.top_k; j0 += kChunk) {
-        float w[kChunk], dot[kChunk];
-        int64_t s[kChunk];
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-            const bool in = j0 + j < p.top_k;
-            const int64_t at = in ? p.slots[t * p.top_k + j0 + j] : -1;
-            s[j] = at >= 0 && at < p.rows ? at : -1;
-            w[j] = s[j] >= 0 ? p.weights[t * p.top_k + j0 + j] : 0.f;
-            dot[j] = 0.f;
-        }
-        for (int64_t h = (int64_t)threadIdx.x * 8; h < p.hidden; h += (int64_t)blockDim.x * 8) {
-            const int have = (int)(p.hidden - h < 8 ? p.hidden - h : 8);
-            const OpVec8<T> g = op_load8<T>(G + h, have, p.wide);
+    const int lane = threadIdx.x & 31, j_of = lane & (kChunk - 1);
+    const T *Y = static_cast<const T *>(p.Y);
+    const int64_t units = p.tokens * p.segments;
+    int32_t slot;
+    float weight;
+    pair_of(p, blockIdx.x / p.segments, j_of, p.tokens, slot, weight);
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t t = u / p.segments;
+        const int64_t h = ((u - t * p.segments) * blockDim.x + threadIdx.x) * 8;
+        const int have = h < p.hidden ? (int)(p.hidden - h < 8 ? p.hidden - h : 8) : 0;
+        int32_t next_slot;
+        float next_weight;
+        pair_of(p, (u + gridDim.x) / p.segments, j_of, p.tokens, next_slot, next_weight);
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int j0 = 0; j0 < p.top_k; j0 += kChunk) {
+            if (j0) pair_of(p, t, j0 + j_of, p.tokens, slot, weight);
             OpVec8<T> y[kChunk];
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j)
-                if (s[j] >= 0) y[j] = op_load8<T>(Y + s[j] * p.ldy + h, have, p.wide);
+            for (int j = 0; j < kChunk; ++j) {
+                const int32_t s = __shfl_sync(0xffffffffu, slot, j);
+                y[j] = op_load8<WIDE, T>(Y + (int64_t)(s < 0 ? 0 : s) * p.ldy + h, s < 0 ? 0 : have);
+            }
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j)
-                if (s[j] >= 0) {
+            for (int j = 0; j < kChunk; ++j) {
+                // (a pair without a row has loaded zeros, and its weight counts for nothing)
+                const float w = __shfl_sync(0xffffffffu, slot, j) < 0 ? 0.f : __shfl_sync(0xffffffffu, weight, j);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, OpType<T>::up(y[j].v[k]), acc[k]);
+            }
+        }
+        OpVec8<T> o;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o.v[k] = OpType<T>::down(acc[k]);
+        op_store8<WIDE, T>(static_cast<T *>(p.out) + t * p.ldo + h, o, have);
+        slot = next_slot;
+        weight = next_weight;
+    }
+}
+
+// Sums eight values over a warp; lane 4 * j of the warp gets value j's.  Each
+// step halves the values a lane carries: nine shuffles instead of forty.
+__device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+    }
+    const bool up = lane & 4;
+    float c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+    c += __shfl_xor_sync(0xffffffffu, c, 2);
+    c += __shfl_xor_sync(0xffffffffu, c, 1);
+    return c;
+}
+
+// A block takes a token at a time, striding over them.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_backward_kernel(const CombineParams p) {
+    constexpr int kChunk = chunk_of<T>();
+    pdl_enter();
+    __shared__ float s_part[2][kThreads / 32][8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, j_of = lane & (kChunk - 1);
+    const T *Y = static_cast<const T *>(p.Y);
+    T *D = static_cast<T *>(p.out);
+    int32_t slot;
+    float weight;
+    int turn = 0;
+    pair_of(p, blockIdx.x, j_of, p.tokens, slot, weight);
+    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+        const T *G = static_cast<const T *>(p.grad) + t * p.ldg;
+        int32_t next_slot;
+        float next_weight;
+        pair_of(p, t + gridDim.x, j_of, p.tokens, next_slot, next_weight);
+        for (int j0 = 0; j0 < p.top_k; j0 += kChunk) {
+            if (j0) pair_of(p, t, j0 + j_of, p.tokens, slot, weight);
+            float dot[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot[j] = 0.f;
+            for (int64_t h = (int64_t)threadIdx.x * 8; h - threadIdx.x * 8 < p.hidden; h += (int64_t)blockDim.x * 8) {
+                const int have = h < p.hidden ? (int)(p.hidden - h < 8 ? p.hidden - h : 8) : 0;
+                const OpVec8<T> g = op_load8<WIDE, T>(G + h, have);
+                OpVec8<T> y[kChunk];
+#pragma unroll
+                for (int j = 0; j < kChunk; ++j) {
+                    const int32_t s = __shfl_sync(0xffffffffu, slot, j);
+                    y[j] = op_load8<WIDE, T>(Y + (int64_t)(s < 0 ? 0 : s) * p.ldy + h, s < 0 ? 0 : have);
+                }
+#pragma unroll
+                for (int j = 0; j < kChunk; ++j) {
+                    const int32_t s = __shfl_sync(0xffffffffu, slot, j);
+                    const float w = __shfl_sync(0xffffffffu, weight, j);
+                    if (s < 0) continue;
                     OpVec8<T> d;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const float gk = OpType<T>::up(g.v[k]);
-                        d.v[k] = OpType<T>::down(w[j] * gk);
+                        d.v[k] = OpType<T>::down(w * gk);
                         dot[j] = fmaf(gk, OpType<T>::up(y[j].v[k]), dot[j]);
                     }
-                    op_store8<T>(D + s[j] * p.ldo + h, d, have, p.wide);
+                    op_store8<WIDE, T>(D + (int64_t)s * p.ldo + h, d, have);
                 }
+            }
+            const float sum = warp_sum8(dot, lane);
+            if ((lane & 3) == 0) s_part[turn][warp][lane >> 2] = sum;
+            __syncthreads();
+            if (threadIdx.x < kChunk && j0 + (int)threadIdx.x < p.top_k) {
+                float total = 0.f;
+                for (int i = 0; i < warps; ++i) total += s_part[turn][i][threadIdx.x];
+                p.dweights[t * p.top_k + j0 + threadIdx.x] = total;
+            }
+            turn ^= 1;      // (the other half is read before the next barrier but one)
         }
+        // rows past the experts' last are no token's: their gradient is zero
+        for (int j = 0; p.order && j < p.top_k; j += 32) {
+            const int64_t mine = t * p.top_k + j + lane;
+            uint32_t idle = __ballot_sync(0xffffffffu, j + lane < p.top_k && mine < p.rows && p.order[mine] < 0);
+            for (; idle; idle &= idle - 1) {
+                T *row = D + (t * p.top_k + j + __ffs(idle) - 1) * p.ldo;
+                OpVec8<T> z;
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-            if (lane == 0) s_part[warp][j] = dot[j];
+                for (int k = 0; k < 8; ++k) z.v[k] = OpType<T>::down(0.f);
+                for (int64_t h = (int64_t)threadIdx.x * 8; h < p.hidden; h += (int64_t)blockDim.x * 8)
+                    op_store8<WIDE, T>(row + h, z, (int)(p.hidden - h < 8 ? p.hidden - h : 8));
+            }
         }
-        __syncthreads();
-        if (threadIdx.x < kChunk && j0 + (int)threadIdx.x < p.top_k) {
-            float sum = 0.f;
-            for (int i = 0; i < warps; ++i) sum += s_part[i][threadIdx.x];
-            p.dweights[t * p.top_k + j0 + threadIdx.x] = sum;
-        }
-        __syncthreads();
-    }
-    // rows past the experts' last: no token's, so their gradient is zero
-    if (p.order) {
-        for (int j = 0; j < p.top_k; ++j) {
-            const int64_t r = t * p.top_k + j;
-            if (r >= p.rows || p.order[r] >= 0) continue;
-            OpVec8<T> z;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) z.v[k] = OpType<T>::down(0.f);
-            for (int64_t h = (int64_t)threadIdx.x * 8; h < p.hidden; h += (int64_t)blockDim.x * 8)
-                op_store8<T>(D + r * p.ldo + h, z, (int)(p.hidden - h < 8 ? p.hidden - h : 8), p.wide);
-        }
+        slot = next_slot;
+        weight = next_weight;
     }
 }
 
@@ -143,7 +200,13 @@ int check_sizes(int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows, int
 // Threads that cover `hidden` in steps of eight, a whole number of warps.
 int threads_for(int64_t hidden) {
     const int64_t want = ((hidden + 7) / 8 + 31) / 32 * 32;
-    return (int)(want < 32 ? 32 : want < kMaxThreads ? want : kMaxThreads);
+    return (int)(want < 32 ? 32 : want < kThreads ? want : kThreads);
+}
+
+// As many blocks as stay resident at once (1024 threads an SM).
+dim3 grid_for(int64_t units, int threads, int sms) {
+    const int64_t most = (int64_t)sms * (1024 / threads);
+    return dim3((unsigned)(units < most ? units : most));
 }
 
 }  // namespace
@@ -167,7 +230,8 @@ int gemm_combine(int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows, in
                             {"slots", slots, (uint64_t)(tokens * top_k) * 4, 4, false},
                             {"weights", weights, weights ? (uint64_t)(tokens * top_k) * 4 : 0, 4, false},
                             {"out", out, op_extent(tokens, hidden, ldo, eb), eb, true}};
-    if ((rc = op_check(spans, 4, nullptr))) return rc;
+    int sms = 0;
+    if ((rc = op_check(spans, 4, &sms))) return rc;
     CombineParams p = {};
     p.Y = Y;
     p.ldy = ldy;
@@ -178,13 +242,16 @@ int gemm_combine(int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows, in
     p.hidden = hidden;
     p.rows = rows;
     p.top_k = (int)top_k;
-    p.wide = op_wide(Y, ldy, eb) && op_wide(out, ldo, eb);
+    p.tokens = tokens;
+    const bool wide = hidden % 8 == 0 && op_wide(Y, ldy, eb) && op_wide(out, ldo, eb);
     const int threads = threads_for(hidden);
-    const dim3 grid((unsigned)tokens, (unsigned)((hidden + threads * 8 - 1) / (threads * 8)), 1);
-    if (grid.y > 65535) return api_error(GEMM_ERR_INVALID_ARG, "hidden out of range");
+    p.segments = (int)((hidden + threads * 8 - 1) / (threads * 8));
+    const dim3 grid = grid_for(tokens * p.segments, threads, sms);
     const cudaError_t e = op_by_type(type, [&](auto t) {
-        return launch_pdl(combine_kernel<decltype(t)>, grid, dim3(threads), 0,
-                          reinterpret_cast<cudaStream_t>(stream_), p);
+        return op_by_flag(wide, [&](auto w) {
+            return launch_pdl(combine_kernel<decltype(t), decltype(w)::value>, grid, dim3(threads), 0,
+                              reinterpret_cast<cudaStream_t>(stream_), p);
+        });
     });
     return op_launched("combine launch", e);
 }
@@ -210,7 +277,8 @@ int gemm_combine_backward(int64_t tokens, int64_t top_k, int64_t hidden, int64_t
                             {"order", order, order ? pairs : 0, 4, false},
                             {"dY", dY, op_extent(rows, hidden, ldd, eb), eb, true},
                             {"dweights", dweights, pairs, 4, true}};
-    if ((rc = op_check(spans, 7, nullptr))) return rc;
+    int sms = 0;
+    if ((rc = op_check(spans, 7, &sms))) return rc;
     CombineParams p = {};
     p.Y = Y;
     p.ldy = ldy;
@@ -225,10 +293,14 @@ int gemm_combine_backward(int64_t tokens, int64_t top_k, int64_t hidden, int64_t
     p.hidden = hidden;
     p.rows = rows;
     p.top_k = (int)top_k;
-    p.wide = op_wide(Y, ldy, eb) && op_wide(grad, ldg, eb) && op_wide(dY, ldd, eb);
+    p.tokens = tokens;
+    const bool wide = hidden % 8 == 0 && op_wide(Y, ldy, eb) && op_wide(grad, ldg, eb) && op_wide(dY, ldd, eb);
+    const int threads = threads_for(hidden);
     const cudaError_t e = op_by_type(type, [&](auto t) {
-        return launch_pdl(combine_backward_kernel<decltype(t)>, dim3((unsigned)tokens), dim3(threads_for(hidden)), 0,
-                          reinterpret_cast<cudaStream_t>(stream_), p);
+        return op_by_flag(wide, [&](auto w) {
+            return launch_pdl(combine_backward_kernel<decltype(t), decltype(w)::value>, grid_for(tokens, threads, sms),
+                              dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream_), p);
+        });
     });
     return op_launched("combine backward launch", e);
 }

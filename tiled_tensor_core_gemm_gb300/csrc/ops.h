@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <cstdio>
+#include <type_traits>
 
 #include "gemm_ops.h"
 #include "internal.h"
@@ -67,30 +68,65 @@ template <typename T> struct alignas(16) OpVec8 {
     T v[8];
 };
 
-// Eight elements from p; those at `have` and beyond are 0.  `wide`: p is on a
-// 16-byte boundary.
-template <typename T>
-__device__ __forceinline__ OpVec8<T> op_load8(const T *p, int have, bool wide) {
+// Eight elements from p, of which the first `have` exist; the rest are 0.
+// WIDE: p is on a 16-byte boundary and have is 0 or 8.  Otherwise the aligned
+// 16-byte blocks that hold at least one of the elements are read (an allocation
+// never ends inside one, so nothing outside the row's own blocks is touched)
+// and shifted into place: as many bytes a load as the aligned case.
+template <bool WIDE, typename T>
+__device__ __forceinline__ OpVec8<T> op_load8(const T *p, int have) {
+    constexpr int W = (int)sizeof(T) * 2;            // 32-bit words of the eight
     OpVec8<T> r;
-    if (wide && have >= 8) {
-        const uint4 *s = reinterpret_cast<const uint4 *>(p);
-        uint4 *d = reinterpret_cast<uint4 *>(r.v);
+    uint32_t *d = reinterpret_cast<uint32_t *>(r.v);
+    if (WIDE) {
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) * 8 / 16); ++i) d[i] = s[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r.v[i] = i < have ? p[i] : OpType<T>::down(0.f);
+        for (int i = 0; i < W; i += 4) {
+            const uint4 w = have > 0 ? __ldg(reinterpret_cast<const uint4 *>(p) + i / 4) : make_uint4(0, 0, 0, 0);
+            d[i] = w.x;
+            d[i + 1] = w.y;
+            d[i + 2] = w.z;
+            d[i + 3] = w.w;
+        }
+        return r;
     }
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint32_t off = (uint32_t)(at & 15u);
+    const uint4 *blocks = reinterpret_cast<const uint4 *>(at - off);
+    const uint32_t end = have > 0 ? off + (uint32_t)have * (uint32_t)sizeof(T) : 0u;   // bytes from the first block
+    uint32_t w[W + 4];
+#pragma unroll
+    for (int i = 0; i < W + 4; i += 4) {
+        const uint4 v = (uint32_t)i * 4u < end ? __ldg(blocks + i / 4) : make_uint4(0, 0, 0, 0);
+        w[i] = v.x;
+        w[i + 1] = v.y;
+        w[i + 2] = v.z;
+        w[i + 3] = v.w;
+    }
+    if (off & 8u) {
+#pragma unroll
+        for (int i = 0; i < W + 2; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4u) {
+#pragma unroll
+        for (int i = 0; i < W + 1; ++i) w[i] = w[i + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) d[i] = sizeof(T) == 2 ? __funnelshift_r(w[i], w[i + 1], 8u * (off & 3u)) : w[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i >= have) r.v[i] = OpType<T>::down(0.f);
     return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void op_store8(T *p, const OpVec8<T> &r, int have, bool wide) {
-    if (wide && have >= 8) {
-        uint4 *d = reinterpret_cast<uint4 *>(p);
-        const uint4 *s = reinterpret_cast<const uint4 *>(r.v);
+// Stores the first `have` of eight elements (WIDE as above).
+template <bool WIDE, typename T>
+__device__ __forceinline__ void op_store8(T *p, const OpVec8<T> &r, int have) {
+    if (WIDE) {
+        if (have > 0) {
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) * 8 / 16); ++i) d[i] = s[i];
+            for (int i = 0; i < (int)(sizeof(T) * 8 / 16); ++i)
+                reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(r.v)[i];
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -98,6 +134,11 @@ __device__ __forceinline__ void op_store8(T *p, const OpVec8<T> &r, int have, bo
     }
 }
 #endif
+
+// Calls f with b as a compile-time constant.
+template <typename F> auto op_by_flag(bool b, F &&f) {
+    return b ? f(std::true_type()) : f(std::false_type());
+}
 
 // Rows of a pitched array all start on 16 bytes.
 inline bool op_wide(const void *p, int64_t ld, int elem) {

@@ -36,7 +36,7 @@ struct QuantParams {
     int tiles_c;
     float top;
     int e5m2;
-    int x_wide, q_wide;       // rows of X start on 16 bytes, rows of Q on 8
+    int q_wide;               // rows of Q start on 8 bytes
 };
 
 __device__ __forceinline__ uint2 to_fp8x8(const float (&f)[8], int e5m2) {
@@ -66,8 +66,16 @@ __device__ __forceinline__ void put8(uint8_t *p, uint2 q, int have, bool wide) {
         if (i < have) p[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
 }
 
-template <typename T, int BLOCK>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p) {
+template <typename T>
+__device__ __forceinline__ uint2 scaled8(const OpVec8<T> &x, float inv, int e5m2) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = OpType<T>::up(x.v[k]) * inv;
+    return to_fp8x8(f, e5m2);
+}
+
+template <typename T, int BLOCK, bool WIDE, bool SCATTER = false>
+__global__ void __launch_bounds__(kQThreads, SCATTER || sizeof(T) == 4 ? 2 : 3) quantize_kernel(const QuantParams p) {
     pdl_enter();
     __shared__ float s_max[16][kTile];   // [row group][column]; tiles use one value a warp
     __shared__ float s_scale[kTile];
@@ -85,9 +93,17 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int64_t r = r0 + ty + 16 * i;
-        x[i] = op_load8<T>(X + r * p.ldx + c, r < p.rows ? have : 0, p.x_wide);
+        x[i] = op_load8<WIDE, T>(X + r * p.ldx + c, r < p.rows ? have : 0);
     }
 
+    // The rows a row goes to: copy j's at lane j of its half-warp.
+    const bool few = p.copies <= 16;
+    int32_t slot[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = r0 + ty + 16 * i;
+        slot[i] = SCATTER && few && tx < p.copies && r < p.rows ? p.slots[r * p.copies + tx] : -1;
+    }
     float scale[kRows];      // of this thread's rows (row blocks)
     float inv8[8];           // of its columns (column blocks)
     float inv = 0.f;         // of the tile
@@ -103,17 +119,14 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p
             if (tx == 0) s_scale[ty + 16 * i] = scale[i];
         }
         __syncthreads();
-        if (threadIdx.x < kTile) {
-            const int64_t r = r0 + threadIdx.x;
-            if (r < p.rows) {
-                if (!p.slots) {
-                    S[r * p.s_row + cb * p.s_col] = s_scale[threadIdx.x];
-                } else {
-                    for (int j = 0; j < p.copies; ++j) {
-                        const int64_t to = p.slots[r * p.copies + j];
-                        if (to >= 0 && to < p.out_rows) S[to * p.s_row + cb * p.s_col] = s_scale[threadIdx.x];
-                    }
-                }
+        if (!SCATTER) {
+            if (threadIdx.x < kTile && r0 + threadIdx.x < p.rows)
+                S[(r0 + threadIdx.x) * p.s_row + cb * p.s_col] = s_scale[threadIdx.x];
+        } else {
+            const int64_t rows = p.rows - r0 < kTile ? p.rows - r0 : kTile;
+            for (int i = threadIdx.x; i < rows * p.copies; i += kQThreads) {
+                const int64_t to = p.slots[r0 * p.copies + i];
+                if (to >= 0 && to < p.out_rows) S[to * p.s_row + cb * p.s_col] = s_scale[i / p.copies];
             }
         }
     } else {
@@ -157,23 +170,37 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p
         }
     }
 
+    // The rows stay packed: without this the compiler keeps their 64 widened
+    // values from the search above, and an SM holds a block less.
+    if (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) asm volatile("" : "+r"(reinterpret_cast<uint32_t *>(x[i].v)[k]));
+    }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int64_t r = r0 + ty + 16 * i;
-        if (r >= p.rows || have == 0) continue;
-        const float row_inv = BLOCK == GEMM_BLOCK_ROW ? 1.f / scale[i] : inv;
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            f[k] = OpType<T>::up(x[i].v[k]) * (BLOCK == GEMM_BLOCK_COL ? inv8[k] : row_inv);
-        const uint2 q = to_fp8x8(f, p.e5m2);
-        if (BLOCK != GEMM_BLOCK_ROW || !p.slots) {
-            put8(Q + r * p.ldq + c, q, have, p.q_wide);
-        } else {
+        if (SCATTER) {
+            const bool in = r < p.rows && have > 0;
+            const uint2 v = scaled8(x[i], 1.f / scale[i], p.e5m2);
+#pragma unroll 2
             for (int j = 0; j < p.copies; ++j) {
-                const int64_t to = p.slots[r * p.copies + j];
-                if (to >= 0 && to < p.out_rows) put8(Q + to * p.ldq + c, q, have, p.q_wide);
+                const int64_t to = few ? __shfl_sync(0xffffffffu, slot[i], (threadIdx.x & 16) | (j & 15))
+                                       : (in ? p.slots[r * p.copies + j] : -1);
+                if (in && to >= 0 && to < p.out_rows) put8(Q + to * p.ldq + c, v, have, p.q_wide);
             }
+            continue;
+        }
+        if (r >= p.rows || have == 0) continue;
+        if (BLOCK == GEMM_BLOCK_COL) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = OpType<T>::up(x[i].v[k]) * inv8[k];
+            put8(Q + r * p.ldq + c, to_fp8x8(f, p.e5m2), have, p.q_wide);
+        } else {
+            put8(Q + r * p.ldq + c, scaled8(x[i], BLOCK == GEMM_BLOCK_ROW ? 1.f / scale[i] : inv, p.e5m2), have,
+                 p.q_wide);
         }
     }
 }
@@ -245,19 +272,24 @@ extern "C" int gemm_quantize_block(int64_t batch, int64_t rows, int64_t cols, in
     p.tiles_c = (int)((cols + kTile - 1) / kTile);
     p.top = to == GEMM_E4M3 ? 448.f : 57344.f;
     p.e5m2 = to == GEMM_E5M2;
-    p.x_wide = op_wide(X, ldx, eb) && (batch == 1 || ((uint64_t)x_stride * eb) % 16 == 0);
+    const bool wide = cols % 8 == 0 && op_wide(X, ldx, eb) && (batch == 1 || ((uint64_t)x_stride * eb) % 16 == 0);
     p.q_wide = (uintptr_t)Q % 8 == 0 && ldq % 8 == 0 && (batch == 1 || q_stride % 8 == 0);
     const int64_t tiles = (rows + kTile - 1) / kTile * p.tiles_c;
     if (tiles > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many blocks");
     const dim3 grid((unsigned)tiles, (unsigned)batch, 1);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const cudaError_t e = op_by_type(type, [&](auto t) {
-        using T = decltype(t);
-        if (block == GEMM_BLOCK_ROW)
-            return launch_pdl(quantize_kernel<T, GEMM_BLOCK_ROW>, grid, dim3(kQThreads), 0, stream, p);
-        if (block == GEMM_BLOCK_COL)
-            return launch_pdl(quantize_kernel<T, GEMM_BLOCK_COL>, grid, dim3(kQThreads), 0, stream, p);
-        return launch_pdl(quantize_kernel<T, GEMM_BLOCK_TILE>, grid, dim3(kQThreads), 0, stream, p);
+        return op_by_flag(wide, [&](auto w) {
+            using T = decltype(t);
+            constexpr bool W = decltype(w)::value;
+            if (slots)
+                return launch_pdl(quantize_kernel<T, GEMM_BLOCK_ROW, W, true>, grid, dim3(kQThreads), 0, stream, p);
+            if (block == GEMM_BLOCK_ROW)
+                return launch_pdl(quantize_kernel<T, GEMM_BLOCK_ROW, W>, grid, dim3(kQThreads), 0, stream, p);
+            if (block == GEMM_BLOCK_COL)
+                return launch_pdl(quantize_kernel<T, GEMM_BLOCK_COL, W>, grid, dim3(kQThreads), 0, stream, p);
+            return launch_pdl(quantize_kernel<T, GEMM_BLOCK_TILE, W>, grid, dim3(kQThreads), 0, stream, p);
+        });
     });
     return op_launched("quantize launch", e);
 }
