@@ -13,7 +13,7 @@
 // The scales change every 128 values of K, so an MMA may sum over one K-block
 // only: four MMAs of K = 32 write a fresh accumulator, and epilogue warps add
 // it, scaled, to sums kept in registers.  NBUF accumulators rotate, so the MMAs
-// of the next blocks run meanwhile.  Per K-block of a 128 x 256 tile the MMAs
+// of the next blocks run meanwhile.  Per K-block of 128 x 256 the MMAs
 // take at least 512 cycles of an SM, reading the accumulator 256 and the
 // multiply-adds (paired, one scale for 128 columns) 128 issue slots a
 // sub-partition; with a scale per column the multiply by it doubles that.
@@ -46,7 +46,6 @@ constexpr int kLanes = 128;
 constexpr int kBlockK = 128;
 constexpr int kSmemMax = 232448;
 constexpr int kCtrlBytes = 1024;       // barriers and flags
-constexpr int kScaleSlots = 8;
 constexpr int kMaxExperts = 1024;
 
 enum Role : uint32_t { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleDrain = 4, kRoleScales = 5 };
@@ -68,9 +67,10 @@ struct ScaledParams {
     uint32_t idesc;
     ScaleView sp, sq;
     void *C;
-    int64_t c_i, c_j;          // element strides of D in C
+    int64_t ldc;
     int swapped;               // P is B^T: C's columns are D's rows
-    int wide;                  // 16-byte stores along C's rows are aligned
+    int wide;                  // C's rows start on 16 bytes
+    int tma_store;             // and end on them: whole boxes leave by TMA
     EpiParams epi;
     const int32_t *offsets;    // experts: rows of each
     int experts, rows;         // 0: one product
@@ -78,27 +78,31 @@ struct ScaledParams {
     unsigned long long timeout_ns;
 };
 
-template <int BN, bool QVEC, int EW>
+template <int BN, bool QVEC, int EW, int CG>
 struct Cfg {
+    static constexpr int ROWS = kLanes * CG;          // D's rows of a tile (a CTA's share is 128)
     static constexpr int COLS = BN / (EW / 4);        // columns of a thread
     static constexpr int CHUNK = COLS < 32 ? COLS : 32;
     static constexpr int THREADS = 128 + EW * 32;
     static constexpr bool SPLIT_REGS = COLS > 64;
     static constexpr int P_BYTES = kLanes * 128;
-    static constexpr int Q_BYTES = BN * 128;
+    static constexpr int Q_BYTES = BN / CG * 128;     // each CTA of a pair loads half of Q's rows
     static constexpr int STAGE = P_BYTES + Q_BYTES;
     static constexpr int NBUF = BN >= 256 ? 2 : 4;
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
+    static constexpr bool SWAPPED = BN < 128;          // the tiles of few tokens
+    static constexpr int OUT_BYTES = SWAPPED ? 2048 : 4096;           // a warp's staging for C
+    static constexpr int SLOTS = BN >= 256 && QVEC ? 4 : 8;          // of the scale ring
     static constexpr int SCALES = kLanes + (QVEC ? BN : 0) + 4;      // floats of a slot: lanes, columns or one
     static constexpr int SLOT_BYTES = (SCALES * 4 + 15) / 16 * 16;
-    static constexpr int FIXED = 1024 + kCtrlBytes + kScaleSlots * SLOT_BYTES + 2 * (kMaxExperts + 1) * 4 + 32;
+    static constexpr int FIXED = 1024 + kCtrlBytes + SLOTS * SLOT_BYTES + EW * OUT_BYTES + 2 * (kMaxExperts + 1) * 4 + 32;
     static constexpr int FIT = (kSmemMax - FIXED) / STAGE;
     static constexpr int STAGES = FIT > 12 ? 12 : FIT;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
     static_assert(!SPLIT_REGS || THREADS == 384, "the register split is written for 384 threads");
     static_assert(STAGES >= 3 && SMEM <= kSmemMax, "ring");
-    static_assert((2 * STAGES + 2 * NBUF + 2 * kScaleSlots) * 8 + 16 <= kCtrlBytes, "barrier area");
-    static_assert(kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
+    static_assert((2 * STAGES + NBUF + 2 * SLOTS) * 8 + 16 <= kCtrlBytes, "barrier area");
+    static_assert(CG == 2 || kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
 };
 
 __device__ __noinline__ void record_failure(uint32_t role, int tile, volatile int *abort_flag) {
@@ -153,7 +157,7 @@ struct Tile {
 
 // Tile t of the launch.  Down `group_i` lane tiles, then across the columns:
 // tiles that run together share both operands' panels in L2.
-template <int BN>
+template <int BN, int ROWS>
 __device__ __forceinline__ Tile tile_at(const ScaledParams &p, const int32_t *first_tile, const int32_t *first_row,
                                         int t) {
     Tile T;
@@ -168,7 +172,7 @@ __device__ __forceinline__ Tile tile_at(const ScaledParams &p, const int32_t *fi
         e = lo;
         r = t - first_tile[e];
         const int rows = first_row[e + 1] - first_row[e];
-        if (p.tokens_on_i) tiles_i = (rows + kLanes - 1) / kLanes;
+        if (p.tokens_on_i) tiles_i = (rows + ROWS - 1) / ROWS;
         else tiles_j = (rows + BN - 1) / BN;
     }
     const int per = p.group_i * tiles_j, g = r / per, first = g * p.group_i;
@@ -176,7 +180,7 @@ __device__ __forceinline__ Tile tile_at(const ScaledParams &p, const int32_t *fi
     const int in = r - g * per;
     const int ti = first + in % gi, tj = in / gi;
     T.e = e;
-    T.i0 = ti * kLanes;
+    T.i0 = ti * ROWS;
     T.j0 = tj * BN;
     T.i1 = p.I;
     T.j1 = p.J;
@@ -234,7 +238,7 @@ __device__ __forceinline__ void add_scaled_columns(float *acc, const uint32_t (&
 // base, base + STEP, ...  AHEAD K-blocks are loaded together, and the next ones
 // are in flight while these are handed over: a load takes about as long as one
 // K-block's MMAs.
-template <int PER, int COUNT, int STEP>
+template <int PER, int COUNT, int STEP, int SLOTS>
 __device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int end, int e, int kb0, int kb1, int t,
                                              Ring &sl, uint8_t *slots, int slot_bytes, uint32_t scf0, uint32_t sce0,
                                              volatile int *abort_flag, unsigned long long timeout_ns) {
@@ -270,7 +274,7 @@ __device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int e
                 if (32 * c + lane < COUNT) slot[32 * c + lane] = cur[a][c];
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(scf0 + 8u * (uint32_t)sl.i);
-            sl.next(kScaleSlots);
+            sl.next(SLOTS);
         }
     }
     return true;
@@ -281,84 +285,207 @@ __device__ __forceinline__ void write_one(const ScaledParams &p, const Tile &T, 
     const int64_t i = (int64_t)T.i0 + row, j = (int64_t)T.j0 + col;
     if (i >= T.i1 || j >= T.j1) return;
     const int64_t n = p.swapped ? i : j;
-    epi_write(p.epi, p.C, i * p.c_i + j * p.c_j, v, epi_bias(p.epi, n, n + 1));
+    epi_write(p.epi, p.C, p.swapped ? j * p.ldc + i : i * p.ldc + j, v, epi_bias(p.epi, n, n + 1));
 }
 
-// A thread's columns of its row.
+// Writes four neighbouring columns of a row of C, [cr][cc .. cc + 4), where they
+// exist.
+__device__ __forceinline__ void write_four(const ScaledParams &p, int64_t cr, int64_t cc, int64_t c_end, float4 v,
+                                           const float (&bias)[4]) {
+    float y[4] = {v.x, v.y, v.z, v.w};
+    const int64_t at = cr * p.ldc + cc;
+    const bool whole = p.wide && cc + 4 <= c_end;
+    if (p.epi.active) {
+        float old[4] = {0.f, 0.f, 0.f, 0.f};
+        if (p.epi.beta != 0.f) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (cc + k < c_end) old[k] = epi_load_old(p.C, at + k, p.epi.out);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = epi_value(p.epi, y[k], old[k], bias[k]);
+    }
+    if (whole && p.epi.active && p.epi.out != GEMM_OUT_F32) {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
+            make_uint2(epi_pack2(p.epi.out, y[0], y[1]), epi_pack2(p.epi.out, y[2], y[3]));
+    } else if (whole) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (cc + k < c_end) epi_store(p.C, at + k, p.epi.active ? p.epi.out : GEMM_OUT_F32, y[k]);
+    }
+}
+
+// Swapped: a warp's 32 rows x COLS columns of D are COLS rows of 32 columns of
+// C.  They go through 2 KB of shared memory, 16 rows of C at a time, so that
+// eight lanes hold 32 neighbouring elements of a row and the epilogue's code is
+// there once (unrolled over the sums it did not fit the instruction caches).
+// The sums move down as they are written.
 template <int COLS>
-__device__ __forceinline__ void write_row(const ScaledParams &p, const Tile &T, int row, int col0,
-                                          const float (&acc)[COLS]) {
-    const int64_t i = (int64_t)T.i0 + row, j = (int64_t)T.j0 + col0;
-    if (p.swapped || !p.wide || j + COLS > T.j1) {
+__device__ __forceinline__ void write_swapped(const ScaledParams &p, const Tile &T, int row0, int col0,
+                                              float (&acc)[COLS], uint32_t buf, int lane) {
+    const int u = lane & 7;
+    const int64_t cc = (int64_t)T.i0 + row0 + 4 * u;
+    float bias[4];
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) write_one(p, T, row, col0 + c, acc[c]);
-        return;
-    }
-    if (i >= T.i1) return;
-    const int64_t at = i * p.c_i + j;
-    const bool half = p.epi.active && p.epi.out != GEMM_OUT_F32;
+    for (int k = 0; k < 4; ++k) bias[k] = cc + k < T.i1 ? epi_bias(p.epi, cc + k, cc + k + 1) : 0.f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < COLS; c0 += 16) {
+        const int64_t r0 = (int64_t)T.j0 + col0 + c0;
+        if (r0 >= T.j1) break;
+        __syncwarp();
 #pragma unroll
-    for (int c = 0; c < COLS; c += 8) {
-        float y[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            y[k] = acc[c + k];
-            if (p.epi.active)
-                y[k] = epi_value(p.epi, y[k], p.epi.beta != 0.f ? epi_load_old(p.C, at + c + k, p.epi.out) : 0.f,
-                                 epi_bias(p.epi, j + c + k, j + c + k + 1));
+        for (int c = 0; c < 16; ++c) ptx::st_shared_f(buf + 4u * (uint32_t)(c * 32 + lane), acc[c]);
+        __syncwarp();
+#pragma unroll 1
+        for (int r = lane >> 3; r < 16 && r0 + r < T.j1; r += 4) {
+            const float4 v = ptx::ld_shared_v4f(buf + 128u * (uint32_t)r + 16u * (uint32_t)u);
+            if (cc < T.i1) write_four(p, r0 + r, cc, T.i1, v, bias);
         }
-        if (half) {
-            uint4 w;
-            w.x = epi_pack2(p.epi.out, y[0], y[1]);
-            w.y = epi_pack2(p.epi.out, y[2], y[3]);
-            w.z = epi_pack2(p.epi.out, y[4], y[5]);
-            w.w = epi_pack2(p.epi.out, y[6], y[7]);
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.C) + at + c) = w;
-        } else {
-            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at + c);
-            d[0] = make_float4(y[0], y[1], y[2], y[3]);
-            d[1] = make_float4(y[4], y[5], y[6], y[7]);
-        }
+#pragma unroll
+        for (int c = 0; c + 16 < COLS; ++c) acc[c] = acc[c + 16];
     }
 }
 
-template <int BN, bool QVEC, int EW>
-__global__ void __launch_bounds__(Cfg<BN, QVEC, EW>::THREADS, 1)
-scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const ScaledParams p) {
-    using Cf = Cfg<BN, QVEC, EW>;
+// A warp's 32 rows x COLS columns of D as rows of C, one row a thread: 32
+// columns at a time through the epilogue in registers (its code is there once;
+// the sums move down), rounded, and into a box of 32 rows x 128 bytes of shared
+// memory with TMA's 128-byte swizzle.  A full box leaves by a TMA store where
+// C's layout allows it and the rows are all this tile's (an expert's last tile
+// ends inside one), else row by row with neighbouring lanes on neighbouring
+// columns.
+template <int COLS>
+__device__ __forceinline__ void write_rows(const ScaledParams &p, const CUtensorMap *tmC, const Tile &T, int row0,
+                                           int col0, float (&acc)[COLS], uint32_t buf, int lane) {
+    const bool active = p.epi.active != 0;
+    const bool half = active && p.epi.out != GEMM_OUT_F32;
+    const int64_t i0 = (int64_t)T.i0 + row0, i = i0 + lane;
+    const bool by_tma = p.tma_store && (!p.experts || i0 + 32 <= T.i1);
+#pragma unroll 1
+    for (int c0 = 0; c0 < COLS; c0 += 32) {
+        const int64_t j = (int64_t)T.j0 + col0 + c0;
+        if (i0 >= T.i1 || j >= T.j1) break;
+        if (active) {
+            if (p.epi.alpha != 1.f) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) acc[c] *= p.epi.alpha;
+            }
+            if (p.epi.beta != 0.f && i < T.i1) {
+                const int64_t at = i * p.ldc + j;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (j + c < T.j1) acc[c] = fmaf(p.epi.beta, epi_load_old(p.C, at + c, p.epi.out), acc[c]);
+            }
+            if (p.epi.bias) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) acc[c] += j + c < T.j1 ? __ldg(p.epi.bias + j + c) : 0.f;
+            }
+            if (p.epi.act == GEMM_ACT_RELU) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) acc[c] = fmaxf(acc[c], 0.f);
+            } else if (p.epi.act == GEMM_ACT_GELU) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) acc[c] = 0.5f * acc[c] * (1.f + erff(acc[c] * 0.70710678118654752f));
+            }
+        }
+        // the box's first half: the store of the one before must have read it
+        const bool first = !half || (c0 & 32) == 0;
+        if (first) {
+            if (lane == 0) ptx::bulk_wait_group_read<0>();
+            __syncwarp();
+        }
+        const uint32_t row = buf + 128u * (uint32_t)lane;
+        if (half) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t unit = (uint32_t)((u + (first ? 0 : 4)) ^ (lane & 7));
+                ptx::st_shared_v4(row + 16u * unit,
+                                  make_uint4(epi_pack2(p.epi.out, acc[8 * u], acc[8 * u + 1]),
+                                             epi_pack2(p.epi.out, acc[8 * u + 2], acc[8 * u + 3]),
+                                             epi_pack2(p.epi.out, acc[8 * u + 4], acc[8 * u + 5]),
+                                             epi_pack2(p.epi.out, acc[8 * u + 6], acc[8 * u + 7])));
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                ptx::st_shared_v4f(row + 16u * (uint32_t)(u ^ (lane & 7)),
+                                   make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]));
+        }
+        const bool last = !half || (c0 & 32) != 0 || j + 32 >= T.j1;
+        if (last) {
+            const int64_t jb = first ? j : j - 32;          // the box's first column
+            if (by_tma) {
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_2d(tmC, buf, (int)jb, (int)i0);
+                    ptx::bulk_commit_group();
+                }
+            } else {
+                __syncwarp();
+                const int rows = T.i1 - i0 < 32 ? (int)(T.i1 - i0) : 32;
+                const int cols = (int)(T.j1 - jb < (half ? 64 : 32) ? T.j1 - jb : (half ? 64 : 32));
+#pragma unroll 2
+                for (int r = 0; r < rows; ++r) {
+                    const uint32_t from = buf + 128u * (uint32_t)r;
+                    const int64_t at = (i0 + r) * p.ldc + jb + lane;
+                    const uint32_t sw = (uint32_t)(r & 7) << 4;
+                    if (half) {
+                        uint16_t *d = static_cast<uint16_t *>(p.C) + at;
+                        if (lane < cols) d[0] = ptx::ld_shared_u16(from + ((2u * (uint32_t)lane) ^ sw));
+                        if (lane + 32 < cols) d[32] = ptx::ld_shared_u16(from + ((2u * (uint32_t)lane + 64u) ^ sw));
+                    } else if (lane < cols) {
+                        static_cast<float *>(p.C)[at] = ptx::ld_shared_f(from + ((4u * (uint32_t)lane) ^ sw));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+#pragma unroll
+        for (int c = 0; c + 32 < COLS; ++c) acc[c] = acc[c + 32];
+    }
+}
+
+template <int BN, bool QVEC, int EW, int CG>
+__global__ void __launch_bounds__((Cfg<BN, QVEC, EW, CG>::THREADS), 1)
+scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+              const __grid_constant__ CUtensorMap tmC, const ScaledParams p) {
+    using Cf = Cfg<BN, QVEC, EW, CG>;
+    constexpr bool kPair = CG == 2;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + Cf::STAGES * Cf::STAGE);
+    uint8_t *out_bufs = ring + Cf::STAGES * Cf::STAGE;          // 1024-byte aligned, as the ring's slots are
+    uint64_t *bars = reinterpret_cast<uint64_t *>(out_bufs + EW * Cf::OUT_BYTES);
     uint8_t *scales = reinterpret_cast<uint8_t *>(bars) + kCtrlBytes;
-    int32_t *first_tile = reinterpret_cast<int32_t *>(scales + kScaleSlots * Cf::SLOT_BYTES);
+    int32_t *first_tile = reinterpret_cast<int32_t *>(scales + Cf::SLOTS * Cf::SLOT_BYTES);
     int32_t *first_row = first_tile + kMaxExperts + 1;
-    constexpr int kBars = 2 * Cf::STAGES + 2 * Cf::NBUF + 2 * kScaleSlots;
+    constexpr int kBars = 2 * Cf::STAGES + Cf::NBUF + 2 * Cf::SLOTS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const uint32_t bar0 = ptx::smem_addr(bars);
     auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
-    auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(Cf::STAGES + s); };
-    auto accf = [&](int b) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + b); };
-    auto acce = [&](int b) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + b); };
-    auto scf = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + 2 * Cf::NBUF + s); };
-    auto sce = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + 2 * Cf::NBUF + kScaleSlots + s); };
-    const uint32_t scales0 = ptx::smem_addr(scales), scf0 = scf(0), sce0 = sce(0);
+    auto done = [&](int s) { return bar0 + 8u * (uint32_t)(Cf::STAGES + s); };    // the MMAs of a stage have completed
+    auto acce = [&](int b) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + b); };
+    auto scf = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + s); };
+    auto sce = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + Cf::SLOTS + s); };
+    const uint32_t scales0 = ptx::smem_addr(scales), out0 = ptx::smem_addr(out_bufs), scf0 = scf(0), sce0 = sce(0);
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t crank = p.splits > 1 ? ptx::cluster_ctarank() : 0u;
+    const uint32_t crank = !kPair && p.splits > 1 ? ptx::cluster_ctarank() : 0u;   // its K range
+    const uint32_t rank = kPair ? ptx::cluster_ctarank() : 0u;                     // its half of the pair's tile
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cf::STAGES; ++s) {
             ptx::mbar_init(full(s), 1);
-            ptx::mbar_init(empty(s), 1);
+            ptx::mbar_init(done(s), 1);
         }
         for (int b = 0; b < Cf::NBUF; ++b) {
-            ptx::mbar_init(accf(b), 1);
-            ptx::mbar_init(acce(b), EW);
+            ptx::mbar_init(acce(b), EW * CG);
         }
-        for (int s = 0; s < kScaleSlots; ++s) {
+        for (int s = 0; s < Cf::SLOTS; ++s) {
             ptx::mbar_init(scf(s), 2);       // the lanes' and the columns' scale warps
             ptx::mbar_init(sce(s), EW);
         }
@@ -368,10 +495,11 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             ptx::prefetch_tensormap(&tmP);
             ptx::prefetch_tensormap(&tmQ);
         }
+        if (p.tma_store) ptx::prefetch_tensormap(&tmC);
     }
     if (warp == 1) {
-        ptx::tmem_alloc<1>(ptx::smem_addr(tmem_slot), Cf::TMEM_COLS);
-        ptx::tmem_relinquish<1>();
+        ptx::tmem_alloc<CG>(ptx::smem_addr(tmem_slot), Cf::TMEM_COLS);
+        ptx::tmem_relinquish<CG>();
     }
     // Global memory from here on: the previous kernel on the stream is done.
     ptx::pdl_wait();
@@ -394,7 +522,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             if (lane == 0) before = e0 ? row : o;
             // tiles of the expert that ends here (e - 1)
             const int n = e > 0 && e <= p.experts ? o - before : 0;
-            int32_t c = p.tokens_on_i ? (n + kLanes - 1) / kLanes * p.tiles_j : (n + BN - 1) / BN * p.tiles_i;
+            int32_t c = p.tokens_on_i ? (n + Cf::ROWS - 1) / Cf::ROWS * p.tiles_j : (n + BN - 1) / BN * p.tiles_i;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int32_t y = __shfl_up_sync(0xffffffffu, c, d);
@@ -407,11 +535,17 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
         }
     }
     ptx::tc_fence_before();
-    __syncthreads();
+    if (kPair) {
+        __syncwarp();
+        ptx::cluster_sync();      // the peer's barriers are ready before any arrival on them
+    } else {
+        __syncthreads();
+    }
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int num_tiles = p.experts ? first_tile[p.experts] : p.tiles_i * p.tiles_j;
-    const int unit = (int)blockIdx.x / p.splits, units = (int)gridDim.x / p.splits;
+    const int share = kPair ? 2 : p.splits;      // CTAs of a tile
+    const int unit = (int)blockIdx.x / share, units = (int)gridDim.x / share;
     const int kb0 = (int)crank * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
 
     // 128 columns a thread need more than the launch's 168 registers: the first
@@ -424,26 +558,27 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 Ring rg;
                 bool ok = true;
                 for (int t = unit; ok && t < num_tiles; t += units) {
-                    const Tile T = tile_at<BN>(p, first_tile, first_row, t);
+                    const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
                     const int ep = p.tokens_on_i ? 0 : T.e, eq = p.tokens_on_i ? T.e : 0;
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!wait_bar(empty(rg.i), rg.phase ^ 1u, abort_flag, p.timeout_ns)) {
+                        if (!wait_bar(done(rg.i), rg.phase ^ 1u, abort_flag, p.timeout_ns)) {
                             record_failure(kRoleProducer, t, abort_flag);
                             ok = false;
                             break;
                         }
                         const uint32_t fb = full(rg.i), sp = ptx::smem_addr(ring + rg.i * Cf::STAGE),
                                        sq = sp + Cf::P_BYTES;
-                        ptx::mbar_arrive_expect_tx(fb, (uint32_t)Cf::STAGE);
-                        const int k0 = kb * kBlockK;
-                        if (p.p_mn) ptx::tma_load_3d(sp, &tmP, fb, T.i0, k0, ep);
-                        else ptx::tma_load_3d(sp, &tmP, fb, k0, T.i0, ep);
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)(Cf::STAGE * CG));
+                        const int k0 = kb * kBlockK, i0 = T.i0 + (int)rank * kLanes, j0 = T.j0 + (int)rank * (BN / CG);
+                        const uint32_t to = kPair ? ptx::mapa_shared(fb, 0) : fb;     // a pair's bytes count in the leader
+                        if (p.p_mn) ptx::tma_load_3d<CG>(sp, &tmP, to, i0, k0, ep);
+                        else ptx::tma_load_3d<CG>(sp, &tmP, to, k0, i0, ep);
                         if (p.q_mn) {
 #pragma unroll
-                            for (int c = 0; c < (BN + 127) / 128; ++c)
-                                ptx::tma_load_3d(sq + c * 16384, &tmQ, fb, T.j0 + c * 128, k0, eq);
+                            for (int c = 0; c < (BN / CG + 127) / 128; ++c)
+                                ptx::tma_load_3d<CG>(sq + c * 16384, &tmQ, to, j0 + c * 128, k0, eq);
                         } else {
-                            ptx::tma_load_3d(sq, &tmQ, fb, k0, T.j0, eq);
+                            ptx::tma_load_3d<CG>(sq, &tmQ, to, k0, j0, eq);
                         }
                         rg.next(Cf::STAGES);
                     }
@@ -452,7 +587,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 // memory and no arrival on its barriers is outstanding.
                 const Ring last = rg;
                 for (int i = 0; ok && i < Cf::STAGES; ++i) {
-                    if (!wait_bar(empty(rg.i), rg.phase ^ 1u, abort_flag, p.timeout_ns)) {
+                    if (!wait_bar(done(rg.i), rg.phase ^ 1u, abort_flag, p.timeout_ns)) {
                         record_failure(kRoleDrain, -1, abort_flag);
                         ok = false;
                         break;
@@ -460,43 +595,52 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                     rg.next(Cf::STAGES);
                 }
                 // Given up: the copies already issued still land in this shared memory.
-                for (int i = 0; !ok && i < Cf::STAGES; ++i) {
+                for (int i = 0; !ok && rank == 0 && i < Cf::STAGES; ++i) {
                     const uint32_t parity = i < last.i ? last.phase : last.phase ^ 1u;
-                    if (last.laps || i < last.i) wait_landed(full(i), parity, p.timeout_ns);
+                    if (last.laps || i < last.i) wait_landed(full(i), parity, p.timeout_ns);   // (of a pair: in the leader)
                 }
             }
             __syncwarp();
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA issuer
-            if (lane == 0) {
+            // The whole warp runs the loop and one elected thread issues: the
+            // descriptors then stay in uniform registers (with a loop of one
+            // thread the issue of a K-block took 650 cycles, more than its MMAs).
+            // One commit a K-block serves both who waits for it: the producer,
+            // for the stage, and the epilogue warps, for the accumulator.
+            if (rank == 0) {
                 Ring rg, buf;
                 bool ok = true;
                 uint32_t last_bar = 0, last_parity = 0;      // of the MMAs issued last
                 for (int t = unit; ok && t < num_tiles; t += units) {
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!wait_bar(acce(buf.i), buf.phase ^ 1u, abort_flag, p.timeout_ns) ||
-                            !wait_bar(full(rg.i), rg.phase, abort_flag, p.timeout_ns)) {
-                            record_failure(kRoleMma, t, abort_flag);
+                        const bool got = wait_bar(full(rg.i), rg.phase, abort_flag, p.timeout_ns) &&
+                                         wait_bar(acce(buf.i), buf.phase ^ 1u, abort_flag, p.timeout_ns);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            if (lane == 0) record_failure(kRoleMma, t, abort_flag);
                             ok = false;
                             break;
                         }
                         ptx::tc_fence_after();
                         const uint32_t sp = ptx::smem_addr(ring + rg.i * Cf::STAGE), sq = sp + Cf::P_BYTES;
+                        // K-major: K advances 32 bytes inside a 128-byte row, 8-row
+                        // groups 1024 bytes apart.  MN-major: 32 rows of K further,
+                        // 128-byte chunks 16 KB apart, 8-row groups 1024.
+                        const uint64_t pd = ptx::sdesc_sw128(sp, p.p_mn ? 16384u : 16u, 1024u);
+                        const uint64_t qd = ptx::sdesc_sw128(sq, p.q_mn ? 16384u : 16u, 1024u);
+                        const uint32_t p_step = p.p_mn ? 4096u / 16u : 32u / 16u, q_step = p.q_mn ? 4096u / 16u : 32u / 16u;
+                        const uint32_t d = tmem + (uint32_t)(buf.i * BN);
+                        if (ptx::elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            // K-major: K advances 32 bytes inside a 128-byte row, 8-row
-                            // groups 1024 bytes apart.  MN-major: 32 rows of K further,
-                            // 128-byte chunks 16 KB apart, 8-row groups 1024.
-                            const uint64_t pd = p.p_mn ? ptx::sdesc_sw128(sp + 4096u * kk, 16384u, 1024u)
-                                                       : ptx::sdesc_sw128(sp + 32u * kk, 16u, 1024u);
-                            const uint64_t qd = p.q_mn ? ptx::sdesc_sw128(sq + 4096u * kk, 16384u, 1024u)
-                                                       : ptx::sdesc_sw128(sq + 32u * kk, 16u, 1024u);
-                            ptx::mma<1, ptx::kKindF8>(tmem + (uint32_t)(buf.i * BN), pd, qd, p.idesc, kk != 0 ? 1u : 0u);
+                            for (int kk = 0; kk < 4; ++kk)
+                                ptx::mma<CG, ptx::kKindF8>(d, pd + (uint64_t)(p_step * kk), qd + (uint64_t)(q_step * kk),
+                                                           p.idesc, kk != 0 ? 1u : 0u);
+                            if (kPair) ptx::mma_commit_pair(done(rg.i), 0x3);
+                            else ptx::mma_commit(done(rg.i));
                         }
-                        ptx::mma_commit(empty(rg.i));
-                        ptx::mma_commit(accf(buf.i));
-                        last_bar = accf(buf.i);
-                        last_parity = buf.phase;
+                        __syncwarp();
+                        last_bar = done(rg.i);
+                        last_parity = rg.phase;
                         rg.next(Cf::STAGES);
                         buf.next(Cf::NBUF);
                     }
@@ -510,12 +654,12 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             Ring sl;
             bool ok = true;
             for (int t = unit; ok && t < num_tiles; t += units) {
-                const Tile T = tile_at<BN>(p, first_tile, first_row, t);
+                const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
                 if (lanes_side)
-                    ok = bring_scales<4, kLanes, 1>(p.sp, T.i0, T.i1, p.tokens_on_i ? 0 : T.e, kb0, kb1, t, sl, scales,
+                    ok = bring_scales<4, kLanes, 1, Cf::SLOTS>(p.sp, T.i0 + (int)rank * kLanes, T.i1, p.tokens_on_i ? 0 : T.e, kb0, kb1, t, sl, scales,
                                                     Cf::SLOT_BYTES, scf0, sce0, abort_flag, p.timeout_ns);
                 else
-                    ok = bring_scales<QVEC ? (BN + 31) / 32 : 1, QVEC ? BN : (BN + 127) / 128, QVEC ? 1 : 128>(
+                    ok = bring_scales<QVEC ? (BN + 31) / 32 : 1, QVEC ? BN : (BN + 127) / 128, QVEC ? 1 : 128, Cf::SLOTS>(
                         p.sq, T.j0, T.j1, p.tokens_on_i ? T.e : 0, kb0, kb1, t, sl, scales + kLanes * 4, Cf::SLOT_BYTES,
                         scf0, sce0, abort_flag, p.timeout_ns);
             }
@@ -524,34 +668,49 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
         if (Cf::SPLIT_REGS) ptx::regs_take<216>();
         // ------------------------------------------------- sums and epilogue
         const uint32_t quarter = warp & 3, half = (warp - 4) >> 2;     // lanes it may read; its columns
-        const int row = (int)(quarter * 32 + lane), col0 = (int)half * Cf::COLS;
+        const int row = (int)(quarter * 32 + lane), col0 = (int)half * Cf::COLS;   // of this CTA's 128
         const uint32_t tbase = tmem + (quarter << 21) + (uint32_t)col0;   // lane field: quarter * 32 << 16
-        Ring buf, sl;
+        Ring rg, buf, sl;
         bool ok = true;
         for (int t = unit; ok && t < num_tiles; t += units) {
-            const Tile T = tile_at<BN>(p, first_tile, first_row, t);
+            const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
             float acc[Cf::COLS];
 #pragma unroll
             for (int c = 0; c < Cf::COLS; ++c) acc[c] = 0.f;
+            // A K-block's scale, and whether its MMAs have completed, are looked up
+            // while the last columns of the block before are on their way.
+            float s = 0.f;
+            bool got = true, ready = false;
+            auto next_scale = [&](const Ring &at) {
+                got = wait_bar(scf(at.i), at.phase, abort_flag, p.timeout_ns);
+                const uint32_t slot = scales0 + (uint32_t)(at.i * Cf::SLOT_BYTES);
+                s = ptx::ld_shared_f(slot + 4u * (uint32_t)row);
+                if (!QVEC) s *= ptx::ld_shared_f(slot + 4u * (uint32_t)(kLanes + (col0 >> 7)));
+            };
+            if (kb0 < kb1) next_scale(sl);
             for (int kb = kb0; kb < kb1; ++kb) {
-                bool got = wait_bar(scf(sl.i), sl.phase, abort_flag, p.timeout_ns);
-                const uint32_t slot = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES);
-                got = got && wait_bar(accf(buf.i), buf.phase, abort_flag, p.timeout_ns);
+                if (!ready) got = wait_bar(done(rg.i), rg.phase, abort_flag, p.timeout_ns) && got;
                 if (!__all_sync(0xffffffffu, got)) {
                     if (lane == 0) record_failure(kRoleEpilogue, t, abort_flag);
                     ok = false;
                     break;
                 }
-                float s = ptx::ld_shared_f(slot + 4u * (uint32_t)row);
-                const uint32_t columns = slot + 4u * (uint32_t)(kLanes + col0);
-                if (!QVEC) s *= ptx::ld_shared_f(slot + 4u * (uint32_t)(kLanes + (col0 >> 7)));
                 ptx::tc_fence_after();
-                const uint32_t src = tbase + (uint32_t)(buf.i * BN);
+                const uint32_t columns = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES) + 4u * (uint32_t)(kLanes + col0);
+                const uint32_t src = tbase + (uint32_t)(buf.i * BN), sce_now = sce(sl.i), acce_now = acce(buf.i);
                 constexpr int kChunks = Cf::COLS / Cf::CHUNK;
+                const float s_now = s;
                 uint32_t r[2][Cf::CHUNK];
                 ptx::tmem_load(src, r[0]);
+                rg.next(Cf::STAGES);
+                buf.next(Cf::NBUF);
+                sl.next(Cf::SLOTS);
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
+                    if (c + 1 == kChunks && kb + 1 < kb1) {
+                        next_scale(sl);
+                        ready = ptx::mbar_test(done(rg.i), rg.phase);
+                    }
                     ptx::tmem_wait(r[c & 1]);
                     if (c + 1 < kChunks) {
                         ptx::tmem_load(src + (uint32_t)((c + 1) * Cf::CHUNK), r[(c + 1) & 1]);
@@ -559,35 +718,45 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                         // the accumulator is read: its next K-block may be summed
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(acce(buf.i));
+                        if (lane == 0) {
+                            if (kPair) ptx::mbar_arrive_peer(ptx::mapa_shared(acce_now, 0));
+                            else ptx::mbar_arrive(acce_now);
+                        }
                     }
-                    if (QVEC) add_scaled_columns<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s, columns + 4u * (uint32_t)(c * Cf::CHUNK));
-                    else add_scaled<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s);
+                    if (QVEC)
+                        add_scaled_columns<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s_now,
+                                                      columns + 4u * (uint32_t)(c * Cf::CHUNK));
+                    else
+                        add_scaled<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s_now);
                 }
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(sce(sl.i));
-                buf.next(Cf::NBUF);
-                sl.next(kScaleSlots);
+                if (lane == 0) ptx::mbar_arrive(sce_now);
             }
             if (!ok) break;
-            if (p.splits > 1) {
+            if (!kPair && p.splits > 1) {
                 // this CTA's K range of the tile, for the cluster to read: [column][lane]
                 float *part = reinterpret_cast<float *>(ring);
 #pragma unroll
                 for (int c = 0; c < Cf::COLS; ++c) part[(col0 + c) * kLanes + row] = acc[c];
                 break;                                   // one tile a cluster
             }
-            write_row<Cf::COLS>(p, T, row, col0, acc);
+            const uint32_t out_buf = out0 + (warp - 4) * (uint32_t)Cf::OUT_BYTES;
+            if constexpr (Cf::SWAPPED)
+                write_swapped<Cf::COLS>(p, T, (int)(quarter * 32), col0, acc, out_buf, (int)lane);
+            else
+                write_rows<Cf::COLS>(p, &tmC, T, (int)(quarter * 32 + rank * kLanes), col0, acc, out_buf, (int)lane);
         }
     }
 
+    // Before the CTA's shared memory goes, its TMA stores must have read it.
+    if (warp >= 4 && lane == 0) ptx::bulk_wait_group_read<0>();
     // K ranges: every CTA of the cluster sums its share of the columns over all
     // of them, in their order, and writes it.
-    if (p.splits > 1) {
+    if (!kPair && p.splits > 1) {
         __syncwarp();
         ptx::cluster_sync();
         if (warp >= 4 && unit < num_tiles && *abort_flag == 0) {
-            const Tile T = tile_at<BN>(p, first_tile, first_row, unit);
+            const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, unit);
             const int row = (int)(((warp - 4) & 3) * 32 + lane);
             const uint32_t part = ptx::smem_addr(ring);
             const int share = BN / p.splits, c0 = (int)crank * share;
@@ -602,9 +771,14 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
         ptx::cluster_sync();
     }
     ptx::tc_fence_before();
-    __syncthreads();
+    if (kPair) {
+        __syncwarp();
+        ptx::cluster_sync();      // neither CTA of a pair leaves while the other may still signal it
+    } else {
+        __syncthreads();
+    }
     ptx::tc_fence_after();
-    if (warp == 1) ptx::tmem_dealloc<1>(tmem, Cf::TMEM_COLS);
+    if (warp == 1) ptx::tmem_dealloc<CG>(tmem, Cf::TMEM_COLS);
 }
 
 
@@ -641,15 +815,35 @@ int encode_bytes(CUtensorMap *map, const void *base, int64_t rows, int64_t cols,
     return api_error(GEMM_ERR_CUDA, msg);
 }
 
+// C in boxes of 32 rows x 128 bytes.
+int encode_rows(CUtensorMap *map, void *C, int out, int64_t rows, int64_t cols, int64_t ld) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return api_error(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const int ob = op_type_bytes(out);
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld * ob)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / ob), 32};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, out == GEMM_OUT_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : out == GEMM_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                           2, C, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return GEMM_OK;
+    char msg[96];
+    std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed for C (CUresult %d)", (int)r);
+    return api_error(GEMM_ERR_CUDA, msg);
+}
+
 struct ScaledPlan {
-    int swap, bn, qvec, splits, grid;
+    int swap, bn, cg, qvec, splits, grid;
 };
 
-template <int BN, bool QVEC, int EW>
-int launch(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &tq, const ScaledParams &p,
-           cudaStream_t stream) {
-    using Cf = Cfg<BN, QVEC, EW>;
-    auto kern = scaled_kernel<BN, QVEC, EW>;
+template <int BN, bool QVEC, int EW, int CG>
+int launch(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &tq, const CUtensorMap &tc,
+           const ScaledParams &p, cudaStream_t stream) {
+    using Cf = Cfg<BN, QVEC, EW, CG>;
+    auto kern = scaled_kernel<BN, QVEC, EW, CG>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
     if (e != cudaSuccess) return op_launched("cudaFuncSetAttribute", e);
     cudaLaunchConfig_t cfg = {};
@@ -659,9 +853,9 @@ int launch(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &tq, c
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     unsigned n = 0;
-    if (pl.splits > 1) {
+    if (CG == 2 || pl.splits > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = (unsigned)pl.splits;
+        attr[n].val.clusterDim.x = CG == 2 ? 2u : (unsigned)pl.splits;
         attr[n].val.clusterDim.y = 1;
         attr[n].val.clusterDim.z = 1;
         ++n;
@@ -673,19 +867,21 @@ int launch(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &tq, c
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return op_launched("block-scaled product launch", cudaLaunchKernelEx(&cfg, kern, tp, tq, p));
+    return op_launched("block-scaled product launch", cudaLaunchKernelEx(&cfg, kern, tp, tq, tc, p));
 }
 
-int launch_plan(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &tq, const ScaledParams &p,
-                cudaStream_t stream) {
+int launch_plan(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &tq, const CUtensorMap &tc,
+                const ScaledParams &p, cudaStream_t stream) {
     switch (pl.bn) {
-        case 16: return launch<16, true, 4>(pl, tp, tq, p, stream);
-        case 32: return launch<32, true, 4>(pl, tp, tq, p, stream);
-        case 64: return launch<64, true, 4>(pl, tp, tq, p, stream);
+        case 16: return launch<16, true, 4, 1>(pl, tp, tq, tc, p, stream);
+        case 32: return launch<32, true, 4, 1>(pl, tp, tq, tc, p, stream);
+        case 64: return launch<64, true, 4, 1>(pl, tp, tq, tc, p, stream);
         case 128:
-            return pl.qvec ? launch<128, true, 8>(pl, tp, tq, p, stream) : launch<128, false, 8>(pl, tp, tq, p, stream);
+            return pl.qvec ? launch<128, true, 8, 1>(pl, tp, tq, tc, p, stream)
+                           : launch<128, false, 8, 1>(pl, tp, tq, tc, p, stream);
         default:
-            return pl.qvec ? launch<256, true, 8>(pl, tp, tq, p, stream) : launch<256, false, 8>(pl, tp, tq, p, stream);
+            return pl.qvec ? launch<256, true, 8, 2>(pl, tp, tq, tc, p, stream)
+                           : launch<256, false, 8, 2>(pl, tp, tq, tc, p, stream);
     }
 }
 
@@ -731,47 +927,56 @@ ScaleView view_of(const gemm_block_scale_t *s, int64_t stride_e) {
     return ScaleView{s->scale, s->stride_k, s->stride_i, stride_e, s->block == 128 ? 7 : 0};
 }
 
-uint32_t idesc_of(int dtype, int bn, int p_mn, int q_mn) {
+uint32_t idesc_of(int dtype, int bn, int cg, int p_mn, int q_mn) {
     // D f32 (bit 4), A/B format (bits 7-9, 10-12: e4m3 0, e5m2 1), A / B MN-major
     // (bits 15, 16), N >> 3 (bits 17-22), M >> 4 (bits 24-28)
     const uint32_t fmt = dtype == GEMM_E5M2 ? 1u : 0u;
     return (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)p_mn << 15) | ((uint32_t)q_mn << 16) |
-           ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(kLanes >> 4) << 24);
+           ((uint32_t)(bn >> 3) << 17) | ((uint32_t)((kLanes * cg) >> 4) << 24);
 }
 
-// Tile width, roles and K ranges of one product.
+// Tile shape, roles and K ranges of one product.
 ScaledPlan plan_product(int64_t M, int64_t N, int64_t num_kb, bool a_col, bool b_tile, int sms) {
     ScaledPlan pl = {};
+    pl.cg = 1;
+    pl.splits = 1;
     if (M <= 64 && !a_col) {
         pl.swap = 1;
         pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
         pl.qvec = 1;
     } else {
-        const int64_t tm = cdiv(M, kLanes);
-        pl.bn = tm * cdiv(N, 256) >= sms ? 256 : 128;
+        pl.bn = 128;
+        if (cdiv(M, 256) * cdiv(N, 256) * 2 > sms / 2) {
+            pl.bn = 256;
+            pl.cg = 2;
+        }
         pl.qvec = !b_tile;
     }
-    const int64_t tiles = pl.swap ? cdiv(N, kLanes) * cdiv(M, pl.bn) : cdiv(M, kLanes) * cdiv(N, pl.bn);
-    pl.splits = 1;
-    while (pl.splits < 8 && tiles * pl.splits * 2 <= sms && num_kb >= 4 * pl.splits * 2) pl.splits *= 2;
-    pl.grid = (int)(pl.splits > 1 ? tiles * pl.splits : std::min<int64_t>(tiles, sms));
+    const int64_t tiles = pl.swap ? cdiv(N, kLanes) * cdiv(M, pl.bn) : cdiv(M, kLanes * pl.cg) * cdiv(N, pl.bn);
+    if (pl.cg == 1)
+        while (pl.splits < 8 && tiles * pl.splits * 2 <= sms && num_kb >= 4 * pl.splits * 2) pl.splits *= 2;
+    pl.grid = (int)(pl.splits > 1 ? tiles * pl.splits : std::min<int64_t>(tiles, sms / pl.cg) * pl.cg);
     return pl;
 }
 
-// Tile width and roles of an expert product, from the rows an expert has on average.
+// Tile shape and roles of an expert product, from the rows an expert has on average.
 ScaledPlan plan_experts(int64_t rows, int64_t N, int64_t experts, int sms) {
     ScaledPlan pl = {};
     const int64_t used = std::max<int64_t>(1, std::min(rows, experts)), avg = cdiv(rows, used);
+    pl.cg = 1;
+    pl.splits = 1;
     if (avg <= 64) {
         pl.swap = 1;
         pl.bn = avg <= 12 ? 16 : avg <= 24 ? 32 : 64;
         pl.qvec = 1;
+    } else if (avg < 256) {
+        pl.bn = 128;
     } else {
         pl.bn = 256;
+        pl.cg = 2;
     }
-    const int64_t wt = pl.swap ? cdiv(N, kLanes) : cdiv(N, pl.bn), rt = pl.swap ? pl.bn : kLanes;
-    pl.splits = 1;
-    pl.grid = (int)std::min<int64_t>(sms, wt * (cdiv(rows, rt) + used));
+    const int64_t wt = pl.swap ? cdiv(N, kLanes) : cdiv(N, pl.bn), rt = pl.swap ? pl.bn : kLanes * pl.cg;
+    pl.grid = (int)std::min<int64_t>(sms / pl.cg, wt * (cdiv(rows, rt) + used)) * pl.cg;
     return pl;
 }
 
@@ -819,23 +1024,32 @@ int encode_and_launch(const ScaledPlan &pl, ScaledParams &p, const Operand &a, i
     const Operand &P = pl.swap ? b : a, &Q = pl.swap ? a : b;
     p.p_mn = pl.swap ? !b_major : a_major;
     p.q_mn = pl.swap ? a_major : !b_major;
-    p.idesc = idesc_of(dtype, pl.bn, p.p_mn, p.q_mn);
+    p.idesc = idesc_of(dtype, pl.bn, pl.cg, p.p_mn, p.q_mn);
     p.swapped = pl.swap;
     p.splits = pl.splits;
     p.kb_per_split = (int)cdiv(p.num_kb, pl.splits);
     p.group_i = 16;
     p.timeout_ns = (unsigned long long)options_snapshot().wait_timeout_ms * 1000000ull;
-    CUtensorMap tp, tq;
+    CUtensorMap tp, tq, tc;
     std::memset(&tp, 0, sizeof tp);
     std::memset(&tq, 0, sizeof tq);
+    std::memset(&tc, 0, sizeof tc);
     if (p.num_kb > 0) {
         const int64_t pe = pl.swap ? experts : 1, qe = pl.swap ? 1 : experts;
         int rc = encode_bytes(&tp, P.p, P.rows, P.cols, P.ld_use, pe, b_expert, kLanes);
         if (rc == GEMM_OK)
-            rc = encode_bytes(&tq, Q.p, Q.rows, Q.cols, Q.ld_use, qe, b_expert, p.q_mn ? 128 : pl.bn);
+            rc = encode_bytes(&tq, Q.p, Q.rows, Q.cols, Q.ld_use, qe, b_expert, p.q_mn ? 128 : pl.bn / pl.cg);
         if (rc) return rc;
     }
-    return launch_plan(pl, tp, tq, p, stream);
+    const int out = p.epi.active ? p.epi.out : GEMM_OUT_F32, ob = op_type_bytes(out);
+    const int64_t rows = pl.swap ? p.J : p.I, cols = pl.swap ? p.I : p.J;
+    p.wide = op_wide(p.C, p.ldc, ob);
+    p.tma_store = !pl.swap && pl.splits == 1 && p.wide && (cols * ob) % 16 == 0;
+    if (p.tma_store) {
+        const int rc = encode_rows(&tc, p.C, out, rows, cols, p.ldc);
+        if (rc) return rc;
+    }
+    return launch_plan(pl, tp, tq, tc, p, stream);
 }
 
 }  // namespace
@@ -890,16 +1104,14 @@ int gemm_run_scaled(int64_t M, int64_t N, int64_t K, int dtype, const void *A, i
     p.I = (int)(pl.swap ? N : M);
     p.J = (int)(pl.swap ? M : N);
     p.num_kb = (int)num_kb;
-    const int64_t ti = cdiv(p.I, kLanes), tj = cdiv(p.J, pl.bn);
+    const int64_t ti = cdiv(p.I, kLanes * pl.cg), tj = cdiv(p.J, pl.bn);
     if (ti * tj * pl.splits > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
     p.tiles_i = (int)ti;
     p.tiles_j = (int)tj;
     p.sp = view_of(pl.swap ? b_scale : a_scale, 0);
     p.sq = view_of(pl.swap ? a_scale : b_scale, 0);
     p.C = C;
-    p.c_i = pl.swap ? 1 : ldc;
-    p.c_j = pl.swap ? ldc : 1;
-    p.wide = op_wide(C, ldc, ob);
+    p.ldc = ldc;
     p.epi = epi;
     p.tokens_on_i = !pl.swap;
     int dev = 0;
@@ -965,9 +1177,7 @@ int gemm_run_experts(int64_t rows, int64_t N, int64_t K, int64_t experts, int dt
     p.sp = view_of(pl.swap ? b_scale : a_scale, pl.swap ? b_scale_expert : 0);
     p.sq = view_of(pl.swap ? a_scale : b_scale, pl.swap ? 0 : b_scale_expert);
     p.C = C;
-    p.c_i = pl.swap ? 1 : ldc;
-    p.c_j = pl.swap ? ldc : 1;
-    p.wide = op_wide(C, ldc, ob);
+    p.ldc = ldc;
     p.epi = epi;
     p.offsets = offsets;
     p.experts = (int)experts;
