@@ -15,14 +15,16 @@
 //
 // The order by expert is a counting sort without atomics on global memory, so
 // it does not depend on timing: a block takes 32 neighbouring tokens and keeps
-// one word a expert in shared memory, bit t set when token t chose it; a pair's
+// one word an expert in shared memory, bit t set when token t chose it; a pair's
 // rank in the block is a population count, the block's counts go to a table,
 // a second kernel scans the table's rows (one per expert, over the blocks) and
-// a third adds the experts' offsets.  Up to kOneBlockTokens tokens one block
-// does all of it in one launch.
+// a third adds the experts' offsets.  Up to kClusterTokens tokens the blocks of
+// one cluster, 16 tokens each, read one another's counts in shared memory and
+// do all of it in one launch.
 #include <type_traits>
 
 #include "ops.h"
+#include "ptx_ops.cuh"
 
 namespace tcgemm {
 namespace {
@@ -31,9 +33,8 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxGroups = 32;
 constexpr int kMaxTopK = 32;
 constexpr int kChunkTokens = 32;       // tokens of a block: bits of a word
-constexpr int kChunkWarps = 8;
-constexpr int kOneBlockTokens = 128;   // tokens one block routes and orders alone
-constexpr int kOneBlockWarps = 32;
+constexpr int kWarps = 16;             // of a routing block
+constexpr int kClusterTokens = 128;    // tokens one cluster routes and orders in one launch
 
 struct RouteParams {
     const void *logits;
@@ -86,6 +87,13 @@ __device__ __forceinline__ void load_row(const T *row, int experts, int lane, bo
     }
 }
 
+// From the shared memory of a block of the cluster (a shared::cluster address).
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -97,38 +105,26 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// Scores of a row; masked experts (-inf) get 0.  An infinite logit takes its
-// limit: the softmax is shared by the infinite ones.
-template <int EPL>
-__device__ __forceinline__ void scores(const float (&x)[EPL], int score, float (&s)[EPL]) {
-    if (score == GEMM_SCORE_SIGMOID) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) s[i] = x[i] > -INFINITY ? 1.f / (1.f + expf(-x[i])) : 0.f;
-        return;
-    }
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
-    m = warp_max(m);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        s[i] = !(x[i] > -INFINITY) ? 0.f : m == INFINITY ? (x[i] == INFINITY ? 1.f : 0.f) : expf(x[i] - m);
-        sum += s[i];
-    }
-    sum = warp_sum(sum);
-    if (sum > 0.f) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) s[i] = s[i] / sum;
-    }
+// exp(x - m), m the row's largest; masked experts (-inf) have 0.  An infinite
+// logit takes its limit: the softmax is shared by the infinite ones.
+__device__ __forceinline__ float softmax_term(float x, float m) {
+    if (!(x > -INFINITY)) return 0.f;
+    return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : expf(x - m);
 }
 
-// Bits of the groups a token may choose from (bit g).  `v`: what the groups are
+// An expert's score; z: the sum of the row's terms (softmax).
+__device__ __forceinline__ float score_of(int score, float x, float m, float z) {
+    if (!(x > -INFINITY)) return 0.f;
+    return score == GEMM_SCORE_SIGMOID ? 1.f / (1.f + expf(-x)) : softmax_term(x, m) / z;
+}
+
+// Clears the keys of the experts whose group does not take part.  `v`: what the groups are
 // judged by (keys, or scores where there is no bias), masked experts -inf; it
 // goes through the warp's `buf` (padded one word in 32).  lanes: 32 over the
 // power of two at or above the number of groups; `lanes` neighbouring lanes scan one group.
 template <int EPL>
-__device__ __forceinline__ uint32_t choose_groups(const RouteParams &p, const float (&v)[EPL], float *buf, int lane) {
+__device__ __forceinline__ void keep_groups(const RouteParams &p, const float (&v)[EPL], uint32_t (&key)[EPL], float *buf,
+                                            int lane) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const int e = expert_of(i, lane);
@@ -162,162 +158,212 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteParams &p, const fl
     const uint32_t keep = __ballot_sync(0xffffffffu, sub == 0 && mine != 0u && ahead < p.top_groups);
     uint32_t bits = 0;
     for (int o = 0; o < p.groups; ++o) bits |= ((keep >> (o * lanes)) & 1u) << o;
-    return bits;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = expert_of(i, lane);
+        if (e < p.experts && !((bits >> (e / p.per)) & 1u)) key[i] = 0u;
+    }
+}
+
+// The largest of a lane's keys and its place (the first of equals).
+template <int EPL>
+__device__ __forceinline__ void lane_best(const uint32_t (&key)[EPL], uint32_t &best, int &at) {
+    best = key[0];
+    at = 0;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i)
+        if (key[i] > best) {
+            best = key[i];
+            at = i;
+        }
 }
 
 // Routes token t by one warp; lane j < top_k returns the j-th choice (or -1)
 // and writes it with its weight.
 template <typename T, int EPL>
 __device__ __forceinline__ int route_token(const RouteParams &p, int t, float *buf, int lane) {
-    float x[EPL], s[EPL];
-    load_row<T, EPL>(static_cast<const T *>(p.logits) + (int64_t)t * p.ldl, p.experts, lane, p.wide, x);
-    scores<EPL>(x, p.score, s);
+    float x[EPL];
+    const T *logits = static_cast<const T *>(p.logits) + (int64_t)t * p.ldl;
+    load_row<T, EPL>(logits, p.experts, lane, p.wide, x);
     const bool grouped = p.groups > 1 && p.top_groups < p.groups;
+    const bool by_score = p.bias || (grouped && p.top2);      // the choice needs every expert's score
     uint32_t key[EPL];
-    {
+    float m = 0.f, z = 1.f;                                   // of the softmax: largest logit, sum
+    if (p.score == GEMM_SCORE_SOFTMAX) {
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+        m = warp_max(m);
+        // (renormalised weights divide by the chosen scores' sum: the whole sum cancels)
+        if (by_score || !p.renormalize) {
+            z = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) z += softmax_term(x[i], m);
+            z = warp_sum(z);
+        }
+    }
+    if (by_score) {
         float v[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = expert_of(i, lane);
-            v[i] = x[i];
-            if (p.bias && x[i] > -INFINITY) v[i] = s[i] + __ldg(p.bias + e);
+            const float s = score_of(p.score, x[i], m, z);
+            v[i] = p.bias && x[i] > -INFINITY ? s + __ldg(p.bias + e) : x[i];
             key[i] = key_of(v[i]);
-            if (grouped && !p.bias && p.top2 && key[i]) v[i] = s[i];
+            if (!p.bias) v[i] = s;
             if (!key[i]) v[i] = -INFINITY;
         }
-        if (grouped) {
-            const uint32_t keep = choose_groups<EPL>(p, v, buf, lane);
+        if (grouped) keep_groups<EPL>(p, v, key, buf, lane);
+    } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = expert_of(i, lane);
-                if (e < p.experts && !((keep >> (e / p.per)) & 1u)) key[i] = 0u;
-            }
-        }
+        for (int i = 0; i < EPL; ++i) key[i] = key_of(x[i]);
+        if (grouped) keep_groups<EPL>(p, x, key, buf, lane);
     }
+    // The largest key of all lanes' largest, top_k times; its lane looks for its next.
     int mine = -1;
-    float w = 0.f;
+    uint32_t best;
+    int at;
+    lane_best<EPL>(key, best, at);
     for (int j = 0; j < p.top_k; ++j) {
-        uint32_t best = key[0];
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top == 0u) break;
+        const uint32_t have = __ballot_sync(0xffffffffu, best == top);
+        const int e = expert_of(at, lane);
+        int winner = __ffs(have) - 1;
+        if (have & (have - 1)) {             // equal keys: the lowest expert's
+            const int low = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)e : 0xffffffffu);
+            winner = (low >> 2) & 31;
+        }
+        const int chosen = __shfl_sync(0xffffffffu, e, winner);
+        if (lane == j) mine = chosen;
+        if (lane == winner) {
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
-        best = __reduce_max_sync(0xffffffffu, best);
-        if (best == 0u) break;
-        int at = kMaxExperts;
-#pragma unroll
-        for (int i = EPL - 1; i >= 0; --i)
-            if (key[i] == best) at = expert_of(i, lane);
-        at = (int)__reduce_min_sync(0xffffffffu, (uint32_t)at);
-        float sel = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (expert_of(i, lane) == at) {
-                key[i] = 0u;
-                sel = s[i];
-            }
-        sel = __shfl_sync(0xffffffffu, sel, (at >> 2) & 31);
-        if (lane == j) {
-            mine = at;
-            w = sel;
+            for (int i = 0; i < EPL; ++i)
+                if (i == at) key[i] = 0u;
+            lane_best<EPL>(key, best, at);
         }
     }
+    float w = 0.f;
+    if (mine >= 0) w = score_of(p.score, OpType<T>::up(logits[mine]), m, z);
     if (p.renormalize) {
-        const float z = warp_sum(w);
-        if (z > 0.f) w = w / z;
+        const float sum = warp_sum(w);
+        if (sum > 0.f) w = w / sum;
     }
-    w *= p.scale;
     if (lane < p.top_k) {
         p.indices[(int64_t)t * p.top_k + lane] = mine;
-        p.weights[(int64_t)t * p.top_k + lane] = mine >= 0 ? w : 0.f;
+        p.weights[(int64_t)t * p.top_k + lane] = w * p.scale;
     }
     return mine;
 }
 
-// Exclusive sum of the block's first `n` values of `v` in shared memory, in
-// place, by warp 0; v[n] gets the total.  (Callers synchronise the block around it.)
-__device__ __forceinline__ void scan_by_warp(int32_t *v, int n, int lane) {
-    int32_t carry = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        const int32_t c = i < n ? v[i] : 0;
-        int32_t inc = c;
+// Exclusive sum of v[0 .. n) in shared memory, in place, by a block of THREADS;
+// v[n] gets the total.  n <= kMaxExperts.
+template <int THREADS>
+__device__ __forceinline__ void block_scan(int32_t *v, int n) {
+    constexpr int PER = kMaxExperts / THREADS;
+    __shared__ int32_t s_warp[THREADS / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t c[PER], sum = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        if (i < n) v[i] = carry + inc - c;
-        carry += __shfl_sync(0xffffffffu, inc, 31);
+    for (int k = 0; k < PER; ++k) {
+        const int i = (int)threadIdx.x * PER + k;
+        c[k] = i < n ? v[i] : 0;
+        sum += c[k];
     }
-    if (lane == 0) v[n] = carry;
+    int32_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int32_t at = inc - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const int32_t y = s_warp[w];
+        if (w < warp) at += y;
+        total += y;
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int i = (int)threadIdx.x * PER + k;
+        if (i < n) v[i] = at;
+        at += c[k];
+    }
+    if (threadIdx.x == 0) v[n] = total;
+    __syncthreads();
 }
 
-// One block for all tokens (at most 32 * WORDS): routes, counts, scans, places.
+// Few tokens: the blocks of one cluster, kWarps neighbouring tokens each, route
+// them, read one another's counts and place the pairs.
 template <typename T, int EPL>
-__global__ void __launch_bounds__(kOneBlockWarps * 32) route_one_block_kernel(const RouteParams p) {
-    pdl_enter();
-    constexpr int kWords = kOneBlockTokens / 32;
-    __shared__ uint32_t s_chose[kWords][EPL * 32];
-    __shared__ int32_t s_first[EPL * 32 + 1];
-    extern __shared__ float s_buf[];        // the warps' group buffers
+__global__ void __launch_bounds__(kWarps * 32) route_cluster_kernel(const RouteParams p) {
+    __shared__ uint32_t s_chose[EPL * 32];          // bit w: the block's w-th token chose the expert
+    __shared__ int32_t s_first[EPL * 32 + 1];       // the experts' first rows
+    __shared__ int32_t s_before[EPL * 32];          // pairs of the expert in the blocks before this one
+    extern __shared__ float s_buf[];                // the warps' group buffers
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kWords * EPL * 32; i += blockDim.x) (&s_chose[0][0])[i] = 0u;
+    const uint32_t rank = ptx::cluster_ctarank();
+    for (int i = threadIdx.x; i < EPL * 32; i += blockDim.x) s_chose[i] = 0u;
+    pdl_enter();
     __syncthreads();
-    int mine[kOneBlockTokens / kOneBlockWarps];
-#pragma unroll
-    for (int n = 0; n < kOneBlockTokens / kOneBlockWarps; ++n) {
-        const int t = n * kOneBlockWarps + warp;
-        mine[n] = -1;
-        if (t < p.tokens) {
-            mine[n] = route_token<T, EPL>(p, t, s_buf + warp * (EPL * 33), lane);
-            if (mine[n] >= 0) atomicOr(&s_chose[n][mine[n]], 1u << warp);   // (bits: the order of arrival is nothing)
-        }
+    const int t = (int)rank * kWarps + warp;
+    int mine = -1;
+    if (t < p.tokens) {
+        mine = route_token<T, EPL>(p, t, s_buf + warp * (EPL * 33), lane);
+        if (mine >= 0) atomicOr(&s_chose[mine], 1u << warp);      // (bits: the order of arrival is nothing)
     }
-    if (!p.offsets) return;
-    __syncthreads();
+    __syncwarp();
+    ptx::cluster_sync();
+    const uint32_t chose = ptx::smem_addr(s_chose);
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
-        int c = 0;
-#pragma unroll
-        for (int n = 0; n < kWords; ++n) c += __popc(s_chose[n][e]);
-        s_first[e] = c;
+        int before = 0, all = 0;
+        for (uint32_t r = 0; r < gridDim.x; ++r) {
+            const int c = __popc(ld_cluster_u32(ptx::mapa_shared(chose + 4u * (uint32_t)e, r)));
+            if (r < rank) before += c;
+            all += c;
+        }
+        s_before[e] = before;
+        s_first[e] = all;
     }
     __syncthreads();
-    if (warp == 0) scan_by_warp(s_first, p.experts, lane);
-    __syncthreads();
-    for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) p.offsets[e] = s_first[e];
+    block_scan<kWarps * 32>(s_first, p.experts);
+    if (rank == 0)
+        for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) p.offsets[e] = s_first[e];
     const int pairs = p.tokens * p.top_k;
-    for (int r = s_first[p.experts] + threadIdx.x; r < pairs; r += blockDim.x) p.order[r] = -1;
-#pragma unroll
-    for (int n = 0; n < kOneBlockTokens / kOneBlockWarps; ++n) {
-        const int t = n * kOneBlockWarps + warp;
-        if (t >= p.tokens || lane >= p.top_k) continue;
+    for (int r = s_first[p.experts] + (int)(rank * blockDim.x + threadIdx.x); r < pairs; r += (int)(gridDim.x * blockDim.x))
+        p.order[r] = -1;
+    if (t < p.tokens && lane < p.top_k) {
         int slot = -1;
-        if (mine[n] >= 0) {
-            slot = s_first[mine[n]] + __popc(s_chose[n][mine[n]] & ((1u << warp) - 1u));
-            for (int w = 0; w < n; ++w) slot += __popc(s_chose[w][mine[n]]);
+        if (mine >= 0) {
+            slot = s_first[mine] + s_before[mine] + __popc(s_chose[mine] & ((1u << warp) - 1u));
             p.order[slot] = t * p.top_k + lane;
         }
         p.slots[t * p.top_k + lane] = slot;
     }
+    __syncwarp();
+    ptx::cluster_sync();          // (no block leaves while another may read its shared memory)
 }
 
 // Routes a block's 32 tokens; leaves each pair's rank among the block's pairs of
 // its expert in slots, and the block's counts in the table.
 template <typename T, int EPL>
-__global__ void __launch_bounds__(kChunkWarps * 32) route_kernel(const RouteParams p) {
-    pdl_enter();
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
     __shared__ uint32_t s_chose[EPL * 32];
     extern __shared__ float s_buf[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < EPL * 32; i += blockDim.x) s_chose[i] = 0u;
+    pdl_enter();
     __syncthreads();
-    int mine[kChunkTokens / kChunkWarps];
+    int mine[kChunkTokens / kWarps];
 #pragma unroll
-    for (int n = 0; n < kChunkTokens / kChunkWarps; ++n) {
-        const int t = blockIdx.x * kChunkTokens + n * kChunkWarps + warp;
+    for (int n = 0; n < kChunkTokens / kWarps; ++n) {
+        const int t = blockIdx.x * kChunkTokens + n * kWarps + warp;
         mine[n] = -1;
         if (t < p.tokens) {
             mine[n] = route_token<T, EPL>(p, t, s_buf + warp * (EPL * 33), lane);
-            if (mine[n] >= 0) atomicOr(&s_chose[mine[n]], 1u << (n * kChunkWarps + warp));
+            if (mine[n] >= 0) atomicOr(&s_chose[mine[n]], 1u << (n * kWarps + warp));
         }
     }
     if (!p.offsets) return;
@@ -325,8 +371,8 @@ __global__ void __launch_bounds__(kChunkWarps * 32) route_kernel(const RoutePara
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
         p.table[(int64_t)e * p.blocks + blockIdx.x] = __popc(s_chose[e]);
 #pragma unroll
-    for (int n = 0; n < kChunkTokens / kChunkWarps; ++n) {
-        const int b = n * kChunkWarps + warp, t = blockIdx.x * kChunkTokens + b;
+    for (int n = 0; n < kChunkTokens / kWarps; ++n) {
+        const int b = n * kWarps + warp, t = blockIdx.x * kChunkTokens + b;
         if (t < p.tokens && lane < p.top_k)
             p.slots[(int64_t)t * p.top_k + lane] = mine[n] >= 0 ? __popc(s_chose[mine[n]] & ((1u << b) - 1u)) : -1;
     }
@@ -367,14 +413,13 @@ __global__ void __launch_bounds__(128) route_scan_kernel(const RouteParams p) {
 }
 
 // Ranks within blocks become rows.
-__global__ void __launch_bounds__(kChunkWarps * 32) route_place_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(256) route_place_kernel(const RouteParams p) {
     pdl_enter();
     __shared__ int32_t s_first[kMaxExperts + 1];
     const int32_t *totals = p.table + (int64_t)p.experts * p.blocks;
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_first[e] = totals[e];
     __syncthreads();
-    if (threadIdx.x < 32) scan_by_warp(s_first, p.experts, threadIdx.x);
-    __syncthreads();
+    block_scan<256>(s_first, p.experts);
     const int64_t pairs = (int64_t)p.tokens * p.top_k;
     const int64_t lo = (int64_t)blockIdx.x * kChunkTokens * p.top_k;
     for (int64_t i = lo + threadIdx.x; i < lo + kChunkTokens * p.top_k && i < pairs; i += blockDim.x) {
@@ -393,40 +438,61 @@ __global__ void __launch_bounds__(kChunkWarps * 32) route_place_kernel(const Rou
 template <typename T, int EPL>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteParams p) {
     pdl_enter();
+    __shared__ float s_ds[8][EPL * 32];             // a token's scores' gradient, by expert
     const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= p.tokens) return;
-    float x[EPL], s[EPL], ds[EPL];
-    load_row<T, EPL>(static_cast<const T *>(p.logits) + (int64_t)t * p.ldl, p.experts, lane, p.wide, x);
+    float *row = s_ds[threadIdx.x >> 5];
+    float x[EPL], s[EPL];
+    const T *logits = static_cast<const T *>(p.logits) + (int64_t)t * p.ldl;
+    load_row<T, EPL>(logits, p.experts, lane, p.wide, x);
     int mine = lane < p.top_k ? p.indices[(int64_t)t * p.top_k + lane] : -1;
     if (mine >= p.experts) mine = -1;
     float g = mine >= 0 ? p.scale * p.grad[(int64_t)t * p.top_k + lane] : 0.f;
-    scores<EPL>(x, p.score, s);
-    // lane j's chosen score, and at the end its gradient back at the expert's lane
-    float sel = 0.f;
-    for (int j = 0; j < p.top_k; ++j) {
-        const int e = __shfl_sync(0xffffffffu, mine, j);
-        float v = 0.f;
+    float m = 0.f, z = 1.f, sel = mine >= 0 ? OpType<T>::up(logits[mine]) : -INFINITY;
+    if (p.score == GEMM_SCORE_SOFTMAX) {
+        m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (expert_of(i, lane) == e) v = s[i];
-        v = __shfl_sync(0xffffffffu, v, e < 0 ? 0 : (e >> 2) & 31);
-        if (lane == j && e >= 0) sel = v;
+        for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+        m = warp_max(m);
+        z = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            s[i] = softmax_term(x[i], m);
+            z += s[i];
+        }
+        z = warp_sum(z);
+        if (z > 0.f) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) s[i] = s[i] / z;
+        }
     }
+#pragma unroll
+    for (int i = 0; i < EPL; i += 4)
+        *reinterpret_cast<float4 *>(row + expert_of(i, lane)) = make_float4(0.f, 0.f, 0.f, 0.f);
+    sel = score_of(p.score, sel, m, z);
     if (p.renormalize) {
         // with the weights themselves, so that one chosen expert's (always 1) gives exactly 0
-        const float z = warp_sum(sel);
-        if (z > 0.f) g = (g - warp_sum(g * (sel / z))) / z;
+        const float sum = warp_sum(sel);
+        if (sum > 0.f) g = (g - warp_sum(g * (sel / sum))) / sum;
     }
     if (mine < 0) g = 0.f;
     const float sum = warp_sum(g * sel);
+    __syncwarp();
+    if (mine >= 0) row[mine] = g;
+    __syncwarp();
+    float ds[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) ds[i] = 0.f;
-    for (int j = 0; j < p.top_k; ++j) {
-        const int e = __shfl_sync(0xffffffffu, mine, j);
-        const float gj = __shfl_sync(0xffffffffu, g, j);
+    for (int i = 0; i < EPL; i += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(row + expert_of(i, lane));
+        ds[i] = v.x;
+        ds[i + 1] = v.y;
+        ds[i + 2] = v.z;
+        ds[i + 3] = v.w;
+    }
+    if (p.score == GEMM_SCORE_SIGMOID) {
+        // (only the chosen experts' scores count)
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (e >= 0 && expert_of(i, lane) == e) ds[i] += gj;
+        for (int i = 0; i < EPL; ++i) s[i] = ds[i] != 0.f ? score_of(p.score, x[i], m, z) : 0.f;
     }
     T *out = static_cast<T *>(p.dlogits) + (int64_t)t * p.ldd;
 #pragma unroll
@@ -536,17 +602,29 @@ int gemm_route(int64_t tokens, int64_t experts, int type, const void *logits, in
     p.order = order;
     p.slots = slots;
     const bool grouped = p.groups > 1 && p.top_groups < p.groups;
-    if (tokens <= kOneBlockTokens && ordered) {
+    if (tokens <= kClusterTokens && ordered) {
         const cudaError_t e = op_by_type(type, [&](auto t) {
             return by_experts(p.experts, [&](auto epl) {
                 constexpr int EPL = decltype(epl)::value;
-                auto kern = route_one_block_kernel<decltype(t), EPL>;
-                const size_t smem = grouped ? kOneBlockWarps * EPL * 33 * 4 : 0;
-                if (smem + 24 * 1024 > 48 * 1024) {
-                    const cudaError_t f = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                    if (f != cudaSuccess) return f;
-                }
-                return launch_pdl(kern, dim3(1), dim3(kOneBlockWarps * 32), smem, stream, p);
+                auto kern = route_cluster_kernel<decltype(t), EPL>;
+                const size_t smem = grouped ? kWarps * EPL * 33 * 4 : 0;
+                cudaError_t f = cudaSuccess;
+                if (smem > 32 * 1024) f = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                if (f != cudaSuccess) return f;
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3((unsigned)((p.tokens + kWarps - 1) / kWarps));
+                cfg.blockDim = dim3(kWarps * 32);
+                cfg.dynamicSmemBytes = smem;
+                cfg.stream = stream;
+                cudaLaunchAttribute attr[2];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = cfg.gridDim.x;
+                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+                attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+                attr[1].val.programmaticStreamSerializationAllowed = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = options_snapshot().pdl != 1 ? 2 : 1;
+                return cudaLaunchKernelEx(&cfg, kern, p);
             });
         });
         return op_launched("route launch", e);
@@ -567,14 +645,18 @@ int gemm_route(int64_t tokens, int64_t experts, int type, const void *logits, in
     cudaError_t e = op_by_type(type, [&](auto t) {
         return by_experts(p.experts, [&](auto epl) {
             constexpr int EPL = decltype(epl)::value;
-            const size_t smem = grouped ? kChunkWarps * EPL * 33 * 4 : 0;
-            return launch_pdl(route_kernel<decltype(t), EPL>, dim3(p.blocks), dim3(kChunkWarps * 32), smem, stream, p);
+            auto kern = route_kernel<decltype(t), EPL>;
+            const size_t smem = grouped ? kWarps * EPL * 33 * 4 : 0;
+            cudaError_t f = cudaSuccess;
+            if (smem > 32 * 1024) f = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (f != cudaSuccess) return f;
+            return launch_pdl(kern, dim3(p.blocks), dim3(kWarps * 32), smem, stream, p);
         });
     });
     if (ordered) {
         if (e == cudaSuccess) e = launch_pdl(route_scan_kernel, dim3((p.experts + 3) / 4), dim3(128), 0, stream, p);
         if (e == cudaSuccess)
-            e = launch_pdl(route_place_kernel, dim3(p.blocks), dim3(kChunkWarps * 32), 0, stream, p);
+            e = launch_pdl(route_place_kernel, dim3(p.blocks), dim3(256), 0, stream, p);
         const cudaError_t f = cudaFreeAsync(ws, stream);
         if (e == cudaSuccess) e = f;
     }

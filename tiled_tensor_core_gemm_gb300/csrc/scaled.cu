@@ -47,6 +47,8 @@ constexpr int kBlockK = 128;
 constexpr int kSmemMax = 232448;
 constexpr int kCtrlBytes = 1024;       // barriers and flags
 constexpr int kMaxExperts = 1024;
+constexpr int kGroup = 4;              // K-blocks whose scales come together
+constexpr int kSlots = 2;
 
 enum Role : uint32_t { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleDrain = 4, kRoleScales = 5 };
 
@@ -92,16 +94,19 @@ struct Cfg {
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr bool SWAPPED = BN < 128;          // the tiles of few tokens
     static constexpr int OUT_BYTES = SWAPPED ? 2048 : 4096;           // a warp's staging for C
-    static constexpr int SLOTS = BN >= 256 && QVEC ? 4 : 8;          // of the scale ring
-    static constexpr int SCALES = kLanes + (QVEC ? BN : 0) + 4;      // floats of a slot: lanes, columns or one
-    static constexpr int SLOT_BYTES = (SCALES * 4 + 15) / 16 * 16;
-    static constexpr int FIXED = 1024 + kCtrlBytes + SLOTS * SLOT_BYTES + EW * OUT_BYTES + 2 * (kMaxExperts + 1) * 4 + 32;
+    // Scales come four K-blocks at a time, in two slots of shared memory: for
+    // each K-block the lanes' 128 and the columns' BN, or, with one scale for 128
+    // columns, the lanes' times each 128 columns' one.
+    static constexpr int HALVES = (BN + 127) / 128;
+    static constexpr int SCALES = QVEC ? kLanes + BN : kLanes * HALVES;     // floats of a K-block
+    static constexpr int SLOT_BYTES = kGroup * SCALES * 4;
+    static constexpr int FIXED = 1024 + kCtrlBytes + kSlots * SLOT_BYTES + EW * OUT_BYTES + 2 * (kMaxExperts + 1) * 4 + 32;
     static constexpr int FIT = (kSmemMax - FIXED) / STAGE;
     static constexpr int STAGES = FIT > 12 ? 12 : FIT;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
     static_assert(!SPLIT_REGS || THREADS == 384, "the register split is written for 384 threads");
     static_assert(STAGES >= 3 && SMEM <= kSmemMax, "ring");
-    static_assert((2 * STAGES + NBUF + 2 * SLOTS) * 8 + 16 <= kCtrlBytes, "barrier area");
+    static_assert((2 * STAGES + NBUF + 2 * kSlots) * 8 + 16 <= kCtrlBytes, "barrier area");
     static_assert(CG == 2 || kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
 };
 
@@ -139,12 +144,10 @@ __device__ __noinline__ void wait_landed(uint32_t bar, uint32_t parity, unsigned
 struct Ring {
     int i = 0;
     uint32_t phase = 0;
-    bool laps = false;         // been round once
     __device__ __forceinline__ void next(int n) {
         if (++i == n) {
             i = 0;
             phase ^= 1u;
-            laps = true;
         }
     }
 };
@@ -234,48 +237,53 @@ __device__ __forceinline__ void add_scaled_columns(float *acc, const uint32_t (&
     }
 }
 
-// One warp's side of the scales of a tile: COUNT of them a K-block, of the rows
-// base, base + STEP, ...  AHEAD K-blocks are loaded together, and the next ones
-// are in flight while these are handed over: a load takes about as long as one
-// K-block's MMAs.
-template <int PER, int COUNT, int STEP, int SLOTS>
-__device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int end, int e, int kb0, int kb1, int t,
-                                             Ring &sl, uint8_t *slots, int slot_bytes, uint32_t scf0, uint32_t sce0,
+// One warp's share of a tile's scales: COUNT of them a K-block, of the rows base,
+// base + 1, ..., each times the one of `by`'s row by_row (BY), kGroup K-blocks at a
+// time.  The next group's loads are in flight while one is handed over (but for
+// 256 of them, which its registers do not hold twice): a load takes about as
+// long as a K-block's MMAs.
+template <int COUNT, bool BY>
+__device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int end, int e, const ScaleView &by,
+                                             int by_row, int by_end, int by_e, int kb0, int kb1, int t, Ring &sl,
+                                             uint8_t *slots, int slot_bytes, int kb_floats, uint32_t scf0, uint32_t sce0,
                                              volatile int *abort_flag, unsigned long long timeout_ns) {
-    constexpr int AHEAD = PER > 4 ? 2 : 4;
+    constexpr int PER = (COUNT + 31) / 32;
     const int lane = threadIdx.x & 31;
-    float cur[AHEAD][PER], nxt[AHEAD][PER];
+    constexpr bool kAhead = PER <= 4;
+    float cur[kGroup][PER], nxt[kGroup][PER];
     auto load = [&](int kb) {
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a)
+        for (int a = 0; a < kGroup; ++a) {
+            const float f = BY && kb + a < kb1 ? scale_at(by, by_row, by_end, kb + a, by_e) : 1.f;
 #pragma unroll
-            for (int c = 0; c < PER; ++c)
-                nxt[a][c] = kb + a < kb1 && 32 * c + lane < COUNT
-                                ? scale_at(v, base + (32 * c + lane) * STEP, end, kb + a, e) : 0.f;
+            for (int c = 0; c < PER; ++c) {
+                nxt[a][c] = kb + a < kb1 && 32 * c + lane < COUNT ? scale_at(v, base + 32 * c + lane, end, kb + a, e) : 0.f;
+                if (BY) nxt[a][c] *= f;
+            }
+        }
     };
-    load(kb0);
-    for (int kb = kb0; kb < kb1; kb += AHEAD) {
+    if (kAhead) load(kb0);
+    for (int kb = kb0; kb < kb1; kb += kGroup) {
+        if (!kAhead) load(kb);
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a)
+        for (int a = 0; a < kGroup; ++a)
 #pragma unroll
             for (int c = 0; c < PER; ++c) cur[a][c] = nxt[a][c];
-        load(kb + AHEAD);
+        if (kAhead) load(kb + kGroup);
+        const bool got = wait_bar(sce0 + 8u * (uint32_t)sl.i, sl.phase ^ 1u, abort_flag, timeout_ns);
+        if (!__all_sync(0xffffffffu, got)) {
+            if (lane == 0) record_failure(kRoleScales, t, abort_flag);
+            return false;
+        }
+        float *slot = reinterpret_cast<float *>(slots + sl.i * slot_bytes);
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            if (kb + a >= kb1) break;
-            const bool got = wait_bar(sce0 + 8u * (uint32_t)sl.i, sl.phase ^ 1u, abort_flag, timeout_ns);
-            if (!__all_sync(0xffffffffu, got)) {
-                if (lane == 0) record_failure(kRoleScales, t, abort_flag);
-                return false;
-            }
-            float *slot = reinterpret_cast<float *>(slots + sl.i * slot_bytes);
+        for (int a = 0; a < kGroup; ++a)
 #pragma unroll
             for (int c = 0; c < PER; ++c)
-                if (32 * c + lane < COUNT) slot[32 * c + lane] = cur[a][c];
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(scf0 + 8u * (uint32_t)sl.i);
-            sl.next(SLOTS);
-        }
+                if (32 * c + lane < COUNT) slot[a * kb_floats + 32 * c + lane] = cur[a][c];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(scf0 + 8u * (uint32_t)sl.i);
+        sl.next(kSlots);
     }
     return true;
 }
@@ -459,9 +467,9 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     uint8_t *out_bufs = ring + Cf::STAGES * Cf::STAGE;          // 1024-byte aligned, as the ring's slots are
     uint64_t *bars = reinterpret_cast<uint64_t *>(out_bufs + EW * Cf::OUT_BYTES);
     uint8_t *scales = reinterpret_cast<uint8_t *>(bars) + kCtrlBytes;
-    int32_t *first_tile = reinterpret_cast<int32_t *>(scales + Cf::SLOTS * Cf::SLOT_BYTES);
+    int32_t *first_tile = reinterpret_cast<int32_t *>(scales + kSlots * Cf::SLOT_BYTES);
     int32_t *first_row = first_tile + kMaxExperts + 1;
-    constexpr int kBars = 2 * Cf::STAGES + Cf::NBUF + 2 * Cf::SLOTS;
+    constexpr int kBars = 2 * Cf::STAGES + Cf::NBUF + 2 * kSlots;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -470,7 +478,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     auto done = [&](int s) { return bar0 + 8u * (uint32_t)(Cf::STAGES + s); };    // the MMAs of a stage have completed
     auto acce = [&](int b) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + b); };
     auto scf = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + s); };
-    auto sce = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + Cf::SLOTS + s); };
+    auto sce = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + kSlots + s); };
     const uint32_t scales0 = ptx::smem_addr(scales), out0 = ptx::smem_addr(out_bufs), scf0 = scf(0), sce0 = sce(0);
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -485,8 +493,8 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
         for (int b = 0; b < Cf::NBUF; ++b) {
             ptx::mbar_init(acce(b), EW * CG);
         }
-        for (int s = 0; s < Cf::SLOTS; ++s) {
-            ptx::mbar_init(scf(s), 2);       // the lanes' and the columns' scale warps
+        for (int s = 0; s < kSlots; ++s) {
+            ptx::mbar_init(scf(s), QVEC || Cf::HALVES == 2 ? 2 : 1);       // the scale warps
             ptx::mbar_init(sce(s), EW);
         }
         *abort_flag = 0;
@@ -549,14 +557,15 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     const int kb0 = (int)crank * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
 
     // 128 columns a thread need more than the launch's 168 registers: the first
-    // warpgroup gives the difference (128 x 72 + 256 x 216 = 384 x 168).
+    // warpgroup gives the difference (128 x 56 + 256 x 224 = 384 x 168, or with a
+    // scale per column, 256 of which a warp brings, 128 x 72 + 256 x 216).
     if (warp < 4) {
-        if (Cf::SPLIT_REGS) ptx::regs_give_back<72>();
+        if (Cf::SPLIT_REGS) ptx::regs_give_back<QVEC ? 72 : 56>();
         if (warp == 0) {
             // ------------------------------------------------------ TMA producer
             if (lane == 0) {
                 Ring rg;
-                bool ok = true;
+                bool ok = true, laps = false;      // laps: the ring has been round once
                 for (int t = unit; ok && t < num_tiles; t += units) {
                     const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
                     const int ep = p.tokens_on_i ? 0 : T.e, eq = p.tokens_on_i ? T.e : 0;
@@ -581,6 +590,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                             ptx::tma_load_3d<CG>(sq, &tmQ, to, k0, j0, eq);
                         }
                         rg.next(Cf::STAGES);
+                        laps = laps || rg.i == 0;
                     }
                 }
                 // Until the MMAs have released every slot no read of this shared
@@ -597,7 +607,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 // Given up: the copies already issued still land in this shared memory.
                 for (int i = 0; !ok && rank == 0 && i < Cf::STAGES; ++i) {
                     const uint32_t parity = i < last.i ? last.phase : last.phase ^ 1u;
-                    if (last.laps || i < last.i) wait_landed(full(i), parity, p.timeout_ns);   // (of a pair: in the leader)
+                    if (laps || i < last.i) wait_landed(full(i), parity, p.timeout_ns);   // (of a pair: in the leader)
                 }
             }
             __syncwarp();
@@ -614,6 +624,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 uint32_t last_bar = 0, last_parity = 0;      // of the MMAs issued last
                 for (int t = unit; ok && t < num_tiles; t += units) {
                     for (int kb = kb0; kb < kb1; ++kb) {
+                        // (the operands first: the accumulator is what comes last)
                         const bool got = wait_bar(full(rg.i), rg.phase, abort_flag, p.timeout_ns) &&
                                          wait_bar(acce(buf.i), buf.phase ^ 1u, abort_flag, p.timeout_ns);
                         if (!__all_sync(0xffffffffu, got)) {
@@ -650,22 +661,25 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             __syncwarp();
         } else {
             // ------------------------------------------------------------ scales
-            const bool lanes_side = warp == 2;
+            const bool first_warp = warp == 2;
             Ring sl;
-            bool ok = true;
+            bool ok = QVEC || first_warp || Cf::HALVES == 2;
             for (int t = unit; ok && t < num_tiles; t += units) {
                 const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
-                if (lanes_side)
-                    ok = bring_scales<4, kLanes, 1, Cf::SLOTS>(p.sp, T.i0 + (int)rank * kLanes, T.i1, p.tokens_on_i ? 0 : T.e, kb0, kb1, t, sl, scales,
-                                                    Cf::SLOT_BYTES, scf0, sce0, abort_flag, p.timeout_ns);
+                const int ep = p.tokens_on_i ? 0 : T.e, eq = p.tokens_on_i ? T.e : 0;
+                const int i0 = T.i0 + (int)rank * kLanes;
+                if (QVEC && !first_warp)
+                    ok = bring_scales<BN, false>(p.sq, T.j0, T.j1, eq, p.sq, 0, 1, 0, kb0, kb1, t, sl,
+                                                 scales + kLanes * 4, Cf::SLOT_BYTES, Cf::SCALES, scf0, sce0, abort_flag,
+                                                 p.timeout_ns);
                 else
-                    ok = bring_scales<QVEC ? (BN + 31) / 32 : 1, QVEC ? BN : (BN + 127) / 128, QVEC ? 1 : 128, Cf::SLOTS>(
-                        p.sq, T.j0, T.j1, p.tokens_on_i ? T.e : 0, kb0, kb1, t, sl, scales + kLanes * 4, Cf::SLOT_BYTES,
-                        scf0, sce0, abort_flag, p.timeout_ns);
+                    ok = bring_scales<kLanes, !QVEC>(p.sp, i0, T.i1, ep, p.sq, T.j0 + (first_warp ? 0 : 128), T.j1, eq, kb0,
+                                                     kb1, t, sl, scales + (first_warp ? 0 : kLanes * 4), Cf::SLOT_BYTES,
+                                                     Cf::SCALES, scf0, sce0, abort_flag, p.timeout_ns);
             }
         }
     } else {
-        if (Cf::SPLIT_REGS) ptx::regs_take<216>();
+        if (Cf::SPLIT_REGS) ptx::regs_take<QVEC ? 216 : 224>();
         // ------------------------------------------------- sums and epilogue
         const uint32_t quarter = warp & 3, half = (warp - 4) >> 2;     // lanes it may read; its columns
         const int row = (int)(quarter * 32 + lane), col0 = (int)half * Cf::COLS;   // of this CTA's 128
@@ -677,17 +691,24 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             float acc[Cf::COLS];
 #pragma unroll
             for (int c = 0; c < Cf::COLS; ++c) acc[c] = 0.f;
-            // A K-block's scale, and whether its MMAs have completed, are looked up
-            // while the last columns of the block before are on their way.
-            float s = 0.f;
+            // The next K-blocks' scales, and whether the next one's MMAs have
+            // completed, are looked up while this one's last columns are on their way.
+            float sv[kGroup];
+            uint32_t columns = 0;          // (a scale per column) the K-block's, in shared memory
             bool got = true, ready = false;
-            auto next_scale = [&](const Ring &at) {
-                got = wait_bar(scf(at.i), at.phase, abort_flag, p.timeout_ns);
-                const uint32_t slot = scales0 + (uint32_t)(at.i * Cf::SLOT_BYTES);
-                s = ptx::ld_shared_f(slot + 4u * (uint32_t)row);
-                if (!QVEC) s *= ptx::ld_shared_f(slot + 4u * (uint32_t)(kLanes + (col0 >> 7)));
+            auto next_group = [&]() {
+                got = wait_bar(scf(sl.i), sl.phase, abort_flag, p.timeout_ns);
+                const uint32_t slot = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES) +
+                                      4u * (uint32_t)(row + (QVEC ? 0 : (col0 >> 7) * kLanes));
+#pragma unroll
+                for (int a = 0; a < kGroup; ++a) sv[a] = ptx::ld_shared_f(slot + 4u * (uint32_t)(a * Cf::SCALES));
             };
-            if (kb0 < kb1) next_scale(sl);
+            auto release_group = [&]() {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sce(sl.i));
+                sl.next(kSlots);
+            };
+            if (kb0 < kb1) next_group();
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!ready) got = wait_bar(done(rg.i), rg.phase, abort_flag, p.timeout_ns) && got;
                 if (!__all_sync(0xffffffffu, got)) {
@@ -696,25 +717,42 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t columns = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES) + 4u * (uint32_t)(kLanes + col0);
-                const uint32_t src = tbase + (uint32_t)(buf.i * BN), sce_now = sce(sl.i), acce_now = acce(buf.i);
-                constexpr int kChunks = Cf::COLS / Cf::CHUNK;
-                const float s_now = s;
-                uint32_t r[2][Cf::CHUNK];
-                ptx::tmem_load(src, r[0]);
+                const uint32_t src = tbase + (uint32_t)(buf.i * BN), acce_now = acce(buf.i);
+                const int in = (kb - kb0) % kGroup;
+                const bool group_ends = in == kGroup - 1 || kb + 1 == kb1;
+                if (QVEC) columns = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES) + 4u * (uint32_t)(in * Cf::SCALES + kLanes + col0);
+                const float s = sv[0];
+#pragma unroll
+                for (int a = 0; a + 1 < kGroup; ++a) sv[a] = sv[a + 1];
                 rg.next(Cf::STAGES);
                 buf.next(Cf::NBUF);
-                sl.next(Cf::SLOTS);
+                // Two loads of 32 columns in flight; each is replaced by the one
+                // two further as soon as it has been added.
+                constexpr int kChunks = Cf::COLS / Cf::CHUNK;
+                uint32_t r[2][Cf::CHUNK];
+                auto add = [&](int c) {
+                    if (QVEC)
+                        add_scaled_columns<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s,
+                                                      columns + 4u * (uint32_t)(c * Cf::CHUNK));
+                    else
+                        add_scaled<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s);
+                };
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    if (c + 1 == kChunks && kb + 1 < kb1) {
-                        next_scale(sl);
+                for (int c = 0; c < kChunks; c += 2) {
+                    if (c == 0) {
+                        ptx::tmem_load(src, r[0]);
+                        if (kChunks > 1) ptx::tmem_load(src + (uint32_t)Cf::CHUNK, r[1]);
+                    }
+                    if (c + 2 >= kChunks && kb + 1 < kb1) {
+                        if (!QVEC && group_ends) {
+                            release_group();
+                            next_group();
+                        }
                         ready = ptx::mbar_test(done(rg.i), rg.phase);
                     }
-                    ptx::tmem_wait(r[c & 1]);
-                    if (c + 1 < kChunks) {
-                        ptx::tmem_load(src + (uint32_t)((c + 1) * Cf::CHUNK), r[(c + 1) & 1]);
-                    } else {
+                    ptx::tmem_wait(r[0]);
+                    if (kChunks > 1) ptx::tmem_wait(r[1]);
+                    if (c + 2 >= kChunks) {
                         // the accumulator is read: its next K-block may be summed
                         ptx::tc_fence_before();
                         __syncwarp();
@@ -723,15 +761,17 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                             else ptx::mbar_arrive(acce_now);
                         }
                     }
-                    if (QVEC)
-                        add_scaled_columns<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s_now,
-                                                      columns + 4u * (uint32_t)(c * Cf::CHUNK));
-                    else
-                        add_scaled<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s_now);
+                    add(c);
+                    if (c + 2 < kChunks) ptx::tmem_load(src + (uint32_t)((c + 2) * Cf::CHUNK), r[0]);
+                    if (c + 1 < kChunks) add(c + 1);
+                    if (c + 3 < kChunks) ptx::tmem_load(src + (uint32_t)((c + 3) * Cf::CHUNK), r[1]);
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(sce_now);
+                if (QVEC && group_ends) {
+                    release_group();
+                    if (kb + 1 < kb1) next_group();
+                }
             }
+            if (!QVEC && ok && kb0 < kb1) release_group();
             if (!ok) break;
             if (!kPair && p.splits > 1) {
                 // this CTA's K range of the tile, for the cluster to read: [column][lane]

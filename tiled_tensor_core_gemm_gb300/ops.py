@@ -84,50 +84,53 @@ def declare(lib):
 
 
 # ----------------------------------------------------------------- helpers ---
+# A decode step calls these operators for microseconds of GPU work each, so the
+# marshalling is kept short: integer device indices, the raw stream, and argument
+# structures that depend on scalars only are built once.
 _types = None
+_epilogues = {}
+_hows = {}
 
 
 def _tables():
-    """torch element types -> the ABI's codes."""
+    """(torch, the package, the library, torch element types -> the ABI's codes, ...)"""
     global _types
     if _types is None:
         import torch
         import tiled_tensor_core_gemm_gb300 as tg
-        _types = (torch, tg,
+        _types = (torch, tg, tg.load_library(),
                   {torch.float32: tg.GEMM_OUT_F32, torch.bfloat16: tg.GEMM_OUT_BF16, torch.float16: tg.GEMM_OUT_F16},
                   {torch.float8_e4m3fn: tg.GEMM_E4M3, torch.float8_e5m2: tg.GEMM_E5M2},
-                  {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16})
+                  {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16},
+                  torch._C._cuda_getCurrentRawStream)
     return _types
 
 
-def _done(tg, rc):
-    if rc != tg.GEMM_OK:
-        raise tg.GemmError(rc, tg.gemm_last_error())
-
-
-def _stream(torch, stream, device):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+def _fail(tg, rc):
+    raise tg.GemmError(rc, tg.gemm_last_error())
 
 
 def _cuda(first, *others):
-    """Every tensor given (None entries skipped) is a CUDA tensor on the first one's device."""
-    if not first.is_cuda:
+    """The CUDA device index every tensor given (None entries skipped) is on."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError("tensors must be CUDA tensors (this library has no CPU path)")
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return index
 
 
-def _rows(name, t):
-    """Row pitch of a 2-D tensor with unit stride along its columns."""
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+def _rows(name, t, rows, cols):
+    """Row pitch of a rows x cols tensor with unit stride along its columns."""
+    sr, sc = t.stride()
+    if cols > 1 and sc != 1:
         raise ValueError(f"{name} must have unit stride along its columns")
-    return max(t.stride(0) if rows > 1 else cols, 1)
+    return sr if rows > 1 and sr > 0 else (cols or 1)
 
 
 def _dense(name, t, shape, dtype):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor")
 
 
@@ -150,24 +153,33 @@ def _major(name, t):
     raise ValueError(f"{name} must be row-major or the transpose of a row-major matrix")
 
 
-def _scale(name, s, torch, extent, num_kb, k_dim, blocks):
-    """A BlockScale over a 2-D (or batched) scale tensor; k_dim: its dimension along K."""
-    if s.dtype != torch.float32:
+def _scale(name, s, f32, extent, num_kb, k_dim, tiles_ok):
+    """A BlockScale over a 2-D (or batched) scale tensor; k_dim: its dimension along K (-1 or -2)."""
+    if s.dtype is not f32:
         raise TypeError(f"{name} must be float32")
-    i_dim = -1 if k_dim == -2 else -2
-    n, kb = s.shape[i_dim], s.shape[k_dim]
-    tiles = -(-extent // BLOCK)
-    if kb != num_kb or not ((1 in blocks and n == extent) or (BLOCK in blocks and n == tiles)):
-        raise ValueError(f"{name}: {tuple(s.shape)} is not a scale for each block of 128 along K, for each row or "
-                         f"column{' or 128 of them' if BLOCK in blocks else ''} (extent {extent}, {num_kb} blocks)")
-    block = 1 if n == extent and 1 in blocks else BLOCK
+    shape, stride = s.shape, s.stride()
+    n, kb = shape[-3 - k_dim], shape[k_dim]
+    if kb == num_kb and n == extent:
+        block = 1
+    elif kb == num_kb and tiles_ok and n == -(-extent // BLOCK):
+        block = BLOCK
+    else:
+        raise ValueError(f"{name}: {tuple(shape)} is not a scale for each block of 128 along K, for each row or "
+                         f"column{' or 128 of them' if tiles_ok else ''} (extent {extent}, {num_kb} blocks)")
     # (a dimension of one element has no stride)
-    return BlockScale(s.data_ptr() or None, s.stride(k_dim) if kb > 1 else 0, s.stride(i_dim) if n > 1 else 0, block, 0)
+    return BlockScale(s.data_ptr(), stride[k_dim] if kb > 1 else 0, stride[-3 - k_dim] if n > 1 else 0, block, 0)
 
 
 def _epilogue(tg, alpha, beta, bias, act, out):
-    return ctypes.byref(tg.GemmEpilogue(alpha, beta, bias.data_ptr() if bias is not None else None,
-                                        tg.ACTIVATIONS[act], tg.OUT_TYPES[out]))
+    if bias is not None:
+        return ctypes.byref(tg.GemmEpilogue(alpha, beta, bias.data_ptr(), tg.ACTIVATIONS[act], tg.OUT_TYPES[out]))
+    key = (alpha, beta, act, out)
+    e = _epilogues.get(key)
+    if e is None:
+        e = ctypes.byref(tg.GemmEpilogue(alpha, beta, None, tg.ACTIVATIONS[act], tg.OUT_TYPES[out]))
+        if len(_epilogues) < 256:
+            _epilogues[key] = e
+    return e
 
 
 # --------------------------------------------------------------- operators ---
@@ -189,25 +201,30 @@ def quantize_block(x, block="row", dtype="e4m3", scatter=None, out_rows=None, st
     outside [0, out_rows) are skipped, and rows no entry names hold nothing
     defined.
     """
-    torch, tg, types, fp8, _ = _tables()
-    if x.dim() not in (2, 3):
+    torch, tg, lib, types, _, _, raw = _tables()
+    dims = x.dim()
+    if dims != 2 and dims != 3:
         raise ValueError("x must be a matrix or a batch of matrices")
-    if x.dtype not in types:
+    kind = types.get(x.dtype)
+    if kind is None:
         raise TypeError("x must be float32, bfloat16 or float16")
     code = _BLOCKS[block]
-    to = tg.DTYPES[dtype]
-    qdt = torch.float8_e4m3fn if to == tg.GEMM_E4M3 else torch.float8_e5m2 if to == tg.GEMM_E5M2 else None
-    if qdt is None:
+    if dtype == "e4m3":
+        to, qdt = tg.GEMM_E4M3, torch.float8_e4m3fn
+    elif dtype == "e5m2":
+        to, qdt = tg.GEMM_E5M2, torch.float8_e5m2
+    else:
         raise TypeError("dtype must be e4m3 or e5m2")
-    _cuda(x, scatter)
-    m, n = x.shape[-2:]
-    batch = x.shape[0] if x.dim() == 3 else 1
-    if n > 1 and x.stride(-1) != 1:
+    index = _cuda(x, scatter)
+    shape, stride = x.shape, x.stride()
+    m, n = shape[-2], shape[-1]
+    batch = shape[0] if dims == 3 else 1
+    if n > 1 and stride[-1] != 1:
         raise ValueError("x must have unit stride along its columns")
-    ldx = max(x.stride(-2) if m > 1 else n, 1)
+    ldx = max(stride[-2] if m > 1 else n, 1)
     rows, copies, slots = m, 1, None
     if scatter is not None:
-        if x.dim() != 2 or block != "row":
+        if dims != 2 or code != 0:
             raise ValueError("scatter takes one matrix and row blocks")
         if scatter.dim() != 2 or scatter.shape[0] != m:
             raise ValueError("scatter must have a row for each row of x")
@@ -219,25 +236,30 @@ def quantize_block(x, block="row", dtype="e4m3", scatter=None, out_rows=None, st
     pitch = -(-n // 16) * 16
     mb = rows if code == 0 else -(-m // BLOCK)
     nb = n if code == 1 else -(-n // BLOCK)
-    lead = (batch,) if x.dim() == 3 else ()
-    q = torch.empty(lead + (rows, pitch), dtype=qdt, device=x.device)
+    device = x.device
+    q = torch.empty((rows, pitch) if dims == 2 else (batch, rows, pitch), dtype=qdt, device=device)
+    at = q.data_ptr()
     if pitch != n:
         q = q[..., :n]
     if code == 0:
         held = -(-mb // 4) * 4
-        s = torch.empty(lead + (nb, held), dtype=torch.float32, device=x.device).transpose(-1, -2)
+        s = torch.empty((nb, held) if dims == 2 else (batch, nb, held), dtype=torch.float32, device=device)
+        s_at = s.data_ptr()
+        s = s.transpose(-1, -2)
         if held != mb:
             s = s[..., :mb, :]
-        s_row, s_col, s_batch = 1, held, nb * held
+        s_row, s_col, s_batch = 1, held or 1, nb * held
     else:
-        s = torch.empty(lead + (mb, nb), dtype=torch.float32, device=x.device)
+        s = torch.empty((mb, nb) if dims == 2 else (batch, mb, nb), dtype=torch.float32, device=device)
+        s_at = s.data_ptr()
         s_row, s_col, s_batch = nb, 1, mb * nb
     if copies == 0 or (scatter is not None and rows == 0):
         return q, s
-    _done(tg, tg.load_library().gemm_quantize_block(
-        batch, m, n, types[x.dtype], x.data_ptr(), ldx, x.stride(0) if batch > 1 else 0, code, to, q.data_ptr(), max(pitch, 1),
-        rows * pitch, s.data_ptr(), s_row, max(s_col, 1), s_batch, slots, copies, rows,
-        _stream(torch, stream, x.device)))
+    rc = lib.gemm_quantize_block(batch, m, n, kind, x.data_ptr(), ldx, stride[0] if batch > 1 else 0, code, to, at,
+                                 pitch or 1, rows * pitch, s_at, s_row, s_col, s_batch, slots, copies, rows,
+                                 raw(index) if stream is None else stream)
+    if rc:
+        _fail(tg, rc)
     return q, s
 
 
@@ -250,33 +272,38 @@ def gemm_scaled(A, a_scale, B, b_scale, C=None, alpha=1.0, beta=0.0, bias=None, 
     ceil(N/128)); any strides.  out: C's type, "f32", "bf16" or "f16"
     (allocated if None; beta must then be 0).  bias: N float32 values or None.
     """
-    torch, tg, _, fp8, outs = _tables()
+    torch, tg, lib, _, fp8, outs, raw = _tables()
     if A.dim() != 2 or B.dim() != 2 or a_scale.dim() != 2 or b_scale.dim() != 2:
         raise ValueError("operands and scales must be 2-D")
-    if A.dtype not in fp8 or B.dtype != A.dtype:
+    code = fp8.get(A.dtype)
+    if code is None or B.dtype is not A.dtype:
         raise TypeError("A and B must both be float8_e4m3fn or both float8_e5m2")
     m, k = A.shape
     k2, n = B.shape
     if k != k2:
         raise ValueError("inner dimensions differ")
-    _cuda(A, B, a_scale, b_scale, C, bias)
+    index = _cuda(A, B, a_scale, b_scale, C, bias)
     num_kb = -(-k // BLOCK)
     lda, a_major = _major("A", A)
     ldb, b_major = _major("B", B)
-    sa = _scale("a_scale", a_scale, torch, m, num_kb, -1, (1, BLOCK))
-    sb = _scale("b_scale", b_scale, torch, n, num_kb, -2, (1, BLOCK))
+    sa = _scale("a_scale", a_scale, torch.float32, m, num_kb, -1, True)
+    sb = _scale("b_scale", b_scale, torch.float32, n, num_kb, -2, True)
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
         C = torch.empty((m, n), dtype=outs[out], device=A.device)
-    elif C.dtype != outs[out] or tuple(C.shape) != (m, n):
+        ldc = n or 1
+    elif C.dtype is not outs[out] or C.shape != (m, n):
         raise TypeError(f"C must be a ({m}, {n}) {outs[out]} tensor")
+    else:
+        ldc = _rows("C", C, m, n)
     if bias is not None:
         _dense("bias", bias, (n,), torch.float32)
-    _done(tg, tg.load_library().gemm_run_scaled(
-        m, n, k, fp8[A.dtype], A.data_ptr(), lda, a_major, ctypes.byref(sa), B.data_ptr(), ldb, b_major,
-        ctypes.byref(sb), C.data_ptr(), _rows("C", C), _epilogue(tg, alpha, beta, bias, act, out),
-        _stream(torch, stream, A.device)))
+    rc = lib.gemm_run_scaled(m, n, k, code, A.data_ptr(), lda, a_major, ctypes.byref(sa), B.data_ptr(), ldb, b_major,
+                             ctypes.byref(sb), C.data_ptr(), ldc, _epilogue(tg, alpha, beta, bias, act, out),
+                             raw(index) if stream is None else stream)
+    if rc:
+        _fail(tg, rc)
     return C
 
 
@@ -290,36 +317,49 @@ def gemm_experts(A, a_scale, W, w_scale, offsets, C=None, alpha=1.0, act="none",
     (E, ceil(K/128), N).  offsets: (E + 1) int32 on the device, ascending.
     Rows outside every expert keep what C holds (undefined if C is None).
     """
-    torch, tg, _, fp8, outs = _tables()
+    torch, tg, lib, _, fp8, outs, raw = _tables()
     if A.dim() != 2 or W.dim() != 3 or a_scale.dim() != 2 or w_scale.dim() != 3:
         raise ValueError("A and a_scale must be 2-D, W and w_scale 3-D")
-    if A.dtype not in fp8 or W.dtype != A.dtype:
+    code = fp8.get(A.dtype)
+    if code is None or W.dtype is not A.dtype:
         raise TypeError("A and W must both be float8_e4m3fn or both float8_e5m2")
     rows, k = A.shape
     experts, k2, n = W.shape
     if k != k2 or w_scale.shape[0] != experts:
         raise ValueError("shapes do not match")
-    _cuda(A, W, a_scale, w_scale, offsets, C)
+    index = _cuda(A, W, a_scale, w_scale, offsets, C)
     _dense("offsets", offsets, (experts + 1,), torch.int32)
     num_kb = -(-k // BLOCK)
-    lda = _rows("A", A)
+    lda = _rows("A", A, rows, k)
     ldb, b_major = _major("W", W)
-    sa = _scale("a_scale", a_scale, torch, rows, num_kb, -1, (1,))
-    sw = _scale("w_scale", w_scale, torch, n, num_kb, -2, (1, BLOCK))
+    sa = _scale("a_scale", a_scale, torch.float32, rows, num_kb, -1, False)
+    sw = _scale("w_scale", w_scale, torch.float32, n, num_kb, -2, True)
     if C is None:
         C = torch.empty((rows, n), dtype=outs[out], device=A.device)
-    elif C.dtype != outs[out] or tuple(C.shape) != (rows, n):
+        ldc = n or 1
+    elif C.dtype is not outs[out] or C.shape != (rows, n):
         raise TypeError(f"C must be a ({rows}, {n}) {outs[out]} tensor")
-    _done(tg, tg.load_library().gemm_run_experts(
-        rows, n, k, experts, fp8[A.dtype], A.data_ptr(), lda, ctypes.byref(sa), offsets.data_ptr(), W.data_ptr(), ldb,
-        W.stride(0) if experts > 1 else 0, b_major, ctypes.byref(sw), w_scale.stride(0) if experts > 1 else 0,
-        C.data_ptr(), _rows("C", C), _epilogue(tg, alpha, 0.0, None, act, out), _stream(torch, stream, A.device)))
+    else:
+        ldc = _rows("C", C, rows, n)
+    rc = lib.gemm_run_experts(rows, n, k, experts, code, A.data_ptr(), lda, ctypes.byref(sa), offsets.data_ptr(),
+                              W.data_ptr(), ldb, W.stride(0) if experts > 1 else 0, b_major, ctypes.byref(sw),
+                              w_scale.stride(0) if experts > 1 else 0, C.data_ptr(), ldc,
+                              _epilogue(tg, alpha, 0.0, None, act, out), raw(index) if stream is None else stream)
+    if rc:
+        _fail(tg, rc)
     return C
 
 
-def _how(top_k, score, groups, top_groups, group_score, renormalize, scale):
-    return RouteHow(top_k, _SCORES[score], groups, groups if top_groups is None else top_groups,
-                    _GROUP_SCORES[group_score], 1 if renormalize else 0, scale)
+def _how(*rules):
+    """A reference to the RouteHow of (top_k, score, groups, top_groups, group_score, renormalize, scale)."""
+    h = _hows.get(rules)
+    if h is None:
+        top_k, score, groups, top_groups, group_score, renormalize, scale = rules
+        h = ctypes.byref(RouteHow(top_k, _SCORES[score], groups, groups if top_groups is None else top_groups,
+                                  _GROUP_SCORES[group_score], 1 if renormalize else 0, scale))
+        if len(_hows) < 256:
+            _hows[rules] = h
+    return h
 
 
 def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max", renormalize=True,
@@ -333,30 +373,27 @@ def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, 
     divided by their sum if renormalize, times scale.  A logit of -inf or NaN
     masks its expert.  The full rules are gemm_route's in include/gemm_ops.h.
     """
-    torch, tg, types, _, _ = _tables()
-    if logits.dim() != 2 or logits.dtype not in types:
+    torch, tg, lib, types, _, _, raw = _tables()
+    kind = types.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
         raise TypeError("logits must be a (tokens, experts) float32, bfloat16 or float16 tensor")
     tokens, experts = logits.shape
-    _cuda(logits, bias)
+    index = _cuda(logits, bias)
     if bias is not None:
         _dense("bias", bias, (experts,), torch.float32)
     how = _how(top_k, score, groups, top_groups, group_score, renormalize, scale)
-    pairs = tokens * max(int(top_k), 0)
-    # one allocation: indices, weights, order, slots (each on 16 bytes), offsets
-    part = -(-pairs // 4) * 4
-    held = torch.empty(4 * part + experts + 1, dtype=torch.int32, device=logits.device)
-    indices, weights, order, slots = held[:4 * part].view(4, part).unbind(0)
-    if part != pairs:
-        indices, weights, order, slots = indices[:pairs], weights[:pairs], order[:pairs], slots[:pairs]
-    offsets = held[4 * part:]
-    at = held.data_ptr()
-    step = 4 * part
-    _done(tg, tg.load_library().gemm_route(
-        tokens, experts, types[logits.dtype], logits.data_ptr(), _rows("logits", logits),
-        bias.data_ptr() if bias is not None else None, ctypes.byref(how), at, at + step, at + 4 * step, at + 2 * step,
-        at + 3 * step, _stream(torch, stream, logits.device)))
+    device, i32, empty = logits.device, torch.int32, torch.empty
     shape = (tokens, top_k)
-    return Routing(indices.view(shape), weights.view(torch.float32).view(shape), offsets, order, slots.view(shape))
+    indices, slots = empty(shape, dtype=i32, device=device), empty(shape, dtype=i32, device=device)
+    weights = empty(shape, dtype=torch.float32, device=device)
+    order = empty(tokens * top_k, dtype=i32, device=device)
+    offsets = empty(experts + 1, dtype=i32, device=device)
+    rc = lib.gemm_route(tokens, experts, kind, logits.data_ptr(), _rows("logits", logits, tokens, experts),
+                        bias.data_ptr() if bias is not None else None, how, indices.data_ptr(), weights.data_ptr(),
+                        offsets.data_ptr(), order.data_ptr(), slots.data_ptr(), raw(index) if stream is None else stream)
+    if rc:
+        _fail(tg, rc)
+    return Routing(indices, weights, offsets, order, slots)
 
 
 def route_backward(grad_weights, logits, indices, score="softmax", renormalize=True, scale=1.0, stream=None):
@@ -365,22 +402,24 @@ def route_backward(grad_weights, logits, indices, score="softmax", renormalize=T
     grad_weights: (T, top_k) float32; logits, score, renormalize and scale as
     given to route; indices as it returned them.
     """
-    torch, tg, types, _, _ = _tables()
-    if logits.dim() != 2 or logits.dtype not in types:
+    torch, tg, lib, types, _, _, raw = _tables()
+    kind = types.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
         raise TypeError("logits must be a (tokens, experts) float32, bfloat16 or float16 tensor")
     if indices.dim() != 2:
         raise ValueError("indices must be (tokens, top_k)")
     tokens, experts = logits.shape
-    top_k = indices.shape[1]
-    _cuda(logits, indices, grad_weights)
-    _dense("indices", indices, (tokens, top_k), torch.int32)
-    _dense("grad_weights", grad_weights, (tokens, top_k), torch.float32)
-    how = _how(top_k, score, 1, 1, "max", renormalize, scale)
+    shape = (tokens, indices.shape[1])
+    index = _cuda(logits, indices, grad_weights)
+    _dense("indices", indices, shape, torch.int32)
+    _dense("grad_weights", grad_weights, shape, torch.float32)
     out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-    _done(tg, tg.load_library().gemm_route_backward(
-        tokens, experts, types[logits.dtype], logits.data_ptr(), _rows("logits", logits), ctypes.byref(how),
-        indices.data_ptr(), grad_weights.data_ptr(), out.data_ptr(), max(experts, 1),
-        _stream(torch, stream, logits.device)))
+    rc = lib.gemm_route_backward(tokens, experts, kind, logits.data_ptr(), _rows("logits", logits, tokens, experts),
+                                 _how(shape[1], score, 1, 1, "max", renormalize, scale), indices.data_ptr(),
+                                 grad_weights.data_ptr(), out.data_ptr(), experts or 1,
+                                 raw(index) if stream is None else stream)
+    if rc:
+        _fail(tg, rc)
     return out
 
 
@@ -391,25 +430,31 @@ def combine(Y, slots, weights: Optional["torch.Tensor"] = None, out=None, stream
     outside [0, R) add nothing; weights: (T, top_k) float32, or None for ones
     (the gradient of quantize_block's scatter of each token to its rows).
     """
-    torch, tg, types, _, _ = _tables()
-    if Y.dim() != 2 or Y.dtype not in types:
+    torch, tg, lib, types, _, _, raw = _tables()
+    kind = types.get(Y.dtype)
+    if kind is None or Y.dim() != 2:
         raise TypeError("Y must be a 2-D float32, bfloat16 or float16 tensor")
     if slots.dim() != 2:
         raise ValueError("slots must be (tokens, top_k)")
-    tokens, top_k = slots.shape
+    shape = slots.shape
+    tokens, top_k = shape
     rows, hidden = Y.shape
-    _cuda(Y, slots, weights, out)
-    _dense("slots", slots, (tokens, top_k), torch.int32)
+    index = _cuda(Y, slots, weights, out)
+    _dense("slots", slots, shape, torch.int32)
     if weights is not None:
-        _dense("weights", weights, (tokens, top_k), torch.float32)
+        _dense("weights", weights, shape, torch.float32)
     if out is None:
         out = torch.empty((tokens, hidden), dtype=Y.dtype, device=Y.device)
-    elif out.dtype != Y.dtype or tuple(out.shape) != (tokens, hidden):
+        ldo = hidden or 1
+    elif out.dtype is not Y.dtype or out.shape != (tokens, hidden):
         raise TypeError(f"out must be a ({tokens}, {hidden}) {Y.dtype} tensor")
-    _done(tg, tg.load_library().gemm_combine(
-        tokens, top_k, hidden, rows, types[Y.dtype], Y.data_ptr(), _rows("Y", Y), slots.data_ptr(),
-        weights.data_ptr() if weights is not None else None, out.data_ptr(), _rows("out", out),
-        _stream(torch, stream, Y.device)))
+    else:
+        ldo = _rows("out", out, tokens, hidden)
+    rc = lib.gemm_combine(tokens, top_k, hidden, rows, kind, Y.data_ptr(), _rows("Y", Y, rows, hidden),
+                          slots.data_ptr(), weights.data_ptr() if weights is not None else None, out.data_ptr(), ldo,
+                          raw(index) if stream is None else stream)
+    if rc:
+        _fail(tg, rc)
     return out
 
 
@@ -421,33 +466,36 @@ def combine_backward(grad, Y, slots, weights, order=None, stream=None):
     get a zero gradient.  Without it rows that no slot names are zeroed too (by
     an extra pass over dY).  The entries of slots are distinct.
     """
-    torch, tg, types, _, _ = _tables()
-    if Y.dim() != 2 or Y.dtype not in types or grad.dtype != Y.dtype:
+    torch, tg, lib, types, _, _, raw = _tables()
+    kind = types.get(Y.dtype)
+    if kind is None or Y.dim() != 2 or grad.dtype is not Y.dtype:
         raise TypeError("grad and Y must be 2-D tensors of one type: float32, bfloat16 or float16")
     if slots.dim() != 2:
         raise ValueError("slots must be (tokens, top_k)")
-    tokens, top_k = slots.shape
+    shape = slots.shape
+    tokens, top_k = shape
     rows, hidden = Y.shape
-    if tuple(grad.shape) != (tokens, hidden):
+    if grad.shape != (tokens, hidden):
         raise ValueError(f"grad must be ({tokens}, {hidden})")
-    _cuda(Y, grad, slots, weights, order)
-    _dense("slots", slots, (tokens, top_k), torch.int32)
-    _dense("weights", weights, (tokens, top_k), torch.float32)
+    index = _cuda(Y, grad, slots, weights, order)
+    _dense("slots", slots, shape, torch.int32)
+    _dense("weights", weights, shape, torch.float32)
     if order is not None:
         _dense("order", order, (tokens * top_k,), torch.int32)
         if rows != tokens * top_k:
             raise ValueError("order goes with tokens * top_k rows")
-    s = _stream(torch, stream, Y.device)
     if order is not None:
         dY = torch.empty((rows, hidden), dtype=Y.dtype, device=Y.device)
     elif stream is None:
         dY = torch.zeros((rows, hidden), dtype=Y.dtype, device=Y.device)
     else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(s, device=Y.device)):
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=Y.device)):
             dY = torch.zeros((rows, hidden), dtype=Y.dtype, device=Y.device)
-    dw = torch.empty((tokens, top_k), dtype=torch.float32, device=Y.device)
-    _done(tg, tg.load_library().gemm_combine_backward(
-        tokens, top_k, hidden, rows, types[Y.dtype], grad.data_ptr(), _rows("grad", grad), Y.data_ptr(), _rows("Y", Y),
-        slots.data_ptr(), weights.data_ptr(), order.data_ptr() if order is not None else None, dY.data_ptr(),
-        max(hidden, 1), dw.data_ptr(), s))
+    dw = torch.empty(shape, dtype=torch.float32, device=Y.device)
+    rc = lib.gemm_combine_backward(tokens, top_k, hidden, rows, kind, grad.data_ptr(),
+                                   _rows("grad", grad, tokens, hidden), Y.data_ptr(), _rows("Y", Y, rows, hidden),
+                                   slots.data_ptr(), weights.data_ptr(), order.data_ptr() if order is not None else None,
+                                   dY.data_ptr(), hidden or 1, dw.data_ptr(), raw(index) if stream is None else stream)
+    if rc:
+        _fail(tg, rc)
     return dY, dw
