@@ -24,6 +24,34 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
             : "memory");
 }
 
+// D[tmem] (+)= P Q^T, FP8 operands in shared memory under the 128-byte swizzle
+// with 8-row groups 1024 bytes apart.  pd, qd: the low words of the descriptors
+// (start address and leading offset in 16-byte units); the high word (stride
+// 1024, version 1, layout 2 as sdesc_sw128 builds it) is the same for both.
+template <int CG>
+__device__ __forceinline__ void mma_f8_sw128(uint32_t d_tmem, uint32_t pd, uint32_t qd, uint32_t idesc, uint32_t acc) {
+    constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | ((uint32_t)kLayoutSw128 << 29);
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}"
+            ::"r"(d_tmem), "r"(pd), "r"(qd), "r"(kHigh), "r"(idesc), "r"(acc) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, p;\n\t}"
+            ::"r"(d_tmem), "r"(pd), "r"(qd), "r"(kHigh), "r"(idesc), "r"(acc) : "memory");
+}
+
+// 2^x to about 2^-22 relative; 0 for x below -126.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;

@@ -23,7 +23,8 @@
 // shared memory; the other warps hold the sums, one lane a thread, and write C.
 // Both operands are read in either major: K-major as rows of 128 bytes, or
 // MN-major in chunks of 128 rows of K by 128 bytes (as tc_gemm.cu reads B).
-// Every wait is bounded as there.
+// Every wait is bounded (a time limit, and a flag that any role raises when it
+// gives up); a role that gives up waits, again bounded, for what it started.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -49,6 +50,7 @@ constexpr int kCtrlBytes = 1024;       // barriers and flags
 constexpr int kMaxExperts = 1024;
 constexpr int kGroup = 4;              // K-blocks whose scales come together
 constexpr int kSlots = 2;
+constexpr int kBoxBytes = 4096;        // 32 rows x 128 bytes of C
 
 enum Role : uint32_t { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleDrain = 4, kRoleScales = 5 };
 
@@ -93,7 +95,7 @@ struct Cfg {
     static constexpr int NBUF = BN >= 256 ? 2 : 4;
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr bool SWAPPED = BN < 128;          // the tiles of few tokens
-    static constexpr int OUT_BYTES = SWAPPED ? 2048 : 4096;           // a warp's staging for C
+    static constexpr int OUT_BYTES = SWAPPED ? 2048 : 2 * kBoxBytes;  // a warp's staging for C
     // Scales come four K-blocks at a time, in two slots of shared memory: for
     // each K-block the lanes' 128 and the columns' BN, or, with one scale for 128
     // columns, the lanes' times each 128 columns' one.
@@ -120,17 +122,29 @@ __device__ __noinline__ void record_failure(uint32_t role, int tile, volatile in
     }
 }
 
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                         unsigned long long timeout_ns) {
-    if (ptx::mbar_try_wait<false>(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer_ns();
-    for (;;) {
+// What bounds every wait of a CTA.
+struct Bounds {
+    volatile int *abort_flag;
+    unsigned long long timeout_ns;
+};
+
+// A whole warp waits for a phase of a barrier (each try already waits a while).
+// False once the time is up or another role has given up.  Kept short, for the
+// loops around it have to stay in the instruction caches, and inline, for a call
+// would have the epilogue warps put their sums away.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Bounds &b, uint32_t role, int tile) {
+    uint64_t t0 = 0;
 #pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (ptx::mbar_try_wait<false>(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (ptx::globaltimer_ns() - t0 > timeout_ns) return false;
+    while (!__all_sync(0xffffffffu, ptx::mbar_try_wait<false>(bar, parity))) {
+        const uint64_t now = ptx::globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, now - t0 > b.timeout_ns || *b.abort_flag != 0)) {
+            if ((threadIdx.x & 31) == 0) record_failure(role, tile, b.abort_flag);
+            __syncwarp();
+            return false;
+        }
     }
+    return true;
 }
 
 // The wait of a role that has given up, for what it started itself.
@@ -246,7 +260,7 @@ template <int COUNT, bool BY>
 __device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int end, int e, const ScaleView &by,
                                              int by_row, int by_end, int by_e, int kb0, int kb1, int t, Ring &sl,
                                              uint8_t *slots, int slot_bytes, int kb_floats, uint32_t scf0, uint32_t sce0,
-                                             volatile int *abort_flag, unsigned long long timeout_ns) {
+                                             const Bounds &bounds) {
     constexpr int PER = (COUNT + 31) / 32;
     const int lane = threadIdx.x & 31;
     constexpr bool kAhead = PER <= 4;
@@ -270,11 +284,7 @@ __device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int e
 #pragma unroll
             for (int c = 0; c < PER; ++c) cur[a][c] = nxt[a][c];
         if (kAhead) load(kb + kGroup);
-        const bool got = wait_bar(sce0 + 8u * (uint32_t)sl.i, sl.phase ^ 1u, abort_flag, timeout_ns);
-        if (!__all_sync(0xffffffffu, got)) {
-            if (lane == 0) record_failure(kRoleScales, t, abort_flag);
-            return false;
-        }
+        if (!wait_warp(sce0 + 8u * (uint32_t)sl.i, sl.phase ^ 1u, bounds, kRoleScales, t)) return false;
         float *slot = reinterpret_cast<float *>(slots + sl.i * slot_bytes);
 #pragma unroll
         for (int a = 0; a < kGroup; ++a)
@@ -288,12 +298,50 @@ __device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int e
     return true;
 }
 
+// x * Phi(x), two values at a time.  Phi(-a) = 2^-P(a) for a = |x| >= 0, P a
+// polynomial of degree 8 fitted to -log2 Phi(-a) on [0, 5.5] (least squares in
+// the Chebyshev basis, reweighted towards the largest error in Phi; 4e-8 in FP32
+// arithmetic, where erf's own rounding leaves 6e-8) and above 25 beyond, where
+// Phi(-a) no longer counts.  One exponential and eight paired multiply-adds,
+// where erff takes about thirty instructions.
+__device__ __forceinline__ float2 gelu2(float2 x) {
+    const float2 a = make_float2(fabsf(x.x), fabsf(x.y));
+    auto both = [](float c) { return make_float2(c, c); };
+    float2 r = both(-2.7720716e-06f);                       // -P
+    r = __ffma2_rn(r, a, both(3.8620983e-05f));
+    r = __ffma2_rn(r, a, both(-1.8254861e-04f));
+    r = __ffma2_rn(r, a, both(-1.4586786e-04f));
+    r = __ffma2_rn(r, a, both(7.0754690e-03f));
+    r = __ffma2_rn(r, a, both(-5.2505028e-02f));
+    r = __ffma2_rn(r, a, both(-4.5920491e-01f));
+    r = __ffma2_rn(r, a, both(-1.1511058e+00f));
+    r = __ffma2_rn(r, a, both(-1.0f));
+    const float hx = ptx::exp2_approx(r.x), hy = ptx::exp2_approx(r.y);
+    return make_float2(x.x * (x.x > 0.f ? 1.f - hx : hx), x.y * (x.y > 0.f ? 1.f - hy : hy));
+}
+
+// The epilogue's value from a whole sum (old: the element of C before, if beta).
+__device__ __forceinline__ float finish(const EpiParams &e, float acc, float old, float bias) {
+    float y = e.alpha * acc;
+    if (e.beta != 0.f) y = fmaf(e.beta, old, y);
+    y += bias;
+    if (e.act == GEMM_ACT_RELU) y = fmaxf(y, 0.f);
+    else if (e.act == GEMM_ACT_GELU) y = gelu2(make_float2(y, y)).x;
+    return y;
+}
+
 // C's element (row i of D, column j) from its whole sum.
 __device__ __forceinline__ void write_one(const ScaledParams &p, const Tile &T, int row, int col, float v) {
     const int64_t i = (int64_t)T.i0 + row, j = (int64_t)T.j0 + col;
     if (i >= T.i1 || j >= T.j1) return;
     const int64_t n = p.swapped ? i : j;
-    epi_write(p.epi, p.C, p.swapped ? j * p.ldc + i : i * p.ldc + j, v, epi_bias(p.epi, n, n + 1));
+    const int64_t at = p.swapped ? j * p.ldc + i : i * p.ldc + j;
+    if (!p.epi.active) {
+        static_cast<float *>(p.C)[at] = v;
+        return;
+    }
+    const float old = p.epi.beta != 0.f ? epi_load_old(p.C, at, p.epi.out) : 0.f;
+    epi_store(p.C, at, p.epi.out, finish(p.epi, v, old, epi_bias(p.epi, n, n + 1)));
 }
 
 // Writes four neighbouring columns of a row of C, [cr][cc .. cc + 4), where they
@@ -311,7 +359,7 @@ __device__ __forceinline__ void write_four(const ScaledParams &p, int64_t cr, in
                 if (cc + k < c_end) old[k] = epi_load_old(p.C, at + k, p.epi.out);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = epi_value(p.epi, y[k], old[k], bias[k]);
+        for (int k = 0; k < 4; ++k) y[k] = finish(p.epi, y[k], old[k], bias[k]);
     }
     if (whole && p.epi.active && p.epi.out != GEMM_OUT_F32) {
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
@@ -359,13 +407,13 @@ __device__ __forceinline__ void write_swapped(const ScaledParams &p, const Tile 
 // A warp's 32 rows x COLS columns of D as rows of C, one row a thread: 32
 // columns at a time through the epilogue in registers (its code is there once;
 // the sums move down), rounded, and into a box of 32 rows x 128 bytes of shared
-// memory with TMA's 128-byte swizzle.  A full box leaves by a TMA store where
+// memory with TMA's 128-byte swizzle, two boxes in turn.  A full box leaves by a TMA store where
 // C's layout allows it and the rows are all this tile's (an expert's last tile
 // ends inside one), else row by row with neighbouring lanes on neighbouring
 // columns.
 template <int COLS>
 __device__ __forceinline__ void write_rows(const ScaledParams &p, const CUtensorMap *tmC, const Tile &T, int row0,
-                                           int col0, float (&acc)[COLS], uint32_t buf, int lane) {
+                                           int col0, float (&acc)[COLS], uint32_t bufs, int &box, int lane) {
     const bool active = p.epi.active != 0;
     const bool half = active && p.epi.out != GEMM_OUT_F32;
     const int64_t i0 = (int64_t)T.i0 + row0, i = i0 + lane;
@@ -394,15 +442,21 @@ __device__ __forceinline__ void write_rows(const ScaledParams &p, const CUtensor
                 for (int c = 0; c < 32; ++c) acc[c] = fmaxf(acc[c], 0.f);
             } else if (p.epi.act == GEMM_ACT_GELU) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) acc[c] = 0.5f * acc[c] * (1.f + erff(acc[c] * 0.70710678118654752f));
+                for (int c = 0; c < 32; c += 2) {
+                    const float2 g = gelu2(make_float2(acc[c], acc[c + 1]));
+                    acc[c] = g.x;
+                    acc[c + 1] = g.y;
+                }
             }
         }
-        // the box's first half: the store of the one before must have read it
+        // a new box, in the buffer of the one before last, which its store must have read
         const bool first = !half || (c0 & 32) == 0;
         if (first) {
-            if (lane == 0) ptx::bulk_wait_group_read<0>();
+            ++box;
+            if (lane == 0) ptx::bulk_wait_group_read<1>();
             __syncwarp();
         }
+        const uint32_t buf = bufs + (uint32_t)((box & 1) * kBoxBytes);
         const uint32_t row = buf + 128u * (uint32_t)lane;
         if (half) {
 #pragma unroll
@@ -472,6 +526,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     constexpr int kBars = 2 * Cf::STAGES + Cf::NBUF + 2 * kSlots;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const Bounds bounds = {abort_flag, p.timeout_ns};
 
     const uint32_t bar0 = ptx::smem_addr(bars);
     auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
@@ -479,7 +534,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     auto acce = [&](int b) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + b); };
     auto scf = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + s); };
     auto sce = [&](int s) { return bar0 + 8u * (uint32_t)(2 * Cf::STAGES + Cf::NBUF + kSlots + s); };
-    const uint32_t scales0 = ptx::smem_addr(scales), out0 = ptx::smem_addr(out_bufs), scf0 = scf(0), sce0 = sce(0);
+    const uint32_t ring0 = ptx::smem_addr(ring), scales0 = ptx::smem_addr(scales), out0 = ptx::smem_addr(out_bufs), scf0 = scf(0), sce0 = sce(0);
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = !kPair && p.splits > 1 ? ptx::cluster_ctarank() : 0u;   // its K range
@@ -557,31 +612,30 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     const int kb0 = (int)crank * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
 
     // 128 columns a thread need more than the launch's 168 registers: the first
-    // warpgroup gives the difference (128 x 56 + 256 x 224 = 384 x 168, or with a
-    // scale per column, 256 of which a warp brings, 128 x 72 + 256 x 216).
+    // warpgroup gives the difference (128 x 72 + 256 x 216 = 384 x 168; with
+    // 56 and 224 the scale warps spill, 2% slower at 8192^3).
     if (warp < 4) {
-        if (Cf::SPLIT_REGS) ptx::regs_give_back<QVEC ? 72 : 56>();
+        if (Cf::SPLIT_REGS) ptx::regs_give_back<72>();
         if (warp == 0) {
             // ------------------------------------------------------ TMA producer
-            if (lane == 0) {
-                Ring rg;
-                bool ok = true, laps = false;      // laps: the ring has been round once
-                for (int t = unit; ok && t < num_tiles; t += units) {
-                    const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
-                    const int ep = p.tokens_on_i ? 0 : T.e, eq = p.tokens_on_i ? T.e : 0;
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!wait_bar(done(rg.i), rg.phase ^ 1u, abort_flag, p.timeout_ns)) {
-                            record_failure(kRoleProducer, t, abort_flag);
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t fb = full(rg.i), sp = ptx::smem_addr(ring + rg.i * Cf::STAGE),
-                                       sq = sp + Cf::P_BYTES;
+            // (the whole warp, one elected thread issuing, as the MMA warp)
+            Ring rg;
+            bool ok = true, laps = false;      // laps: the ring has been round once
+            for (int t = unit; ok && t < num_tiles; t += units) {
+                const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
+                const int ep = p.tokens_on_i ? 0 : T.e, eq = p.tokens_on_i ? T.e : 0;
+                const int i0 = T.i0 + (int)rank * kLanes, j0 = T.j0 + (int)rank * (BN / CG);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!wait_warp(done(rg.i), rg.phase ^ 1u, bounds, kRoleProducer, t)) {
+                        ok = false;
+                        break;
+                    }
+                    if (ptx::elect_one()) {
+                        const uint32_t fb = full(rg.i), sp = ring0 + (uint32_t)(rg.i * Cf::STAGE), sq = sp + Cf::P_BYTES;
                         if (rank == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)(Cf::STAGE * CG));
-                        const int k0 = kb * kBlockK, i0 = T.i0 + (int)rank * kLanes, j0 = T.j0 + (int)rank * (BN / CG);
+                        const int k0 = kb * kBlockK;
                         const uint32_t to = kPair ? ptx::mapa_shared(fb, 0) : fb;     // a pair's bytes count in the leader
-                        if (p.p_mn) ptx::tma_load_3d<CG>(sp, &tmP, to, i0, k0, ep);
-                        else ptx::tma_load_3d<CG>(sp, &tmP, to, k0, i0, ep);
+                        ptx::tma_load_3d<CG>(sp, &tmP, to, p.p_mn ? i0 : k0, p.p_mn ? k0 : i0, ep);
                         if (p.q_mn) {
 #pragma unroll
                             for (int c = 0; c < (BN / CG + 127) / 128; ++c)
@@ -589,26 +643,24 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                         } else {
                             ptx::tma_load_3d<CG>(sq, &tmQ, to, k0, j0, eq);
                         }
-                        rg.next(Cf::STAGES);
-                        laps = laps || rg.i == 0;
                     }
-                }
-                // Until the MMAs have released every slot no read of this shared
-                // memory and no arrival on its barriers is outstanding.
-                const Ring last = rg;
-                for (int i = 0; ok && i < Cf::STAGES; ++i) {
-                    if (!wait_bar(done(rg.i), rg.phase ^ 1u, abort_flag, p.timeout_ns)) {
-                        record_failure(kRoleDrain, -1, abort_flag);
-                        ok = false;
-                        break;
-                    }
+                    __syncwarp();
                     rg.next(Cf::STAGES);
+                    laps = laps || rg.i == 0;
                 }
-                // Given up: the copies already issued still land in this shared memory.
-                for (int i = 0; !ok && rank == 0 && i < Cf::STAGES; ++i) {
-                    const uint32_t parity = i < last.i ? last.phase : last.phase ^ 1u;
-                    if (laps || i < last.i) wait_landed(full(i), parity, p.timeout_ns);   // (of a pair: in the leader)
-                }
+            }
+            // Until the MMAs have released every slot no read of this shared
+            // memory and no arrival on its barriers is outstanding.
+            const Ring last = rg;
+            for (int i = 0; ok && i < Cf::STAGES; ++i) {
+                ok = wait_warp(done(rg.i), rg.phase ^ 1u, bounds, kRoleDrain, -1);
+                rg.next(Cf::STAGES);
+            }
+            // Given up: the copies already issued still land in this shared memory
+            // (those of a pair are counted in the leader).
+            for (int i = 0; !ok && rank == 0 && i < Cf::STAGES; ++i) {
+                const uint32_t parity = i < last.i ? last.phase : last.phase ^ 1u;
+                if (laps || i < last.i) wait_landed(full(i), parity, p.timeout_ns);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -622,30 +674,27 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 Ring rg, buf;
                 bool ok = true;
                 uint32_t last_bar = 0, last_parity = 0;      // of the MMAs issued last
+                // descriptors in 16-byte units: leading offset, and one MMA's step along K
+                const uint32_t p_lead = (p.p_mn ? 1024u : 1u) << 16, q_lead = (p.q_mn ? 1024u : 1u) << 16;
+                const uint32_t p_step = p.p_mn ? 256u : 2u, q_step = p.q_mn ? 256u : 2u;
                 for (int t = unit; ok && t < num_tiles; t += units) {
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        // (the operands first: the accumulator is what comes last)
-                        const bool got = wait_bar(full(rg.i), rg.phase, abort_flag, p.timeout_ns) &&
-                                         wait_bar(acce(buf.i), buf.phase ^ 1u, abort_flag, p.timeout_ns);
-                        if (!__all_sync(0xffffffffu, got)) {
-                            if (lane == 0) record_failure(kRoleMma, t, abort_flag);
+                        if (!wait_warp(full(rg.i), rg.phase, bounds, kRoleMma, t) ||
+                            !wait_warp(acce(buf.i), buf.phase ^ 1u, bounds, kRoleMma, t)) {
                             ok = false;
                             break;
                         }
                         ptx::tc_fence_after();
-                        const uint32_t sp = ptx::smem_addr(ring + rg.i * Cf::STAGE), sq = sp + Cf::P_BYTES;
-                        // K-major: K advances 32 bytes inside a 128-byte row, 8-row
-                        // groups 1024 bytes apart.  MN-major: 32 rows of K further,
-                        // 128-byte chunks 16 KB apart, 8-row groups 1024.
-                        const uint64_t pd = ptx::sdesc_sw128(sp, p.p_mn ? 16384u : 16u, 1024u);
-                        const uint64_t qd = ptx::sdesc_sw128(sq, p.q_mn ? 16384u : 16u, 1024u);
-                        const uint32_t p_step = p.p_mn ? 4096u / 16u : 32u / 16u, q_step = p.q_mn ? 4096u / 16u : 32u / 16u;
-                        const uint32_t d = tmem + (uint32_t)(buf.i * BN);
                         if (ptx::elect_one()) {
+                            // K-major: K advances 32 bytes inside a 128-byte row, 8-row
+                            // groups 1024 bytes apart.  MN-major: 32 rows of K further,
+                            // 128-byte chunks 16 KB apart, 8-row groups 1024.
+                            const uint32_t sp = ring0 + (uint32_t)(rg.i * Cf::STAGE);
+                            const uint32_t pd = (sp >> 4) | p_lead, qd = ((sp + Cf::P_BYTES) >> 4) | q_lead;
+                            const uint32_t d = tmem + (uint32_t)(buf.i * BN);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                ptx::mma<CG, ptx::kKindF8>(d, pd + (uint64_t)(p_step * kk), qd + (uint64_t)(q_step * kk),
-                                                           p.idesc, kk != 0 ? 1u : 0u);
+                                ptx::mma_f8_sw128<CG>(d, pd + p_step * kk, qd + q_step * kk, p.idesc, kk != 0 ? 1u : 0u);
                             if (kPair) ptx::mma_commit_pair(done(rg.i), 0x3);
                             else ptx::mma_commit(done(rg.i));
                         }
@@ -670,34 +719,34 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 const int i0 = T.i0 + (int)rank * kLanes;
                 if (QVEC && !first_warp)
                     ok = bring_scales<BN, false>(p.sq, T.j0, T.j1, eq, p.sq, 0, 1, 0, kb0, kb1, t, sl,
-                                                 scales + kLanes * 4, Cf::SLOT_BYTES, Cf::SCALES, scf0, sce0, abort_flag,
-                                                 p.timeout_ns);
+                                                 scales + kLanes * 4, Cf::SLOT_BYTES, Cf::SCALES, scf0, sce0, bounds);
                 else
                     ok = bring_scales<kLanes, !QVEC>(p.sp, i0, T.i1, ep, p.sq, T.j0 + (first_warp ? 0 : 128), T.j1, eq, kb0,
                                                      kb1, t, sl, scales + (first_warp ? 0 : kLanes * 4), Cf::SLOT_BYTES,
-                                                     Cf::SCALES, scf0, sce0, abort_flag, p.timeout_ns);
+                                                     Cf::SCALES, scf0, sce0, bounds);
             }
         }
     } else {
-        if (Cf::SPLIT_REGS) ptx::regs_take<QVEC ? 216 : 224>();
+        if (Cf::SPLIT_REGS) ptx::regs_take<216>();
         // ------------------------------------------------- sums and epilogue
         const uint32_t quarter = warp & 3, half = (warp - 4) >> 2;     // lanes it may read; its columns
         const int row = (int)(quarter * 32 + lane), col0 = (int)half * Cf::COLS;   // of this CTA's 128
         const uint32_t tbase = tmem + (quarter << 21) + (uint32_t)col0;   // lane field: quarter * 32 << 16
         Ring rg, buf, sl;
+        int box = 0;                                                   // of C, written so far
         bool ok = true;
         for (int t = unit; ok && t < num_tiles; t += units) {
-            const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
             float acc[Cf::COLS];
 #pragma unroll
             for (int c = 0; c < Cf::COLS; ++c) acc[c] = 0.f;
             // The next K-blocks' scales, and whether the next one's MMAs have
-            // completed, are looked up while this one's last columns are on their way.
+            // completed, are looked up between handing the accumulator back and
+            // adding the last columns.
             float sv[kGroup];
             uint32_t columns = 0;          // (a scale per column) the K-block's, in shared memory
-            bool got = true, ready = false;
+            bool ready = false;
             auto next_group = [&]() {
-                got = wait_bar(scf(sl.i), sl.phase, abort_flag, p.timeout_ns);
+                ok = wait_warp(scf(sl.i), sl.phase, bounds, kRoleEpilogue, t) && ok;
                 const uint32_t slot = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES) +
                                       4u * (uint32_t)(row + (QVEC ? 0 : (col0 >> 7) * kLanes));
 #pragma unroll
@@ -710,12 +759,9 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             };
             if (kb0 < kb1) next_group();
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!ready) got = wait_bar(done(rg.i), rg.phase, abort_flag, p.timeout_ns) && got;
-                if (!__all_sync(0xffffffffu, got)) {
-                    if (lane == 0) record_failure(kRoleEpilogue, t, abort_flag);
-                    ok = false;
-                    break;
-                }
+                if (!__all_sync(0xffffffffu, ready)) ok = wait_warp(done(rg.i), rg.phase, bounds, kRoleEpilogue, t) && ok;
+                ready = false;
+                if (!ok) break;
                 ptx::tc_fence_after();
                 const uint32_t src = tbase + (uint32_t)(buf.i * BN), acce_now = acce(buf.i);
                 const int in = (kb - kb0) % kGroup;
@@ -743,13 +789,6 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                         ptx::tmem_load(src, r[0]);
                         if (kChunks > 1) ptx::tmem_load(src + (uint32_t)Cf::CHUNK, r[1]);
                     }
-                    if (c + 2 >= kChunks && kb + 1 < kb1) {
-                        if (!QVEC && group_ends) {
-                            release_group();
-                            next_group();
-                        }
-                        ready = ptx::mbar_test(done(rg.i), rg.phase);
-                    }
                     ptx::tmem_wait(r[0]);
                     if (kChunks > 1) ptx::tmem_wait(r[1]);
                     if (c + 2 >= kChunks) {
@@ -759,6 +798,13 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                         if (lane == 0) {
                             if (kPair) ptx::mbar_arrive_peer(ptx::mapa_shared(acce_now, 0));
                             else ptx::mbar_arrive(acce_now);
+                        }
+                        if (kb + 1 < kb1) {
+                            ready = ptx::mbar_test(done(rg.i), rg.phase);
+                            if (!QVEC && group_ends) {
+                                release_group();
+                                next_group();
+                            }
                         }
                     }
                     add(c);
@@ -780,11 +826,12 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 for (int c = 0; c < Cf::COLS; ++c) part[(col0 + c) * kLanes + row] = acc[c];
                 break;                                   // one tile a cluster
             }
+            const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
             const uint32_t out_buf = out0 + (warp - 4) * (uint32_t)Cf::OUT_BYTES;
             if constexpr (Cf::SWAPPED)
                 write_swapped<Cf::COLS>(p, T, (int)(quarter * 32), col0, acc, out_buf, (int)lane);
             else
-                write_rows<Cf::COLS>(p, &tmC, T, (int)(quarter * 32 + rank * kLanes), col0, acc, out_buf, (int)lane);
+                write_rows<Cf::COLS>(p, &tmC, T, (int)(quarter * 32 + rank * kLanes), col0, acc, out_buf, box, (int)lane);
         }
     }
 
