@@ -1,7 +1,37 @@
 // Argument checks shared by the expert-layer operators' C entries.
 #include "ops.h"
 
+#include <mutex>
+
 namespace tcgemm {
+
+cudaError_t op_malloc(void **p, size_t bytes, int dev, cudaStream_t stream) {
+    static std::mutex mu;
+    static cudaMemPool_t pools[64];
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaMemPool_t pool;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!pools[dev]) {
+            cudaMemPoolProps props = {};
+            props.allocType = cudaMemAllocationTypePinned;
+            props.location.type = cudaMemLocationTypeDevice;
+            props.location.id = dev;
+            cudaMemPool_t made = nullptr;
+            cudaError_t e = cudaMemPoolCreate(&made, &props);
+            if (e != cudaSuccess) return e;
+            uint64_t keep = 256ull << 20;
+            e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
+            if (e != cudaSuccess) {
+                cudaMemPoolDestroy(made);
+                return e;
+            }
+            pools[dev] = made;
+        }
+        pool = pools[dev];
+    }
+    return cudaMallocFromPoolAsync(p, bytes, pool, stream);
+}
 
 int op_check(const OpSpan *spans, int count, int *sms) {
     char msg[256];

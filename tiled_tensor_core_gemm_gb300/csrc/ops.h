@@ -35,6 +35,12 @@ inline uint64_t op_extent(int64_t rows, int64_t cols, int64_t ld, int elem) {
 // that every span is its memory.  Returns a gemm_status_t; *sms as asked.
 int op_check(const OpSpan *spans, int count, int *sms);
 
+// Workspace on `stream` (cudaFreeAsync returns it), from a pool of the library's
+// own that keeps up to 256 MiB over a synchronisation: the default pool gives
+// its memory back there, and the next call then waits for the driver (200 us
+// and more for a workspace of a megabyte).
+cudaError_t op_malloc(void **p, size_t bytes, int dev, cudaStream_t stream);
+
 inline int op_type_bytes(int type) { return type == GEMM_OUT_F32 ? 4 : 2; }
 inline bool op_type_ok(int type) { return type == GEMM_OUT_F32 || type == GEMM_OUT_BF16 || type == GEMM_OUT_F16; }
 inline int op_launched(const char *what, cudaError_t e) {

@@ -633,7 +633,9 @@ int gemm_route(int64_t tokens, int64_t experts, int type, const void *logits, in
     void *ws = nullptr;
     if (ordered) {
         const size_t bytes = ((size_t)p.experts * p.blocks + p.experts) * 4;
-        const cudaError_t e = cudaMallocAsync(&ws, bytes, stream);
+        int dev = 0;
+        cudaGetDevice(&dev);
+        const cudaError_t e = op_malloc(&ws, bytes, dev, stream);
         if (e != cudaSuccess) {
             cudaGetLastError();
             char msg[128];

@@ -109,7 +109,7 @@ struct Cfg {
     static_assert(!SPLIT_REGS || THREADS == 384, "the register split is written for 384 threads");
     static_assert(STAGES >= 3 && SMEM <= kSmemMax, "ring");
     static_assert((2 * STAGES + NBUF + 2 * kSlots) * 8 + 16 <= kCtrlBytes, "barrier area");
-    static_assert(CG == 2 || kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
+    static_assert(!SWAPPED || kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
 };
 
 __device__ __noinline__ void record_failure(uint32_t role, int tile, volatile int *abort_flag) {
@@ -330,20 +330,6 @@ __device__ __forceinline__ float finish(const EpiParams &e, float acc, float old
     return y;
 }
 
-// C's element (row i of D, column j) from its whole sum.
-__device__ __forceinline__ void write_one(const ScaledParams &p, const Tile &T, int row, int col, float v) {
-    const int64_t i = (int64_t)T.i0 + row, j = (int64_t)T.j0 + col;
-    if (i >= T.i1 || j >= T.j1) return;
-    const int64_t n = p.swapped ? i : j;
-    const int64_t at = p.swapped ? j * p.ldc + i : i * p.ldc + j;
-    if (!p.epi.active) {
-        static_cast<float *>(p.C)[at] = v;
-        return;
-    }
-    const float old = p.epi.beta != 0.f ? epi_load_old(p.C, at, p.epi.out) : 0.f;
-    epi_store(p.C, at, p.epi.out, finish(p.epi, v, old, epi_bias(p.epi, n, n + 1)));
-}
-
 // Writes four neighbouring columns of a row of C, [cr][cc .. cc + 4), where they
 // exist.
 __device__ __forceinline__ void write_four(const ScaledParams &p, int64_t cr, int64_t cc, int64_t c_end, float4 v,
@@ -537,7 +523,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     const uint32_t ring0 = ptx::smem_addr(ring), scales0 = ptx::smem_addr(scales), out0 = ptx::smem_addr(out_bufs), scf0 = scf(0), sce0 = sce(0);
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t crank = !kPair && p.splits > 1 ? ptx::cluster_ctarank() : 0u;   // its K range
+    const uint32_t crank = Cf::SWAPPED && p.splits > 1 ? ptx::cluster_ctarank() : 0u;   // its K range
     const uint32_t rank = kPair ? ptx::cluster_ctarank() : 0u;                     // its half of the pair's tile
 
     if (threadIdx.x == 0) {
@@ -607,7 +593,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int num_tiles = p.experts ? first_tile[p.experts] : p.tiles_i * p.tiles_j;
-    const int share = kPair ? 2 : p.splits;      // CTAs of a tile
+    const int share = kPair ? 2 : Cf::SWAPPED ? p.splits : 1;      // CTAs of a tile
     const int unit = (int)blockIdx.x / share, units = (int)gridDim.x / share;
     const int kb0 = (int)crank * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
 
@@ -819,7 +805,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             }
             if (!QVEC && ok && kb0 < kb1) release_group();
             if (!ok) break;
-            if (!kPair && p.splits > 1) {
+            if (Cf::SWAPPED && p.splits > 1) {
                 // this CTA's K range of the tile, for the cluster to read: [column][lane]
                 float *part = reinterpret_cast<float *>(ring);
 #pragma unroll
@@ -838,20 +824,32 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     // Before the CTA's shared memory goes, its TMA stores must have read it.
     if (warp >= 4 && lane == 0) ptx::bulk_wait_group_read<0>();
     // K ranges: every CTA of the cluster sums its share of the columns over all
-    // of them, in their order, and writes it.
-    if (!kPair && p.splits > 1) {
+    // of them, in their order, and writes it: rows of C, four neighbouring
+    // elements a thread and step, two steps' loads in flight.
+    if (Cf::SWAPPED && p.splits > 1) {
         __syncwarp();
         ptx::cluster_sync();
         if (warp >= 4 && unit < num_tiles && *abort_flag == 0) {
             const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, unit);
-            const int row = (int)(((warp - 4) & 3) * 32 + lane);
-            const uint32_t part = ptx::smem_addr(ring);
-            const int share = BN / p.splits, c0 = (int)crank * share;
-            for (int c = c0 + (int)((warp - 4) >> 2); c < c0 + share; c += EW / 4) {
-                float v = 0.f;
-                for (int s = 0; s < p.splits; ++s)
-                    v += ptx::ld_cluster_f(ptx::mapa_shared(part + 4u * (uint32_t)(c * kLanes + row), (uint32_t)s));
-                write_one(p, T, row, c, v);
+            const int share = BN / p.splits, c0 = (int)crank * share, quads = share * (kLanes / 4);
+            constexpr int kStep = EW * 32;
+            const int64_t cc = (int64_t)T.i0 + 4 * lane;               // (a warp's lanes take a whole row of the tile)
+            float bias[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bias[k] = cc + k < T.i1 ? epi_bias(p.epi, cc + k, cc + k + 1) : 0.f;
+            for (int q = (int)threadIdx.x - 128; q < quads; q += 2 * kStep) {
+                const int c = c0 + q / 32, d = c0 + min(q + kStep, quads - 1) / 32;
+                const uint32_t at0 = ring0 + 4u * (uint32_t)(c * kLanes + 4 * (int)lane);
+                const uint32_t at1 = ring0 + 4u * (uint32_t)(d * kLanes + 4 * (int)lane);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
+                for (int s = 0; s < p.splits; ++s) {
+                    const float4 x = ptx::ld_cluster_v4f(ptx::mapa_shared(at0, (uint32_t)s));
+                    const float4 y = ptx::ld_cluster_v4f(ptx::mapa_shared(at1, (uint32_t)s));
+                    v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+                    w = make_float4(w.x + y.x, w.y + y.y, w.z + y.z, w.w + y.w);
+                }
+                if (T.j0 + c < T.j1 && cc < T.i1) write_four(p, (int64_t)T.j0 + c, cc, T.i1, v, bias);
+                if (q + kStep < quads && T.j0 + d < T.j1 && cc < T.i1) write_four(p, (int64_t)T.j0 + d, cc, T.i1, w, bias);
             }
         }
         __syncwarp();
@@ -962,7 +960,7 @@ int launch_plan(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &
     switch (pl.bn) {
         case 16: return launch<16, true, 4, 1>(pl, tp, tq, tc, p, stream);
         case 32: return launch<32, true, 4, 1>(pl, tp, tq, tc, p, stream);
-        case 64: return launch<64, true, 4, 1>(pl, tp, tq, tc, p, stream);
+        case 64: return launch<64, true, 8, 1>(pl, tp, tq, tc, p, stream);
         case 128:
             return pl.qvec ? launch<128, true, 8, 1>(pl, tp, tq, tc, p, stream)
                            : launch<128, false, 8, 1>(pl, tp, tq, tc, p, stream);
@@ -1022,28 +1020,44 @@ uint32_t idesc_of(int dtype, int bn, int cg, int p_mn, int q_mn) {
            ((uint32_t)(bn >> 3) << 17) | ((uint32_t)((kLanes * cg) >> 4) << 24);
 }
 
-// Tile shape, roles and K ranges of one product.
+// Tile shape, roles and K ranges of one product: the cheapest by a model of the
+// kernel's pace, in units of a 16-column tile's K-block (about 0.3 us):
+//   swapped tiles of 16, 32, 64 columns   1, 1.05, 1.15 a K-block
+//   128 x 128                             1.25 a K-block, 5 a tile
+//   256 x 256 on a CTA pair               1.6 a K-block, 10 a tile
+// and 8 or 9 more for K cut in 2 or 4 ranges (the cluster's exchange: measured
+// 2.4 us; 8 ranges cost 9 us and are never taken).
 ScaledPlan plan_product(int64_t M, int64_t N, int64_t num_kb, bool a_col, bool b_tile, int sms) {
-    ScaledPlan pl = {};
-    pl.cg = 1;
-    pl.splits = 1;
-    if (M <= 64 && !a_col) {
-        pl.swap = 1;
-        pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-        pl.qvec = 1;
-    } else {
-        pl.bn = 128;
-        if (cdiv(M, 256) * cdiv(N, 256) * 2 > sms / 2) {
-            pl.bn = 256;
-            pl.cg = 2;
+    ScaledPlan best = {};
+    double least = 0.;
+    auto consider = [&](int swap, int bn, int cg, int splits, double per_kb, double per_tile) {
+        const int64_t tiles = swap ? cdiv(N, kLanes) * cdiv(M, bn) : cdiv(M, kLanes * cg) * cdiv(N, bn);
+        if (splits > 1 && (tiles * splits > sms || num_kb < 2 * splits)) return;
+        const int64_t at_once = sms / cg, rounds = cdiv(tiles * splits, at_once);
+        const double cost = rounds * (cdiv(num_kb, splits) * per_kb + per_tile) +
+                            (splits == 1 ? 0. : splits == 2 ? 8. : 9.);
+        if (best.bn && cost >= least) return;
+        least = cost;
+        best.swap = swap;
+        best.bn = bn;
+        best.cg = cg;
+        best.qvec = swap || !b_tile;
+        best.splits = splits;
+        best.grid = (int)(splits > 1 ? tiles * splits : std::min<int64_t>(tiles, at_once) * cg);
+    };
+    // (swapped, A is read by the MMA's column side, which takes an M-major
+    // operand only in chunks of 128)
+    if (!a_col)
+        for (int splits = 1; splits <= 4; splits *= 2) {
+            if (M <= 16) consider(1, 16, 1, splits, 1., 2.);
+            else if (M <= 32) consider(1, 32, 1, splits, 1.05, 2.);
+            else consider(1, 64, 1, splits, 1.15, 3.);
         }
-        pl.qvec = !b_tile;
+    if (M > 64 || a_col) {
+        consider(0, 128, 1, 1, 1.25, 5.);
+        consider(0, 256, 2, 1, 1.6, 10.);
     }
-    const int64_t tiles = pl.swap ? cdiv(N, kLanes) * cdiv(M, pl.bn) : cdiv(M, kLanes * pl.cg) * cdiv(N, pl.bn);
-    if (pl.cg == 1)
-        while (pl.splits < 8 && tiles * pl.splits * 2 <= sms && num_kb >= 4 * pl.splits * 2) pl.splits *= 2;
-    pl.grid = (int)(pl.splits > 1 ? tiles * pl.splits : std::min<int64_t>(tiles, sms / pl.cg) * pl.cg);
-    return pl;
+    return best;
 }
 
 // Tile shape and roles of an expert product, from the rows an expert has on average.
@@ -1052,11 +1066,15 @@ ScaledPlan plan_experts(int64_t rows, int64_t N, int64_t experts, int sms) {
     const int64_t used = std::max<int64_t>(1, std::min(rows, experts)), avg = cdiv(rows, used);
     pl.cg = 1;
     pl.splits = 1;
-    if (avg <= 64) {
+    // One tile should hold most experts' rows, which scatter around the average:
+    // swapped tiles up to 48 rows, 128 x 128 tiles up to 112, 256 x 256 beyond.
+    // Measured (2048 x 4096, 64 experts): 64 rows on average 143 us in swapped
+    // tiles of 64 columns, where every second expert needs two, 113 us in 128 x 128.
+    if (avg <= 48) {
         pl.swap = 1;
         pl.bn = avg <= 12 ? 16 : avg <= 24 ? 32 : 64;
         pl.qvec = 1;
-    } else if (avg < 256) {
+    } else if (avg <= 112) {
         pl.bn = 128;
     } else {
         pl.bn = 256;
@@ -1078,7 +1096,7 @@ int pack_operands(Operand *a, Operand *b, int dev, void **ws, cudaStream_t strea
     const uint64_t na = a->pack ? (uint64_t)a->rows * a->ld_use : 0, nb = b->pack ? (uint64_t)b->rows * b->ld_use : 0;
     const uint64_t off = (na + 255) / 256 * 256;
     if (!na && !nb) return GEMM_OK;
-    cudaError_t e = cudaMallocAsync(ws, off + nb, stream);
+    cudaError_t e = op_malloc(ws, off + nb, dev, stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         *ws = nullptr;
