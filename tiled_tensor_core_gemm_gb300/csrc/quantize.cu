@@ -36,7 +36,7 @@ struct QuantParams {
     int tiles_c;
     float top;
     int e5m2;
-    int q_wide;               // rows of Q start on 8 bytes
+    int q_wide;               // rows of Q start on 8 bytes (16 when rows are scattered)
 };
 
 __device__ __forceinline__ uint2 to_fp8x8(const float (&f)[8], int e5m2) {
@@ -75,7 +75,7 @@ __device__ __forceinline__ uint2 scaled8(const OpVec8<T> &x, float inv, int e5m2
 }
 
 template <typename T, int BLOCK, bool WIDE, bool SCATTER = false>
-__global__ void __launch_bounds__(kQThreads, SCATTER || sizeof(T) == 4 ? 2 : 3) quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_kernel(const QuantParams p) {
     pdl_enter();
     __shared__ float s_max[16][kTile];   // [row group][column]; tiles use one value a warp
     __shared__ float s_scale[kTile];
@@ -96,18 +96,11 @@ __global__ void __launch_bounds__(kQThreads, SCATTER || sizeof(T) == 4 ? 2 : 3) 
         x[i] = op_load8<WIDE, T>(X + r * p.ldx + c, r < p.rows ? have : 0);
     }
 
-    // The rows a row goes to: copy j's at lane j of its half-warp.
-    const bool few = p.copies <= 16;
-    int32_t slot[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t r = r0 + ty + 16 * i;
-        slot[i] = SCATTER && few && tx < p.copies && r < p.rows ? p.slots[r * p.copies + tx] : -1;
-    }
-    float scale[kRows];      // of this thread's rows (row blocks)
-    float inv8[8];           // of its columns (column blocks)
+    float inv8[8];           // 1 / scale of its rows (row blocks) or columns (column blocks)
     float inv = 0.f;         // of the tile
     if (BLOCK == GEMM_BLOCK_ROW) {
+        // Lane i (mod 8) of a row's half-warp divides for the thread's i-th row.
+        float mine = 0.f;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             float m = 0.f;
@@ -115,19 +108,16 @@ __global__ void __launch_bounds__(kQThreads, SCATTER || sizeof(T) == 4 ? 2 : 3) 
             for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(OpType<T>::up(x[i].v[k])));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            scale[i] = fmaxf(m / p.top, 0x1p-126f);
-            if (tx == 0) s_scale[ty + 16 * i] = scale[i];
+            if ((tx & 7) == i) mine = m;
         }
-        __syncthreads();
+        const float s = fmaxf(mine / p.top, 0x1p-126f), s_inv = 1.f / s;
+        if (tx < kRows) s_scale[ty + 16 * tx] = s;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) inv8[i] = __shfl_sync(0xffffffffu, s_inv, (threadIdx.x & 16) | i);
         if (!SCATTER) {
+            __syncthreads();
             if (threadIdx.x < kTile && r0 + threadIdx.x < p.rows)
                 S[(r0 + threadIdx.x) * p.s_row + cb * p.s_col] = s_scale[threadIdx.x];
-        } else {
-            const int64_t rows = p.rows - r0 < kTile ? p.rows - r0 : kTile;
-            for (int i = threadIdx.x; i < rows * p.copies; i += kQThreads) {
-                const int64_t to = p.slots[r0 * p.copies + i];
-                if (to >= 0 && to < p.out_rows) S[to * p.s_row + cb * p.s_col] = s_scale[i / p.copies];
-            }
         }
     } else {
         float m[8];
@@ -178,20 +168,36 @@ __global__ void __launch_bounds__(kQThreads, SCATTER || sizeof(T) == 4 ? 2 : 3) 
 #pragma unroll
             for (int k = 0; k < 4; ++k) asm volatile("" : "+r"(reinterpret_cast<uint32_t *>(x[i].v)[k]));
     }
+    if (SCATTER) {
+        // The tile's rows meet in shared memory; eight lanes then write a row to each
+        // of its places, 16 bytes a lane, and its scale.
+        __shared__ __align__(16) uint8_t s_q[kTile][kTile];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            *reinterpret_cast<uint2 *>(&s_q[ty + 16 * i][tx * 8]) = scaled8(x[i], inv8[i], p.e5m2);
+        __syncthreads();
+        const int lane8 = threadIdx.x & 7;
+        const int64_t at = cb * kTile + lane8 * 16;
+        const int left = at < p.cols ? (int)(p.cols - at < 16 ? p.cols - at : 16) : 0;
+        for (int g = threadIdx.x >> 3; g < kTile && r0 + g < p.rows; g += kQThreads / 8) {
+            const int32_t *slots = p.slots + (r0 + g) * p.copies;
+            const uint4 v = *reinterpret_cast<const uint4 *>(&s_q[g][lane8 * 16]);
+#pragma unroll 4
+            for (int j = 0; j < p.copies; ++j) {
+                const int32_t to = __ldg(slots + j);
+                if (to < 0 || to >= p.out_rows) continue;
+                uint8_t *d = Q + (int64_t)to * p.ldq + at;
+                if (p.q_wide && left == 16) *reinterpret_cast<uint4 *>(d) = v;
+                else
+                    for (int k = 0; k < left; ++k) d[k] = s_q[g][lane8 * 16 + k];
+                if (lane8 == 0) S[(int64_t)to * p.s_row + cb * p.s_col] = s_scale[g];
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int64_t r = r0 + ty + 16 * i;
-        if (SCATTER) {
-            const bool in = r < p.rows && have > 0;
-            const uint2 v = scaled8(x[i], 1.f / scale[i], p.e5m2);
-#pragma unroll 2
-            for (int j = 0; j < p.copies; ++j) {
-                const int64_t to = few ? __shfl_sync(0xffffffffu, slot[i], (threadIdx.x & 16) | (j & 15))
-                                       : (in ? p.slots[r * p.copies + j] : -1);
-                if (in && to >= 0 && to < p.out_rows) put8(Q + to * p.ldq + c, v, have, p.q_wide);
-            }
-            continue;
-        }
         if (r >= p.rows || have == 0) continue;
         if (BLOCK == GEMM_BLOCK_COL) {
             float f[8];
@@ -199,8 +205,7 @@ __global__ void __launch_bounds__(kQThreads, SCATTER || sizeof(T) == 4 ? 2 : 3) 
             for (int k = 0; k < 8; ++k) f[k] = OpType<T>::up(x[i].v[k]) * inv8[k];
             put8(Q + r * p.ldq + c, to_fp8x8(f, p.e5m2), have, p.q_wide);
         } else {
-            put8(Q + r * p.ldq + c, scaled8(x[i], BLOCK == GEMM_BLOCK_ROW ? 1.f / scale[i] : inv, p.e5m2), have,
-                 p.q_wide);
+            put8(Q + r * p.ldq + c, scaled8(x[i], BLOCK == GEMM_BLOCK_ROW ? inv8[i] : inv, p.e5m2), have, p.q_wide);
         }
     }
 }
@@ -273,7 +278,8 @@ extern "C" int gemm_quantize_block(int64_t batch, int64_t rows, int64_t cols, in
     p.top = to == GEMM_E4M3 ? 448.f : 57344.f;
     p.e5m2 = to == GEMM_E5M2;
     const bool wide = cols % 8 == 0 && op_wide(X, ldx, eb) && (batch == 1 || ((uint64_t)x_stride * eb) % 16 == 0);
-    p.q_wide = (uintptr_t)Q % 8 == 0 && ldq % 8 == 0 && (batch == 1 || q_stride % 8 == 0);
+    const int q_align = slots ? 16 : 8;
+    p.q_wide = (uintptr_t)Q % q_align == 0 && ldq % q_align == 0 && (batch == 1 || q_stride % 8 == 0);
     const int64_t tiles = (rows + kTile - 1) / kTile * p.tiles_c;
     if (tiles > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many blocks");
     const dim3 grid((unsigned)tiles, (unsigned)batch, 1);
