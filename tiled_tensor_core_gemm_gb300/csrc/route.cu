@@ -219,11 +219,36 @@ __device__ __forceinline__ int route_token(const RouteParams &p, int t, float *b
         for (int i = 0; i < EPL; ++i) key[i] = key_of(x[i]);
         if (grouped) keep_groups<EPL>(p, x, key, buf, lane);
     }
-    // The largest key of all lanes' largest, top_k times; its lane looks for its next.
+    // The largest key of all lanes' largest, top_k times.  A lane with few keys
+    // has them sorted (stably: equal keys in the order of their experts) and drops
+    // its first when it wins; one with many looks for its next.
     int mine = -1;
     uint32_t best;
     int at;
-    lane_best<EPL>(key, best, at);
+    uint32_t places = 0;                     // of the sorted keys, four bits each
+    if constexpr (EPL <= 8) {
+        int place[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) place[i] = i;
+#pragma unroll
+        for (int n = 0; n < EPL; ++n)
+#pragma unroll
+            for (int i = n & 1; i + 1 < EPL; i += 2) {
+                const bool swap = key[i] < key[i + 1];
+                const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
+                const int first = swap ? place[i + 1] : place[i], second = swap ? place[i] : place[i + 1];
+                key[i] = hi;
+                key[i + 1] = lo;
+                place[i] = first;
+                place[i + 1] = second;
+            }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) places |= (uint32_t)place[i] << (4 * i);
+        best = key[0];
+        at = place[0];
+    } else {
+        lane_best<EPL>(key, best, at);
+    }
     for (int j = 0; j < p.top_k; ++j) {
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
         if (top == 0u) break;
@@ -236,7 +261,15 @@ __device__ __forceinline__ int route_token(const RouteParams &p, int t, float *b
         }
         const int chosen = __shfl_sync(0xffffffffu, e, winner);
         if (lane == j) mine = chosen;
-        if (lane == winner) {
+        if constexpr (EPL <= 8) {
+            const bool won = lane == winner;
+#pragma unroll
+            for (int i = 0; i + 1 < EPL; ++i) key[i] = won ? key[i + 1] : key[i];
+            key[EPL - 1] = won ? 0u : key[EPL - 1];
+            places = won ? places >> 4 : places;
+            best = key[0];
+            at = (int)(places & 15u);
+        } else if (lane == winner) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
                 if (i == at) key[i] = 0u;
@@ -461,10 +494,9 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteParams p
             z += s[i];
         }
         z = warp_sum(z);
-        if (z > 0.f) {
+        const float inv = z > 0.f ? 1.f / z : 0.f;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) s[i] = s[i] / z;
-        }
+        for (int i = 0; i < EPL; ++i) s[i] *= inv;
     }
 #pragma unroll
     for (int i = 0; i < EPL; i += 4)
