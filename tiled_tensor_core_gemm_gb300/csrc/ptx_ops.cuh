@@ -59,11 +59,19 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Arrive on a barrier of another CTA of the cluster (a shared::cluster address)
-// that hands over Tensor Memory only: no ordinary writes go with it, so it is
-// not a release at cluster scope (which waits for all of the thread's writes).
-__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+// Arrive, where `yes` and without a branch, on a barrier of another CTA of the
+// cluster (a shared::cluster address) that hands over Tensor Memory only: no
+// ordinary writes go with it, so it is not a release at cluster scope (which
+// waits for all of the thread's writes).
+__device__ __forceinline__ void mbar_arrive_peer_if(uint32_t bar_cluster, bool yes) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}"
+                 ::"r"(bar_cluster), "r"((uint32_t)yes) : "memory");
+}
+
+// The same on a barrier of this CTA.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool yes) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+                 ::"r"(bar), "r"((uint32_t)yes) : "memory");
 }
 
 __device__ __forceinline__ float ld_shared_f(uint32_t addr) {
@@ -132,6 +140,15 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
+
+// Registers of a load that an earlier tmem_wait covered: no use of them moves above this.
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                          "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tmem_landed(uint32_t (&)[16]) {}
 
 // A warpgroup's registers a thread, at run time.
 template <int N> __device__ __forceinline__ void regs_give_back() {

@@ -96,18 +96,16 @@ struct Cfg {
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr bool SWAPPED = BN < 128;          // the tiles of few tokens
     static constexpr int OUT_BYTES = SWAPPED ? 2048 : 2 * kBoxBytes;  // a warp's staging for C
-    // Scales come four K-blocks at a time, in two slots of shared memory: for
-    // each K-block the lanes' 128 and the columns' BN, or, with one scale for 128
-    // columns, the lanes' times each 128 columns' one.
-    static constexpr int HALVES = (BN + 127) / 128;
-    static constexpr int SCALES = QVEC ? kLanes + BN : kLanes * HALVES;     // floats of a K-block
+    // With a scale per column, scales come four K-blocks at a time in two slots of
+    // shared memory: for each K-block the lanes' 128 and the columns' BN.
+    static constexpr int SCALES = QVEC ? kLanes + BN : 0;     // floats of a K-block
     static constexpr int SLOT_BYTES = kGroup * SCALES * 4;
     static constexpr int FIXED = 1024 + kCtrlBytes + kSlots * SLOT_BYTES + EW * OUT_BYTES + 2 * (kMaxExperts + 1) * 4 + 32;
     static constexpr int FIT = (kSmemMax - FIXED) / STAGE;
-    static constexpr int STAGES = FIT > 12 ? 12 : FIT;
+    static constexpr int STAGES = FIT >= 8 ? 8 : 4;                   // a power of two
     static constexpr int SMEM = FIXED + STAGES * STAGE;
     static_assert(!SPLIT_REGS || THREADS == 384, "the register split is written for 384 threads");
-    static_assert(STAGES >= 3 && SMEM <= kSmemMax, "ring");
+    static_assert(STAGES <= FIT && SMEM <= kSmemMax, "ring");
     static_assert((2 * STAGES + NBUF + 2 * kSlots) * 8 + 16 <= kCtrlBytes, "barrier area");
     static_assert(!SWAPPED || kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
 };
@@ -154,16 +152,15 @@ __device__ __noinline__ void wait_landed(uint32_t bar, uint32_t parity, unsigned
         if (ptx::globaltimer_ns() - t0 > timeout_ns) return;
 }
 
-// A position in a ring of n slots: its index and the parity of its lap.
-struct Ring {
-    int i = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int n) {
-        if (++i == n) {
-            i = 0;
-            phase ^= 1u;
-        }
+// A position in rings of 2^k slots, as the number of steps taken: one register
+// gives the slot and the parity of the lap in every ring that steps with it.
+struct Steps {
+    uint32_t n = 0;
+    template <int SLOTS> __device__ __forceinline__ int slot() const {
+        static_assert((SLOTS & (SLOTS - 1)) == 0, "a power of two");
+        return (int)(n & (uint32_t)(SLOTS - 1));
     }
+    template <int SLOTS> __device__ __forceinline__ uint32_t parity() const { return (n / (uint32_t)SLOTS) & 1u; }
 };
 
 // One output tile: D's rows [i0, i1) and columns [j0, j1) of expert e (0 outside
@@ -213,10 +210,10 @@ __device__ __forceinline__ Tile tile_at(const ScaledParams &p, const int32_t *fi
     return T;
 }
 
-// The scale of row i (clamped below `end`) in K-block kb of expert e.
-__device__ __forceinline__ float scale_at(const ScaleView &v, int i, int end, int kb, int e) {
+// Where the scale of row i (clamped below `end`) in K-block kb of expert e is.
+__device__ __forceinline__ const float *scale_of(const ScaleView &v, int i, int end, int kb, int e) {
     i = i < end ? i : end - 1;
-    return __ldg(v.p + kb * v.stride_k + (int64_t)(i >> v.shift) * v.stride_i + e * v.stride_e);
+    return v.p + kb * v.stride_k + (int64_t)(i >> v.shift) * v.stride_i + e * v.stride_e;
 }
 
 // acc += r * s (paired: two columns an instruction).
@@ -252,29 +249,24 @@ __device__ __forceinline__ void add_scaled_columns(float *acc, const uint32_t (&
 }
 
 // One warp's share of a tile's scales: COUNT of them a K-block, of the rows base,
-// base + 1, ..., each times the one of `by`'s row by_row (BY), kGroup K-blocks at a
-// time.  The next group's loads are in flight while one is handed over (but for
-// 256 of them, which its registers do not hold twice): a load takes about as
-// long as a K-block's MMAs.
-template <int COUNT, bool BY>
-__device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int end, int e, const ScaleView &by,
-                                             int by_row, int by_end, int by_e, int kb0, int kb1, int t, Ring &sl,
-                                             uint8_t *slots, int slot_bytes, int kb_floats, uint32_t scf0, uint32_t sce0,
-                                             const Bounds &bounds) {
+// base + 1, ..., kGroup K-blocks at a time.  The next group's loads are in flight
+// while one is handed over where the registers hold both; a load takes about as
+// long as a K-block's MMAs, and there are two slots.
+template <int COUNT>
+__device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int end, int e, int kb0, int kb1, int t,
+                                             Steps &sl, uint8_t *slots, int slot_bytes, int kb_floats, uint32_t scf0,
+                                             uint32_t sce0, const Bounds &bounds) {
     constexpr int PER = (COUNT + 31) / 32;
     const int lane = threadIdx.x & 31;
     constexpr bool kAhead = PER <= 4;
     float cur[kGroup][PER], nxt[kGroup][PER];
     auto load = [&](int kb) {
 #pragma unroll
-        for (int a = 0; a < kGroup; ++a) {
-            const float f = BY && kb + a < kb1 ? scale_at(by, by_row, by_end, kb + a, by_e) : 1.f;
+        for (int a = 0; a < kGroup; ++a)
 #pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                nxt[a][c] = kb + a < kb1 && 32 * c + lane < COUNT ? scale_at(v, base + 32 * c + lane, end, kb + a, e) : 0.f;
-                if (BY) nxt[a][c] *= f;
-            }
-        }
+            for (int c = 0; c < PER; ++c)
+                nxt[a][c] = kb + a < kb1 && 32 * c + lane < COUNT ? __ldg(scale_of(v, base + 32 * c + lane, end, kb + a, e))
+                                                                  : 0.f;
     };
     if (kAhead) load(kb0);
     for (int kb = kb0; kb < kb1; kb += kGroup) {
@@ -284,16 +276,16 @@ __device__ __forceinline__ bool bring_scales(const ScaleView &v, int base, int e
 #pragma unroll
             for (int c = 0; c < PER; ++c) cur[a][c] = nxt[a][c];
         if (kAhead) load(kb + kGroup);
-        if (!wait_warp(sce0 + 8u * (uint32_t)sl.i, sl.phase ^ 1u, bounds, kRoleScales, t)) return false;
-        float *slot = reinterpret_cast<float *>(slots + sl.i * slot_bytes);
+        if (!wait_warp(sce0 + 8u * (uint32_t)sl.slot<kSlots>(), sl.parity<kSlots>() ^ 1u, bounds, kRoleScales, t)) return false;
+        float *slot = reinterpret_cast<float *>(slots + sl.slot<kSlots>() * slot_bytes);
 #pragma unroll
         for (int a = 0; a < kGroup; ++a)
 #pragma unroll
             for (int c = 0; c < PER; ++c)
                 if (32 * c + lane < COUNT) slot[a * kb_floats + 32 * c + lane] = cur[a][c];
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(scf0 + 8u * (uint32_t)sl.i);
-        sl.next(kSlots);
+        if (lane == 0) ptx::mbar_arrive(scf0 + 8u * (uint32_t)sl.slot<kSlots>());
+        ++sl.n;
     }
     return true;
 }
@@ -535,7 +527,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             ptx::mbar_init(acce(b), EW * CG);
         }
         for (int s = 0; s < kSlots; ++s) {
-            ptx::mbar_init(scf(s), QVEC || Cf::HALVES == 2 ? 2 : 1);       // the scale warps
+            ptx::mbar_init(scf(s), 2);       // the scale warps
             ptx::mbar_init(sce(s), EW);
         }
         *abort_flag = 0;
@@ -598,26 +590,27 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     const int kb0 = (int)crank * p.kb_per_split, kb1 = min(p.num_kb, kb0 + p.kb_per_split);
 
     // 128 columns a thread need more than the launch's 168 registers: the first
-    // warpgroup gives the difference (128 x 72 + 256 x 216 = 384 x 168; with
-    // 56 and 224 the scale warps spill, 2% slower at 8192^3).
+    // warpgroup gives the difference (128 x 56 + 256 x 224 = 384 x 168; with
+    // a scale per column, 256 of which a warp brings, 128 x 72 + 256 x 216).
     if (warp < 4) {
-        if (Cf::SPLIT_REGS) ptx::regs_give_back<72>();
+        if (Cf::SPLIT_REGS) ptx::regs_give_back<QVEC ? 72 : 56>();
         if (warp == 0) {
             // ------------------------------------------------------ TMA producer
             // (the whole warp, one elected thread issuing, as the MMA warp)
-            Ring rg;
-            bool ok = true, laps = false;      // laps: the ring has been round once
+            Steps at;
+            bool ok = true;
             for (int t = unit; ok && t < num_tiles; t += units) {
                 const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
                 const int ep = p.tokens_on_i ? 0 : T.e, eq = p.tokens_on_i ? T.e : 0;
                 const int i0 = T.i0 + (int)rank * kLanes, j0 = T.j0 + (int)rank * (BN / CG);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!wait_warp(done(rg.i), rg.phase ^ 1u, bounds, kRoleProducer, t)) {
+                    if (!wait_warp(done(at.slot<Cf::STAGES>()), at.parity<Cf::STAGES>() ^ 1u, bounds, kRoleProducer, t)) {
                         ok = false;
                         break;
                     }
                     if (ptx::elect_one()) {
-                        const uint32_t fb = full(rg.i), sp = ring0 + (uint32_t)(rg.i * Cf::STAGE), sq = sp + Cf::P_BYTES;
+                        const int stage = at.slot<Cf::STAGES>();
+                        const uint32_t fb = full(stage), sp = ring0 + (uint32_t)(stage * Cf::STAGE), sq = sp + Cf::P_BYTES;
                         if (rank == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)(Cf::STAGE * CG));
                         const int k0 = kb * kBlockK;
                         const uint32_t to = kPair ? ptx::mapa_shared(fb, 0) : fb;     // a pair's bytes count in the leader
@@ -631,22 +624,19 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                         }
                     }
                     __syncwarp();
-                    rg.next(Cf::STAGES);
-                    laps = laps || rg.i == 0;
+                    ++at.n;
                 }
             }
             // Until the MMAs have released every slot no read of this shared
             // memory and no arrival on its barriers is outstanding.
-            const Ring last = rg;
-            for (int i = 0; ok && i < Cf::STAGES; ++i) {
-                ok = wait_warp(done(rg.i), rg.phase ^ 1u, bounds, kRoleDrain, -1);
-                rg.next(Cf::STAGES);
-            }
+            const uint32_t issued = at.n;
+            for (int i = 0; ok && i < Cf::STAGES; ++i, ++at.n)
+                ok = wait_warp(done(at.slot<Cf::STAGES>()), at.parity<Cf::STAGES>() ^ 1u, bounds, kRoleDrain, -1);
             // Given up: the copies already issued still land in this shared memory
             // (those of a pair are counted in the leader).
-            for (int i = 0; !ok && rank == 0 && i < Cf::STAGES; ++i) {
-                const uint32_t parity = i < last.i ? last.phase : last.phase ^ 1u;
-                if (laps || i < last.i) wait_landed(full(i), parity, p.timeout_ns);
+            for (uint32_t n = issued > Cf::STAGES ? issued - Cf::STAGES : 0; !ok && rank == 0 && n < issued; ++n) {
+                const Steps one = {n};
+                wait_landed(full(one.slot<Cf::STAGES>()), one.parity<Cf::STAGES>(), p.timeout_ns);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -657,7 +647,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             // One commit a K-block serves both who waits for it: the producer,
             // for the stage, and the epilogue warps, for the accumulator.
             if (rank == 0) {
-                Ring rg, buf;
+                Steps at;
                 bool ok = true;
                 uint32_t last_bar = 0, last_parity = 0;      // of the MMAs issued last
                 // descriptors in 16-byte units: leading offset, and one MMA's step along K
@@ -665,8 +655,9 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 const uint32_t p_step = p.p_mn ? 256u : 2u, q_step = p.q_mn ? 256u : 2u;
                 for (int t = unit; ok && t < num_tiles; t += units) {
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!wait_warp(full(rg.i), rg.phase, bounds, kRoleMma, t) ||
-                            !wait_warp(acce(buf.i), buf.phase ^ 1u, bounds, kRoleMma, t)) {
+                        const int stage = at.slot<Cf::STAGES>(), buf = at.slot<Cf::NBUF>();
+                        if (!wait_warp(full(stage), at.parity<Cf::STAGES>(), bounds, kRoleMma, t) ||
+                            !wait_warp(acce(buf), at.parity<Cf::NBUF>() ^ 1u, bounds, kRoleMma, t)) {
                             ok = false;
                             break;
                         }
@@ -675,89 +666,117 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                             // K-major: K advances 32 bytes inside a 128-byte row, 8-row
                             // groups 1024 bytes apart.  MN-major: 32 rows of K further,
                             // 128-byte chunks 16 KB apart, 8-row groups 1024.
-                            const uint32_t sp = ring0 + (uint32_t)(rg.i * Cf::STAGE);
+                            const uint32_t sp = ring0 + (uint32_t)(stage * Cf::STAGE);
                             const uint32_t pd = (sp >> 4) | p_lead, qd = ((sp + Cf::P_BYTES) >> 4) | q_lead;
-                            const uint32_t d = tmem + (uint32_t)(buf.i * BN);
+                            const uint32_t d = tmem + (uint32_t)(buf * BN);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 ptx::mma_f8_sw128<CG>(d, pd + p_step * kk, qd + q_step * kk, p.idesc, kk != 0 ? 1u : 0u);
-                            if (kPair) ptx::mma_commit_pair(done(rg.i), 0x3);
-                            else ptx::mma_commit(done(rg.i));
+                            if (kPair) ptx::mma_commit_pair(done(stage), 0x3);
+                            else ptx::mma_commit(done(stage));
                         }
                         __syncwarp();
-                        last_bar = done(rg.i);
-                        last_parity = rg.phase;
-                        rg.next(Cf::STAGES);
-                        buf.next(Cf::NBUF);
+                        last_bar = done(stage);
+                        last_parity = at.parity<Cf::STAGES>();
+                        ++at.n;
                     }
                 }
                 if (!ok && last_bar) wait_landed(last_bar, last_parity, p.timeout_ns);
             }
             __syncwarp();
         } else {
-            // ------------------------------------------------------------ scales
-            const bool first_warp = warp == 2;
-            Ring sl;
-            bool ok = QVEC || first_warp || Cf::HALVES == 2;
+            // --------------------------------------- scales (with one per column)
+            Steps sl;
+            bool ok = QVEC;
             for (int t = unit; ok && t < num_tiles; t += units) {
                 const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
-                const int ep = p.tokens_on_i ? 0 : T.e, eq = p.tokens_on_i ? T.e : 0;
-                const int i0 = T.i0 + (int)rank * kLanes;
-                if (QVEC && !first_warp)
-                    ok = bring_scales<BN, false>(p.sq, T.j0, T.j1, eq, p.sq, 0, 1, 0, kb0, kb1, t, sl,
-                                                 scales + kLanes * 4, Cf::SLOT_BYTES, Cf::SCALES, scf0, sce0, bounds);
+                if (warp == 2)
+                    ok = bring_scales<kLanes>(p.sp, T.i0 + (int)rank * kLanes, T.i1, p.tokens_on_i ? 0 : T.e, kb0, kb1, t, sl,
+                                              scales, Cf::SLOT_BYTES, Cf::SCALES, scf0, sce0, bounds);
                 else
-                    ok = bring_scales<kLanes, !QVEC>(p.sp, i0, T.i1, ep, p.sq, T.j0 + (first_warp ? 0 : 128), T.j1, eq, kb0,
-                                                     kb1, t, sl, scales + (first_warp ? 0 : kLanes * 4), Cf::SLOT_BYTES,
-                                                     Cf::SCALES, scf0, sce0, bounds);
+                    ok = bring_scales<BN>(p.sq, T.j0, T.j1, p.tokens_on_i ? T.e : 0, kb0, kb1, t, sl, scales + kLanes * 4,
+                                          Cf::SLOT_BYTES, Cf::SCALES, scf0, sce0, bounds);
             }
         }
     } else {
-        if (Cf::SPLIT_REGS) ptx::regs_take<216>();
+        if (Cf::SPLIT_REGS) ptx::regs_take<QVEC ? 216 : 224>();
         // ------------------------------------------------- sums and epilogue
         const uint32_t quarter = warp & 3, half = (warp - 4) >> 2;     // lanes it may read; its columns
         const int row = (int)(quarter * 32 + lane), col0 = (int)half * Cf::COLS;   // of this CTA's 128
         const uint32_t tbase = tmem + (quarter << 21) + (uint32_t)col0;   // lane field: quarter * 32 << 16
-        Ring rg, buf, sl;
+        Steps at, sl;                                                  // K-blocks, and groups of them
         int box = 0;                                                   // of C, written so far
+        const uint32_t acce_to = kPair ? ptx::mapa_shared(acce(0), 0) : acce(0);   // where accumulators are handed back
         bool ok = true;
         for (int t = unit; ok && t < num_tiles; t += units) {
             float acc[Cf::COLS];
 #pragma unroll
             for (int c = 0; c < Cf::COLS; ++c) acc[c] = 0.f;
-            // The next K-blocks' scales, and whether the next one's MMAs have
-            // completed, are looked up between handing the accumulator back and
-            // adding the last columns.
-            float sv[kGroup];
-            uint32_t columns = 0;          // (a scale per column) the K-block's, in shared memory
-            bool ready = false;
-            auto next_group = [&]() {
-                ok = wait_warp(scf(sl.i), sl.phase, bounds, kRoleEpilogue, t) && ok;
-                const uint32_t slot = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES) +
-                                      4u * (uint32_t)(row + (QVEC ? 0 : (col0 >> 7) * kLanes));
-#pragma unroll
-                for (int a = 0; a < kGroup; ++a) sv[a] = ptx::ld_shared_f(slot + 4u * (uint32_t)(a * Cf::SCALES));
+            // Scales.  One for 128 columns: each thread reads its row's and the
+            // columns' straight from memory, two K-blocks ahead.  One per column:
+            // through shared memory, where two warps bring them, the row's next one
+            // looked up between handing the accumulator back and adding the last
+            // columns (the group's end, needed until then, after them).
+            bool ready = false;                                  // the next K-block's MMAs have completed
+            float s_next = 0.f;
+            const float *row_at = nullptr, *col_at = nullptr;    // of the K-block two further
+            float row_1 = 0.f, col_1 = 0.f, row_2 = 0.f, col_2 = 0.f;
+            const uint32_t row_scale = scales0 + 4u * (uint32_t)row;
+            auto group_begins = [&]() {
+                ok = wait_warp(scf(sl.slot<kSlots>()), sl.parity<kSlots>(), bounds, kRoleEpilogue, t) && ok;
             };
-            auto release_group = [&]() {
+            auto group_ends = [&]() {
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(sce(sl.i));
-                sl.next(kSlots);
+                ptx::mbar_arrive_if(sce(sl.slot<kSlots>()), lane == 0);
+                ++sl.n;
             };
-            if (kb0 < kb1) next_group();
+            auto in_group = [&](int kb) { return (kb - kb0) % kGroup; };
+            auto scale_offset = [&](int kb) {
+                return (uint32_t)(sl.slot<kSlots>() * Cf::SLOT_BYTES + in_group(kb) * Cf::SCALES * 4);
+            };
+            auto next_scale = [&](int kb) {
+                if (in_group(kb) == 0) {
+                    group_ends();
+                    group_begins();
+                }
+                s_next = ptx::ld_shared_f(row_scale + scale_offset(kb));
+            };
+            if (QVEC && kb0 < kb1) {
+                group_begins();
+                s_next = ptx::ld_shared_f(row_scale + scale_offset(kb0));
+            }
+            if (!QVEC && kb0 < kb1) {
+                const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
+                row_at = scale_of(p.sp, T.i0 + (int)(rank * kLanes) + row, T.i1, kb0, p.tokens_on_i ? 0 : T.e);
+                col_at = scale_of(p.sq, T.j0 + (col0 & 128), T.j1, kb0, p.tokens_on_i ? T.e : 0);
+                row_1 = __ldg(row_at);
+                col_1 = __ldg(col_at);
+                if (kb0 + 1 < kb1) {
+                    row_2 = __ldg(row_at += p.sp.stride_k);
+                    col_2 = __ldg(col_at += p.sq.stride_k);
+                }
+            }
+#pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!__all_sync(0xffffffffu, ready)) ok = wait_warp(done(rg.i), rg.phase, bounds, kRoleEpilogue, t) && ok;
-                ready = false;
+                if (!__all_sync(0xffffffffu, ready))
+                    ok = wait_warp(done(at.slot<Cf::STAGES>()), at.parity<Cf::STAGES>(), bounds, kRoleEpilogue, t) && ok;
                 if (!ok) break;
+                ready = false;
                 ptx::tc_fence_after();
-                const uint32_t src = tbase + (uint32_t)(buf.i * BN), acce_now = acce(buf.i);
-                const int in = (kb - kb0) % kGroup;
-                const bool group_ends = in == kGroup - 1 || kb + 1 == kb1;
-                if (QVEC) columns = scales0 + (uint32_t)(sl.i * Cf::SLOT_BYTES) + 4u * (uint32_t)(in * Cf::SCALES + kLanes + col0);
-                const float s = sv[0];
-#pragma unroll
-                for (int a = 0; a + 1 < kGroup; ++a) sv[a] = sv[a + 1];
-                rg.next(Cf::STAGES);
-                buf.next(Cf::NBUF);
+                const int buf = at.slot<Cf::NBUF>();
+                const uint32_t src = tbase + (uint32_t)(buf * BN), release = acce_to + 8u * (uint32_t)buf;
+                // (a scale per column) the K-block's columns' scales
+                const uint32_t columns = scales0 + scale_offset(kb) + 4u * (uint32_t)(kLanes + col0);
+                const float s = QVEC ? s_next : row_1 * col_1;
+                ++at.n;
+                if (!QVEC) {
+                    row_1 = row_2;
+                    col_1 = col_2;
+                    if (kb + 2 < kb1) {
+                        row_2 = __ldg(row_at += p.sp.stride_k);
+                        col_2 = __ldg(col_at += p.sq.stride_k);
+                    }
+                }
                 // Two loads of 32 columns in flight; each is replaced by the one
                 // two further as soon as it has been added.
                 constexpr int kChunks = Cf::COLS / Cf::CHUNK;
@@ -769,28 +788,21 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                     else
                         add_scaled<Cf::CHUNK>(acc + c * Cf::CHUNK, r[c & 1], s);
                 };
+                ptx::tmem_load(src, r[0]);
+                if (kChunks > 1) ptx::tmem_load(src + (uint32_t)Cf::CHUNK, r[1]);
 #pragma unroll
                 for (int c = 0; c < kChunks; c += 2) {
-                    if (c == 0) {
-                        ptx::tmem_load(src, r[0]);
-                        if (kChunks > 1) ptx::tmem_load(src + (uint32_t)Cf::CHUNK, r[1]);
-                    }
                     ptx::tmem_wait(r[0]);
-                    if (kChunks > 1) ptx::tmem_wait(r[1]);
+                    if (kChunks > 1) ptx::tmem_landed(r[1]);
                     if (c + 2 >= kChunks) {
                         // the accumulator is read: its next K-block may be summed
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (kPair) ptx::mbar_arrive_peer(ptx::mapa_shared(acce_now, 0));
-                            else ptx::mbar_arrive(acce_now);
-                        }
+                        if (kPair) ptx::mbar_arrive_peer_if(release, lane == 0);
+                        else ptx::mbar_arrive_if(release, lane == 0);
                         if (kb + 1 < kb1) {
-                            ready = ptx::mbar_test(done(rg.i), rg.phase);
-                            if (!QVEC && group_ends) {
-                                release_group();
-                                next_group();
-                            }
+                            ready = ptx::mbar_test(done(at.slot<Cf::STAGES>()), at.parity<Cf::STAGES>());
+                            if (QVEC && in_group(kb + 1) != 0) next_scale(kb + 1);
                         }
                     }
                     add(c);
@@ -798,12 +810,9 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                     if (c + 1 < kChunks) add(c + 1);
                     if (c + 3 < kChunks) ptx::tmem_load(src + (uint32_t)((c + 3) * Cf::CHUNK), r[1]);
                 }
-                if (QVEC && group_ends) {
-                    release_group();
-                    if (kb + 1 < kb1) next_group();
-                }
+                if (QVEC && kb + 1 < kb1 && in_group(kb + 1) == 0) next_scale(kb + 1);
             }
-            if (!QVEC && ok && kb0 < kb1) release_group();
+            if (QVEC && ok && kb0 < kb1) group_ends();
             if (!ok) break;
             if (Cf::SWAPPED && p.splits > 1) {
                 // this CTA's K range of the tile, for the cluster to read: [column][lane]
