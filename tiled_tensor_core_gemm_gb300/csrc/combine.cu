@@ -10,6 +10,9 @@
 // and as many blocks as fit an SM stride over the tokens.  In the backward pass
 // g[t] is read once; each row's product with it is summed over the block in a
 // fixed order, so results do not depend on timing.
+//
+// Measured on GB300, 8192 tokens x 8 rows x 4096 BF16: 91 us (604 MB, 6.6 TB/s)
+// and 177 us for the gradients (1141 MB, 6.4 TB/s), 98% and 95% of a plain copy.
 #include "ops.h"
 
 namespace tcgemm {

@@ -12,6 +12,10 @@
 // memory over the row groups (columns), or both (tiles); the values are then
 // rounded from the registers.  It is bound by HBM: one read of X, one write of
 // q (one per copy when a row goes to its experts' rows) and of the scales.
+//
+// Measured on GB300, BF16 to E4M3: 8191 x 5120 by columns 23.5 us (127 MB, 5.4
+// TB/s, 80% of a plain copy); 8192 x 4096 by rows to eight rows each 67 us (344 MB,
+// 5.1 TB/s: four fifths of it writes, in 128-byte pieces).
 #include <cuda_fp8.h>
 
 #include "ops.h"

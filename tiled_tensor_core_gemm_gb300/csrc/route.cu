@@ -21,6 +21,10 @@
 // a third adds the experts' offsets.  Up to kClusterTokens tokens the blocks of
 // one cluster, 16 tokens each, read one another's counts in shared memory and
 // do all of it in one launch.
+//
+// Bound by latency and issue, not by memory.  Measured on GB300: 48 x 256 with
+// groups 11.5 us, one launch; 16384 x 128 16 us for the choice (4.2 MB of logits),
+// 3.6 for the scan and 5 for the placing, 9.5 for the gradient.
 #include <type_traits>
 
 #include "ops.h"

@@ -13,18 +13,30 @@
 // The scales change every 128 values of K, so an MMA may sum over one K-block
 // only: four MMAs of K = 32 write a fresh accumulator, and epilogue warps add
 // it, scaled, to sums kept in registers.  NBUF accumulators rotate, so the MMAs
-// of the next blocks run meanwhile.  Per K-block of 128 x 256 the MMAs
-// take at least 512 cycles of an SM, reading the accumulator 256 and the
-// multiply-adds (paired, one scale for 128 columns) 128 issue slots a
-// sub-partition; with a scale per column the multiply by it doubles that.
+// of the next blocks run meanwhile.
+//
+// What bounds it (GB300, 8192^3 in 256 x 256 tiles on CTA pairs, 452 us = 2.4
+// PFLOP/s, 64% of the FP8 rate): the epilogue warps.  Per K-block of 128 x 256
+// the MMAs take 520 cycles of an SM back to back and the kernel 850 to 900: of an
+// epilogue warp's own 850, about 100 to find the MMAs complete, 270 to read the
+// accumulator (two loads of 32 columns in flight), 260 for the multiply-adds (two
+// warps a scheduler, 128 cycles each), the rest hand-over and lookups, each of
+// which waits on shared memory that the MMAs and TMA keep busy.  Without the
+// multiply-adds the same loop runs at 350 us, without reading the accumulator too
+// at 337, next to 320 for the unscaled FP8 product.  The registers hold no third
+// load and no more warps; a longer loop does not fit the instruction caches (two
+// K-blocks unrolled: 690 us).  With a scale per column (the weight gradient) the
+// multiplies by it and their loads from shared memory add half as much again.
+// Few tokens stream the weights: 8 x 8192 x 8192 takes 16 us by graph replay
+// against 9.9 of HBM, in two K ranges of 64 tiles.
 //
 // Roles: warp 0 issues the TMA loads of P and Q into a ring; warp 1 the MMAs;
-// warp 2 brings the lanes' scales and warp 3 the columns' into a second ring in
-// shared memory; the other warps hold the sums, one lane a thread, and write C.
-// Both operands are read in either major: K-major as rows of 128 bytes, or
-// MN-major in chunks of 128 rows of K by 128 bytes (as tc_gemm.cu reads B).
-// Every wait is bounded (a time limit, and a flag that any role raises when it
-// gives up); a role that gives up waits, again bounded, for what it started.
+// with a scale per column, warp 2 brings the lanes' scales and warp 3 the
+// columns' into shared memory; the other warps hold the sums, one lane a thread,
+// and write C.  Both operands are read in either major: K-major as rows of 128
+// bytes, or MN-major in chunks of 128 rows of K by 128 bytes (as tc_gemm.cu reads
+// B).  Every wait is bounded (a time limit, and a flag that any role raises when
+// it gives up); a role that gives up waits, again bounded, for what it started.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
