@@ -299,6 +299,7 @@ GEMM_API int gemm_get_status(struct CUstream_st *stream);
  *   "debug_stall_mma" test hook: 1 makes the tensor-core kernel's MMA thread
  *                    first wait on a barrier nothing arrives at, so the wait
  *                    expires and gemm_get_status() reports GEMM_ERR_TIMEOUT
+ *                    (so does the block-scaled product's, gemm_ops.h)
  * Returns GEMM_ERR_INVALID_ARG for an unknown key or an out-of-range value.
  */
 GEMM_API int gemm_set_option(const char *key, int64_t value);

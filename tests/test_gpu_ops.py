@@ -305,6 +305,25 @@ def test_scaled_a_nan_or_infinity_stays_in_its_row():
         assert bool(got[2].isnan().all()) and not bool(torch.isfinite(got[4]).any())
 
 
+@pytest.mark.parametrize("M,N,K", [(8, 512, 4096), (150, 300, 700), (600, 1024, 2048)])
+def test_scaled_wait_that_runs_out_is_reported_and_leaves_the_device_usable(M, N, K):
+    A, sa = made(M, K, "row", "e4m3", 160)
+    B, sb = made(N, K, "tile", "e4m3", 170)
+    want = tg.gemm_scaled(A, sa, B.t(), sb.t())
+    s = torch.cuda.current_stream().cuda_stream
+    assert tg.gemm_set_option("wait_timeout_ms", 100) == tg.GEMM_OK
+    assert tg.gemm_set_option("debug_stall_mma", 1) == tg.GEMM_OK
+    try:
+        tg.gemm_scaled(A, sa, B.t(), sb.t())
+        assert tg.gemm_get_status(s) == tg.GEMM_ERR_TIMEOUT
+        assert "role=mma" in tg.gemm_last_error()
+    finally:
+        tg.gemm_set_option("wait_timeout_ms", 2000)
+        tg.gemm_set_option("debug_stall_mma", 0)
+    assert tg.gemm_get_status(s) == tg.GEMM_OK
+    assert torch.equal(tg.gemm_scaled(A, sa, B.t(), sb.t()), want)
+
+
 def test_scaled_runs_on_other_streams_in_order_and_repeats_bit_for_bit():
     A, sa = made(24, 4096, "row", "e4m3", 140)
     B, sb = made(2048, 4096, "tile", "e4m3", 150)
@@ -380,6 +399,21 @@ def test_experts_scale_per_column_a_that_tma_cannot_address_and_no_rows():
     check_experts(tg.gemm_experts(A, sa, W, sw, off), A, sa, W, sw, off, "f32")
     none = tg.gemm_experts(A[:0], sa[:0], W, sw, torch.zeros(E + 1, dtype=torch.int32, device="cuda"))
     assert none.shape == (0, N)
+
+
+@pytest.mark.parametrize("out", ("f32", "bf16"))
+def test_experts_many_tiles_a_block(out):
+    # whole and ragged tiles in turn on every block: boxes of C leave by TMA and by ordinary stores
+    E, N, K = 48, 1024, 256
+    counts = [260 + (37 * e) % 90 for e in range(E)]
+    off = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    A, sa = made(int(off[-1]), K, "row", "e4m3", 260)
+    W, sw = tg.quantize_block(randn(E, N, K, seed=261), "tile")
+    W, sw = W.transpose(1, 2), sw.transpose(1, 2)
+    first = tg.gemm_experts(A, sa, W, sw, off, out=out)
+    check_experts(first, A, sa, W, sw, off, out)
+    for _ in range(5):
+        assert torch.equal(tg.gemm_experts(A, sa, W, sw, off, out=out), first)
 
 
 def test_experts_many_and_weights_past_32_bits():
@@ -713,10 +747,11 @@ def test_the_example_runs_them_together():
     assert all(v < 0.08 for v in found.values())
 
 
-def test_operators_in_a_cuda_graph():
-    x = randn(40, 512, seed=60, dtype=torch.bfloat16)
+@pytest.mark.parametrize("T", (40, 300))         # 300: the routing takes a workspace
+def test_operators_in_a_cuda_graph(T):
+    x = randn(T, 512, seed=60, dtype=torch.bfloat16)
     w, ws = tg.quantize_block(randn(8, 256, 512, seed=61), "tile")
-    logits = randn(40, 8, seed=62)
+    logits = randn(T, 8, seed=62)
 
     def layer():
         r = tg.route(logits, 2)
@@ -729,7 +764,7 @@ def test_operators_in_a_cuda_graph():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out = layer()
-    logits.copy_(randn(40, 8, seed=63))
+    logits.copy_(randn(T, 8, seed=63))
     graph.replay()
     torch.cuda.synchronize()
     got = out.clone()

@@ -87,6 +87,7 @@ struct ScaledParams {
     int swapped;               // P is B^T: C's columns are D's rows
     int wide;                  // C's rows start on 16 bytes
     int tma_store;             // and end on them: whole boxes leave by TMA
+    int debug_stall;           // test hook: the MMA warp first waits for what cannot come
     EpiParams epi;
     const int32_t *offsets;    // experts: rows of each
     int experts, rows;         // 0: one product
@@ -491,6 +492,8 @@ __device__ __forceinline__ void write_rows(const ScaledParams &p, const CUtensor
                         static_cast<float *>(p.C)[at] = ptx::ld_shared_f(from + ((4u * (uint32_t)lane) ^ sw));
                     }
                 }
+                // (an empty group, so that groups count boxes whichever way they left)
+                if (lane == 0) ptx::bulk_commit_group();
                 __syncwarp();
             }
         }
@@ -665,6 +668,9 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 // descriptors in 16-byte units: leading offset, and one MMA's step along K
                 const uint32_t p_lead = (p.p_mn ? 1024u : 1u) << 16, q_lead = (p.q_mn ? 1024u : 1u) << 16;
                 const uint32_t p_step = p.p_mn ? 256u : 2u, q_step = p.q_mn ? 256u : 2u;
+                // (no accumulator is handed back before the first has been written; half
+                // the limit, so that this wait and not one behind it runs out first)
+                if (p.debug_stall) ok = wait_warp(acce(0), 0u, Bounds{abort_flag, p.timeout_ns / 2}, kRoleMma, unit);
                 for (int t = unit; ok && t < num_tiles; t += units) {
                     for (int kb = kb0; kb < kb1; ++kb) {
                         const int stage = at.slot<Cf::STAGES>(), buf = at.slot<Cf::NBUF>();
@@ -1155,7 +1161,9 @@ int encode_and_launch(const ScaledPlan &pl, ScaledParams &p, const Operand &a, i
     p.splits = pl.splits;
     p.kb_per_split = (int)cdiv(p.num_kb, pl.splits);
     p.group_i = 16;
-    p.timeout_ns = (unsigned long long)options_snapshot().wait_timeout_ms * 1000000ull;
+    const Options opt = options_snapshot();
+    p.timeout_ns = (unsigned long long)opt.wait_timeout_ms * 1000000ull;
+    p.debug_stall = opt.debug_stall_mma;
     CUtensorMap tp, tq, tc;
     std::memset(&tp, 0, sizeof tp);
     std::memset(&tq, 0, sizeof tq);
