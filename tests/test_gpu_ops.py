@@ -221,6 +221,27 @@ def test_scaled_product(shape, layout):
         check_product(tg.gemm_scaled(A, sa, B, sb, out=out), A, B, sa, sb, out)
 
 
+# on this device's 152 SMs the first takes 256 x 256 tiles, the second 256 x 192, both on CTA
+# pairs with several tiles in flight and ragged ends
+@pytest.mark.parametrize("M,N,K", [(2000, 2001, 2100), (2600, 2296, 1000)])
+@pytest.mark.parametrize("layout", ("forward", "input", "weight"))
+@pytest.mark.parametrize("out,act", [("f32", "none"), ("bf16", "gelu")])
+def test_scaled_pair_tiles(M, N, K, layout, out, act):
+    if layout == "weight":
+        A, sa = made(K, M, "col", "e4m3", 12)
+        A, sa = A.t(), sa.t()
+        B, sb = made(K, N, "col", "e4m3", 22)
+    else:
+        A, sa = made(M, K, "row", "e4m3", 12)
+        B, sb = made(N, K, "tile", "e4m3", 22) if layout == "forward" else made(K, N, "tile", "e4m3", 22)
+        if layout == "forward":
+            B, sb = B.t(), sb.t()
+    bias = randn(N, seed=32)
+    got = tg.gemm_scaled(A, sa, B, sb, bias=bias, act=act, out=out)
+    check_product(got, A, B, sa, sb, out, bias=bias, act=act)
+    assert torch.equal(got, tg.gemm_scaled(A, sa, B, sb, bias=bias, act=act, out=out))
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 300, 500), (150, 260, 390), (150, 1030, 4200)])
 @pytest.mark.parametrize("a_block,b_block", [("row", "row"), ("tile", "tile"), ("tile", "row"), ("row", "tile")])
 def test_scaled_block_kinds(M, N, K, a_block, b_block):

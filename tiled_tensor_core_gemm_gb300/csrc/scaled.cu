@@ -101,12 +101,15 @@ struct Cfg {
     static constexpr int COLS = BN / (EW / 4);        // columns of a thread
     static constexpr int CHUNK = COLS < 32 ? COLS : 32;
     static constexpr int THREADS = 128 + EW * 32;
-    static constexpr bool SPLIT_REGS = COLS > 64;
+    // Registers a thread after the first warpgroup has given some up (0: as launched).
+    static constexpr int GIVE = THREADS == 512 ? 56 : COLS > 64 ? (QVEC ? 72 : 56) : 0;
+    static constexpr int TAKE = THREADS == 512 ? 152 : COLS > 64 ? (QVEC ? 216 : 224) : 0;
+    static constexpr int LAUNCH = THREADS == 512 ? 128 : 168;         // what __launch_bounds__ leaves them
     static constexpr int P_BYTES = kLanes * 128;
     static constexpr int Q_BYTES = BN / CG * 128;     // each CTA of a pair loads half of Q's rows
     static constexpr int STAGE = P_BYTES + Q_BYTES;
-    static constexpr int NBUF = BN >= 256 ? 2 : 4;
-    static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
+    static constexpr int NBUF = BN > 128 ? 2 : 4;
+    static constexpr int TMEM_COLS = BN >= 128 ? 512 : NBUF * BN;     // a power of two, at least 32
     static constexpr bool SWAPPED = BN < 128;          // the tiles of few tokens
     static constexpr int OUT_BYTES = SWAPPED ? 2048 : 2 * kBoxBytes;  // a warp's staging for C
     // With a scale per column, scales come four K-blocks at a time in two slots of
@@ -117,7 +120,7 @@ struct Cfg {
     static constexpr int FIT = (kSmemMax - FIXED) / STAGE;
     static constexpr int STAGES = FIT >= 8 ? 8 : 4;                   // a power of two
     static constexpr int SMEM = FIXED + STAGES * STAGE;
-    static_assert(!SPLIT_REGS || THREADS == 384, "the register split is written for 384 threads");
+    static_assert(GIVE == 0 || 128 * GIVE + EW * 32 * TAKE <= THREADS * LAUNCH, "the shares exceed the launch's registers");
     static_assert(STAGES <= FIT && SMEM <= kSmemMax, "ring");
     static_assert((2 * STAGES + NBUF + 2 * kSlots) * 8 + 16 <= kCtrlBytes, "barrier area");
     static_assert(!SWAPPED || kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
@@ -608,7 +611,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
     // warpgroup gives the difference (128 x 56 + 256 x 224 = 384 x 168; with
     // a scale per column, 256 of which a warp brings, 128 x 72 + 256 x 216).
     if (warp < 4) {
-        if (Cf::SPLIT_REGS) ptx::regs_give_back<QVEC ? 72 : 56>();
+        if constexpr (Cf::GIVE != 0) ptx::regs_give_back<Cf::GIVE>();
         if (warp == 0) {
             // ------------------------------------------------------ TMA producer
             // (the whole warp, one elected thread issuing, as the MMA warp)
@@ -717,28 +720,44 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
             }
         }
     } else {
-        if (Cf::SPLIT_REGS) ptx::regs_take<QVEC ? 216 : 224>();
+        if constexpr (Cf::TAKE != 0) ptx::regs_take<Cf::TAKE>();
         // ------------------------------------------------- sums and epilogue
         const uint32_t quarter = warp & 3, half = (warp - 4) >> 2;     // lanes it may read; its columns
         const int row = (int)(quarter * 32 + lane), col0 = (int)half * Cf::COLS;   // of this CTA's 128
         const uint32_t tbase = tmem + (quarter << 21) + (uint32_t)col0;   // lane field: quarter * 32 << 16
         Steps at, sl;                                                  // K-blocks, and groups of them
         int box = 0;                                                   // of C, written so far
+        // One scale for 128 columns: each thread reads its row's and the columns'
+        // straight from memory, two K-blocks ahead.  In 192 columns a tile's first are
+        // asked for before the epilogue of the one before (in 256 the registers they
+        // hold there would be spilled: 463 -> 572 us at 8192^3).
+        constexpr bool kEarly = BN == 192;
+        const float *row_at = nullptr, *col_at = nullptr;              // of the K-block two further
+        float row_even = 0.f, col_even = 0.f, row_odd = 0.f, col_odd = 0.f;
+        auto first_scales = [&](int t) {
+            if (QVEC || t >= num_tiles || kb0 >= kb1) return;
+            const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
+            row_at = scale_of(p.sp, T.i0 + (int)(rank * kLanes) + row, T.i1, kb0, p.tokens_on_i ? 0 : T.e);
+            col_at = scale_of(p.sq, T.j0 + col0, T.j1, kb0, p.tokens_on_i ? T.e : 0);
+            row_even = __ldg(row_at);
+            col_even = __ldg(col_at);
+            if (kb0 + 1 < kb1) {
+                row_odd = __ldg(row_at += p.sp.stride_k);
+                col_odd = __ldg(col_at += p.sq.stride_k);
+            }
+        };
+        if (kEarly) first_scales(unit);
         const uint32_t acce_to = kPair ? ptx::mapa_shared(acce(0), 0) : acce(0);   // where accumulators are handed back
         bool ok = true;
         for (int t = unit; ok && t < num_tiles; t += units) {
             float acc[Cf::COLS];
 #pragma unroll
             for (int c = 0; c < Cf::COLS; ++c) acc[c] = 0.f;
-            // Scales.  One for 128 columns: each thread reads its row's and the
-            // columns' straight from memory, two K-blocks ahead.  One per column:
-            // through shared memory, where two warps bring them, the row's next one
+            // Scales.  One for 128 columns: see above.  One per column: through shared memory, where two warps bring them, the row's next one
             // looked up between handing the accumulator back and adding the last
             // columns (the group's end, needed until then, after them).
             bool ready = false;                                  // the next K-block's MMAs have completed
             float s_next = 0.f;
-            const float *row_at = nullptr, *col_at = nullptr;    // of the K-block two further
-            float row_1 = 0.f, col_1 = 0.f, row_2 = 0.f, col_2 = 0.f;
             const uint32_t row_scale = scales0 + 4u * (uint32_t)row;
             auto group_begins = [&]() {
                 ok = wait_warp(scf(sl.slot<kSlots>()), sl.parity<kSlots>(), bounds, kRoleEpilogue, t) && ok;
@@ -759,20 +778,10 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 }
                 s_next = ptx::ld_shared_f(row_scale + scale_offset(kb));
             };
+            if (!kEarly) first_scales(t);
             if (QVEC && kb0 < kb1) {
                 group_begins();
                 s_next = ptx::ld_shared_f(row_scale + scale_offset(kb0));
-            }
-            if (!QVEC && kb0 < kb1) {
-                const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
-                row_at = scale_of(p.sp, T.i0 + (int)(rank * kLanes) + row, T.i1, kb0, p.tokens_on_i ? 0 : T.e);
-                col_at = scale_of(p.sq, T.j0 + (col0 & 128), T.j1, kb0, p.tokens_on_i ? T.e : 0);
-                row_1 = __ldg(row_at);
-                col_1 = __ldg(col_at);
-                if (kb0 + 1 < kb1) {
-                    row_2 = __ldg(row_at += p.sp.stride_k);
-                    col_2 = __ldg(col_at += p.sq.stride_k);
-                }
             }
 #pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -785,15 +794,20 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 const uint32_t src = tbase + (uint32_t)(buf * BN), release = acce_to + 8u * (uint32_t)buf;
                 // (a scale per column) the K-block's columns' scales
                 const uint32_t columns = scales0 + scale_offset(kb) + 4u * (uint32_t)(kLanes + col0);
-                const float s = QVEC ? s_next : row_1 * col_1;
+                float s = s_next;
                 ++at.n;
                 if (!QVEC) {
-                    row_1 = row_2;
-                    col_1 = col_2;
-                    if (kb + 2 < kb1) {
-                        row_2 = __ldg(row_at += p.sp.stride_k);
-                        col_2 = __ldg(col_at += p.sq.stride_k);
-                    }
+                    // even and odd K-blocks in registers of their own: a move from one to
+                    // the other would wait for a load issued one K-block ago
+                    auto take = [&](float &r_scale, float &c_scale) {
+                        s = r_scale * c_scale;
+                        if (kb + 2 < kb1) {
+                            r_scale = __ldg(row_at += p.sp.stride_k);
+                            c_scale = __ldg(col_at += p.sq.stride_k);
+                        }
+                    };
+                    if ((kb - kb0) & 1) take(row_odd, col_odd);
+                    else take(row_even, col_even);
                 }
                 // Two loads of 32 columns in flight; each is replaced by the one
                 // two further as soon as it has been added.
@@ -839,6 +853,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
                 for (int c = 0; c < Cf::COLS; ++c) part[(col0 + c) * kLanes + row] = acc[c];
                 break;                                   // one tile a cluster
             }
+            if (kEarly) first_scales(t + units);
             const Tile T = tile_at<BN, Cf::ROWS>(p, first_tile, first_row, t);
             const uint32_t out_buf = out0 + (warp - 4) * (uint32_t)Cf::OUT_BYTES;
             if constexpr (Cf::SWAPPED)
@@ -991,6 +1006,7 @@ int launch_plan(const ScaledPlan &pl, const CUtensorMap &tp, const CUtensorMap &
         case 128:
             return pl.qvec ? launch<128, true, 8, 1>(pl, tp, tq, tc, p, stream)
                            : launch<128, false, 8, 1>(pl, tp, tq, tc, p, stream);
+        case 192: return launch<192, false, 12, 2>(pl, tp, tq, tc, p, stream);
         default:
             return pl.qvec ? launch<256, true, 8, 2>(pl, tp, tq, tc, p, stream)
                            : launch<256, false, 8, 2>(pl, tp, tq, tc, p, stream);
@@ -1049,12 +1065,14 @@ uint32_t idesc_of(int dtype, int bn, int cg, int p_mn, int q_mn) {
 
 // Tile shape, roles and K ranges of one product: the cheapest by a model of the
 // kernel's pace, in units of a 16-column tile's K-block (about 0.3 us):
-//   swapped tiles of 16, 32, 64 columns   1, 1.05, 1.15 a K-block
+//   swapped tiles of 16, 32, 64 columns   1, 1.05, 1.15 a K-block, 2 or 3 a tile
 //   128 x 128                             1.25 a K-block, 5 a tile
-//   256 x 256 on a CTA pair               1.6 a K-block, 10 a tile
+//   256 x 256, 256 x 192 on a CTA pair    1.5, 1.3 a K-block, 13.5, 7.7 a tile
 // and 8 or 9 more for K cut in 2 or 4 ranges (the cluster's exchange: measured
-// 2.4 us; 8 ranges cost 9 us and are never taken).
-ScaledPlan plan_product(int64_t M, int64_t N, int64_t num_kb, bool a_col, bool b_tile, int sms) {
+// 2.4 us; 8 ranges cost 9 us and are never taken).  Both sides measured, in us:
+// 256 columns 463 at 8192^3, 107 at 8192 x 8192 x 1024, 28 at 2048^3; 192 columns
+// (three warpgroups' sums, half the epilogue) 517, 103 and 31.
+ScaledPlan plan_product(int64_t M, int64_t N, int64_t num_kb, bool a_col, bool b_col, bool b_tile, int sms) {
     ScaledPlan best = {};
     double least = 0.;
     auto consider = [&](int swap, int bn, int cg, int splits, double per_kb, double per_tile) {
@@ -1082,13 +1100,14 @@ ScaledPlan plan_product(int64_t M, int64_t N, int64_t num_kb, bool a_col, bool b
         }
     if (M > 64 || a_col) {
         consider(0, 128, 1, 1, 1.25, 5.);
-        consider(0, 256, 2, 1, 1.6, 10.);
+        consider(0, 256, 2, 1, 1.5, 13.5);
+        if (b_tile && b_col) consider(0, 192, 2, 1, 1.3, 7.7);     // (whole 128-column chunks of B otherwise)
     }
     return best;
 }
 
 // Tile shape and roles of an expert product, from the rows an expert has on average.
-ScaledPlan plan_experts(int64_t rows, int64_t N, int64_t experts, int sms) {
+ScaledPlan plan_experts(int64_t rows, int64_t N, int64_t num_kb, int64_t experts, bool b_col, bool b_tile, int sms) {
     ScaledPlan pl = {};
     const int64_t used = std::max<int64_t>(1, std::min(rows, experts)), avg = cdiv(rows, used);
     pl.cg = 1;
@@ -1104,7 +1123,11 @@ ScaledPlan plan_experts(int64_t rows, int64_t N, int64_t experts, int sms) {
     } else if (avg <= 112) {
         pl.bn = 128;
     } else {
-        pl.bn = 256;
+        // 256 or 192 columns as plan_product has it, the tiles' fixed cost higher here
+        // (32768 rows over 32 experts 4096 x 2048: 391 us and 380; 16384 over 64,
+        // 2048 x 4096: 231 and 246)
+        const double wide = (double)cdiv(N, 256) * (1.5 * num_kb + 18.), narrow = (double)cdiv(N, 192) * (1.3 * num_kb + 8.7);
+        pl.bn = b_col && b_tile && narrow < wide ? 192 : 256;
         pl.cg = 2;
     }
     const int64_t wt = pl.swap ? cdiv(N, kLanes) : cdiv(N, pl.bn), rt = pl.swap ? pl.bn : kLanes * pl.cg;
@@ -1232,7 +1255,7 @@ int gemm_run_scaled(int64_t M, int64_t N, int64_t K, int dtype, const void *A, i
     if ((rc = op_check(spans, 6, &sms))) return rc;
     plan_operand(&a);
     plan_operand(&b);
-    const ScaledPlan pl = plan_product(M, N, num_kb, a_major != 0, b_scale->block == 128, sms);
+    const ScaledPlan pl = plan_product(M, N, num_kb, a_major != 0, b_major != 0, b_scale->block == 128, sms);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     ScaledParams p = {};
     p.I = (int)(pl.swap ? N : M);
@@ -1297,7 +1320,7 @@ int gemm_run_experts(int64_t rows, int64_t N, int64_t K, int64_t experts, int dt
     int sms = 0;
     if ((rc = op_check(spans, 6, &sms))) return rc;
     b.ld_use = ldb;
-    ScaledPlan pl = plan_experts(rows, N, experts, sms);
+    ScaledPlan pl = plan_experts(rows, N, num_kb, experts, b_major != 0, b_scale->block == 128, sms);
     if (!pl.swap) pl.qvec = b_scale->block != 128;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     ScaledParams p = {};
