@@ -237,26 +237,22 @@ def quantize_block(x, block="row", dtype="e4m3", scatter=None, out_rows=None, st
     mb = rows if code == 0 else -(-m // BLOCK)
     nb = n if code == 1 else -(-n // BLOCK)
     device = x.device
-    q = torch.empty((rows, pitch) if dims == 2 else (batch, rows, pitch), dtype=qdt, device=device)
-    at = q.data_ptr()
-    if pitch != n:
-        q = q[..., :n]
+    # (one allocation each, with the strides they are to have)
     if code == 0:
         held = -(-mb // 4) * 4
-        s = torch.empty((nb, held) if dims == 2 else (batch, nb, held), dtype=torch.float32, device=device)
-        s_at = s.data_ptr()
-        s = s.transpose(-1, -2)
-        if held != mb:
-            s = s[..., :mb, :]
         s_row, s_col, s_batch = 1, held or 1, nb * held
     else:
-        s = torch.empty((mb, nb) if dims == 2 else (batch, mb, nb), dtype=torch.float32, device=device)
-        s_at = s.data_ptr()
         s_row, s_col, s_batch = nb, 1, mb * nb
+    if dims == 2:
+        q = torch.empty_strided((rows, n), (pitch or 1, 1), dtype=qdt, device=device)
+        s = torch.empty_strided((mb, nb), (s_row, s_col), dtype=torch.float32, device=device)
+    else:
+        q = torch.empty_strided((batch, rows, n), (rows * pitch, pitch or 1, 1), dtype=qdt, device=device)
+        s = torch.empty_strided((batch, mb, nb), (s_batch, s_row, s_col), dtype=torch.float32, device=device)
     if copies == 0 or (scatter is not None and rows == 0):
         return q, s
-    rc = lib.gemm_quantize_block(batch, m, n, kind, x.data_ptr(), ldx, stride[0] if batch > 1 else 0, code, to, at,
-                                 pitch or 1, rows * pitch, s_at, s_row, s_col, s_batch, slots, copies, rows,
+    rc = lib.gemm_quantize_block(batch, m, n, kind, x.data_ptr(), ldx, stride[0] if batch > 1 else 0, code, to,
+                                 q.data_ptr(), pitch or 1, rows * pitch, s.data_ptr(), s_row, s_col, s_batch, slots, copies, rows,
                                  raw(index) if stream is None else stream)
     if rc:
         _fail(tg, rc)
