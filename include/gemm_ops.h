@@ -8,6 +8,9 @@
  * without synchronising, a gemm_status_t returned, gemm_last_error() for the
  * message.  Index arrays live on the device and are int32.
  *
+ * Matrices that are only read, row by row (X of the quantisation, logits, Y and
+ * grad), may have a row pitch of 0: one row that stands for all of them.
+ *
  * Element types: `type` arguments are gemm_out_t for FP32 / BF16 / FP16 data
  * and gemm_dtype_t's GEMM_E4M3 / GEMM_E5M2 for FP8 data.
  */

@@ -790,3 +790,59 @@ def test_operators_in_a_cuda_graph(T):
     torch.cuda.synchronize()
     got = out.clone()
     assert torch.equal(got, layer())
+
+
+# --------------------------------------------------- one row expanded over all ---
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,H", [(5, 2, 64), (70, 4, 1000), (33, 3, 77)])
+def test_a_row_expanded_is_read_like_its_copies(T, k, H, dtype):
+    # a neighbour in the same storage that a dense pitch would read: equal results come from the row alone
+    def expanded(rows, cols, seed):
+        held = randn(rows + 1, cols, seed=seed, dtype=dtype)
+        held[1:] = math.nan
+        return held[:1].expand(rows, cols)
+    R = T * k
+    slots = torch.randperm(R, generator=gen(70), device="cuda").view(T, k).to(torch.int32)
+    w, y, g = randn(T, k, seed=71), randn(R, H, seed=72, dtype=dtype), randn(T, H, seed=73, dtype=dtype)
+    ye, ge = expanded(R, H, 74), expanded(T, H, 75)
+    assert torch.equal(tg.combine(ye, slots, w), tg.combine(ye.contiguous(), slots, w))
+    for a, b in ((ge, y), (g, ye), (ge, ye)):
+        got, want = tg.combine_backward(a, b, slots, w), tg.combine_backward(a.contiguous(), b.contiguous(), slots, w)
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
+    x = expanded(T, 64, 76)
+    r = tg.route(x, 3)
+    assert all(torch.equal(u, v) for u, v in zip(r, tg.route(x.contiguous(), 3)))
+    gw = randn(T, 3, seed=77)
+    assert torch.equal(tg.route_backward(gw, x, r.indices), tg.route_backward(gw, x.contiguous(), r.indices))
+    for block in ("row", "col", "tile"):
+        for z in (ye, expanded(R, 1, 78)):
+            q, s = tg.quantize_block(z, block)
+            eq, es = tg.quantize_block(z.contiguous(), block)
+            assert same_bits(q, eq) and torch.equal(s, es)
+
+
+def test_combine_backward_takes_the_gradient_of_a_sum_over_tokens():
+    T, k, H = 40, 2, 264
+    slots = torch.randperm(T * k, generator=gen(80), device="cuda").view(T, k).to(torch.int32)
+    w, y = randn(T, k, seed=81), randn(T * k, H, seed=82)
+    out = tg.combine(y, slots, w).requires_grad_(True)
+    grad, = torch.autograd.grad(out.sum(0), out, randn(H, seed=83))
+    assert grad.stride() == (0, 1)
+    got, want = tg.combine_backward(grad, y, slots, w), tg.combine_backward(grad.contiguous(), y, slots, w)
+    assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+def test_expanded_rows_are_refused_where_they_are_written_or_go_through_tma():
+    A, sa = made(8, 128, "row", "e4m3", 84)
+    B, sb = made(64, 128, "tile", "e4m3", 85)
+    one = torch.zeros(1, 64, device="cuda").expand(8, 64)
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    slots = torch.zeros(8, 1, dtype=torch.int32, device="cuda")
+    A1 = A[:1].expand(8, 128)
+    for call in (lambda: tg.gemm_scaled(A, sa, B.t(), sb.t(), C=one), lambda: tg.gemm_scaled(A1, sa, B.t(), sb.t()),
+                 lambda: tg.gemm_scaled(A, sa, B[:1].expand(64, 128).t(), sb.t()),
+                 lambda: tg.gemm_experts(A, sa, B.t()[None], sb.t()[None], off, C=one),
+                 lambda: tg.gemm_experts(A1, sa, B.t()[None], sb.t()[None], off),
+                 lambda: tg.combine(randn(8, 64), slots, out=one)):
+        with pytest.raises(ValueError, match="expanded"):
+            call()

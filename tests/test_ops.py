@@ -238,3 +238,49 @@ def test_majors_of_views():
     assert ops._major("t", t[:, :1].t()) == (1, 0) or ops._major("t", t[:, :1].t()) == (32, 1)
     with pytest.raises(ValueError):
         ops._major("t", t[:, ::2])
+
+
+# ------------------------------------------- one row (or column) expanded ---
+def test_row_pitch_of_an_expanded_row():
+    row = torch.zeros(1, 64)
+    z = torch.zeros(5, 64, requires_grad=True)
+    kept = []
+    z.register_hook(kept.append)
+    z.sum(0).backward(torch.ones(64))
+    assert kept[0].stride() == (0, 1)             # what autograd hands back from a sum over the rows
+    for t in (row.expand(4096, 64), kept[0], torch.zeros(1, 1).expand(6, 1)):
+        assert ops._rows("t", t, *t.shape, True) == 0
+        with pytest.raises(ValueError, match="t must have rows of its own"):
+            ops._rows("t", t, *t.shape)
+    assert ops._rows("t", row, 1, 64) == 64
+    assert ops._rows("t", torch.zeros(3, 64)[:, :7], 3, 7) == 64
+    assert ops._rows("t", torch.zeros(1, 0).expand(4, 0), 4, 0) == 1
+
+
+def test_majors_of_expanded_matrices_are_refused():
+    one = torch.zeros(1, 1)
+    for t in (one.expand(6, 1), one.expand(1, 6), torch.zeros(1, 64).expand(6, 64), torch.zeros(64, 1).expand(64, 6),
+              torch.zeros(2, 1, 1).expand(2, 6, 1)):
+        with pytest.raises(ValueError, match="not expanded"):
+            ops._major("t", t)
+    assert ops._major("t", torch.zeros(6, 1)) == (1, 0)
+    assert ops._major("t", torch.zeros(1, 0).expand(6, 0)) == (1, 0)
+
+
+def test_a_pitch_of_zero_is_for_matrices_that_are_only_read(lib):
+    def backward(**kw):
+        a = dict(ldg=64, ldy=64, ldd=64)
+        a.update(kw)
+        return lib.gemm_combine_backward(4, 2, 64, 8, 1, P, a["ldg"], P << 1, a["ldy"], P << 2, P << 3, P << 4, P << 5,
+                                         a["ldd"], P << 6, None)
+
+    def route_backward(ldl, ldd):
+        return lib.gemm_route_backward(4, 16, 0, P, ldl, how(), P << 2, P << 3, P << 4, ldd, None)
+    for call in (lambda: quant(lib, ldx=0), lambda: route(lib, ldl=0), lambda: route_backward(0, 16),
+                 lambda: combine(lib, ldy=0), lambda: backward(ldg=0), lambda: backward(ldy=0)):
+        assert call() != tg.GEMM_OK               # (the addresses are no device's)
+        assert "leading" not in tg.gemm_last_error()
+    for call in (lambda: quant(lib, ldq=0), lambda: route_backward(16, 0), lambda: combine(lib, ldo=0),
+                 lambda: backward(ldd=0), lambda: scaled(lib, lda=0), lambda: scaled(lib, ldc=0),
+                 lambda: experts(lib, lda=0), lambda: experts(lib, ldc=0)):
+        refused(call(), "leading")

@@ -225,7 +225,7 @@ int gemm_combine(int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows, in
     int rc = check_sizes(tokens, top_k, hidden, rows, type);
     if (rc) return rc;
     const int64_t kLdMax = 1LL << 36;
-    if (ldy < hidden || ldo < hidden || ldy > kLdMax || ldo > kLdMax)
+    if (!op_read_pitch_ok(ldy, hidden) || ldo < hidden || ldo > kLdMax)
         return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
     if (tokens == 0 || hidden == 0) return GEMM_OK;
     const int eb = op_type_bytes(type);
@@ -266,7 +266,7 @@ int gemm_combine_backward(int64_t tokens, int64_t top_k, int64_t hidden, int64_t
     int rc = check_sizes(tokens, top_k, hidden, rows, type);
     if (rc) return rc;
     const int64_t kLdMax = 1LL << 36;
-    if (ldg < hidden || ldy < hidden || ldd < hidden || ldg > kLdMax || ldy > kLdMax || ldd > kLdMax)
+    if (!op_read_pitch_ok(ldg, hidden) || !op_read_pitch_ok(ldy, hidden) || ldd < hidden || ldd > kLdMax)
         return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
     if (order && rows != tokens * top_k)
         return api_error(GEMM_ERR_INVALID_ARG, "order needs rows = tokens * top_k");

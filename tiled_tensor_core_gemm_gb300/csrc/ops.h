@@ -30,6 +30,10 @@ inline uint64_t op_extent(int64_t rows, int64_t cols, int64_t ld, int elem) {
     return rows > 0 && cols > 0 ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * (uint64_t)elem : 0;
 }
 
+// The pitch of a matrix that is only read, row by row: 0 (one row stands for
+// all) or at least a row.
+inline bool op_read_pitch_ok(int64_t ld, int64_t cols) { return (ld == 0 || ld >= cols) && ld <= (1LL << 36); }
+
 // Checks the spans (NULL, alignment, a written span overlapping another) before
 // any CUDA call, then that the current device is one this library serves and
 // that every span is its memory.  Returns a gemm_status_t; *sms as asked.

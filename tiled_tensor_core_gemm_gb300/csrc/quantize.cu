@@ -232,7 +232,7 @@ extern "C" int gemm_quantize_block(int64_t batch, int64_t rows, int64_t cols, in
         return api_error(GEMM_ERR_INVALID_ARG, "size out of range (0 <= rows, cols < 2^31, batch <= 65535)");
     const int64_t mb = block == GEMM_BLOCK_ROW ? rows : (rows + 127) / 128;
     const int64_t nb = block == GEMM_BLOCK_COL ? cols : (cols + 127) / 128;
-    if (ldx < cols || ldq < cols || ldx > kLdMax || ldq > kLdMax)
+    if (!op_read_pitch_ok(ldx, cols) || ldq < cols || ldq > kLdMax)
         return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
     if (x_stride < 0 || q_stride < 0 || s_row < 0 || s_col < 0 || s_batch < 0 || x_stride > (1LL << 46) ||
         q_stride > (1LL << 46) || s_row > kLdMax || s_col > kLdMax || s_batch > (1LL << 46))

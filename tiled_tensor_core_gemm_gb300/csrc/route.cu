@@ -557,7 +557,7 @@ int check_route(int64_t tokens, int64_t experts, int type, int64_t ldl, const ge
     if (tokens < 0 || tokens > 0x7fffffffLL - 64) return api_error(GEMM_ERR_INVALID_ARG, "tokens out of range");
     if (experts < 1 || experts > kMaxExperts)
         return api_error(GEMM_ERR_INVALID_ARG, "experts must be in [1, 1024]");
-    if (ldl < experts || ldl > (1LL << 36)) return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
+    if (!op_read_pitch_ok(ldl, experts)) return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
     if (how->score != GEMM_SCORE_SOFTMAX && how->score != GEMM_SCORE_SIGMOID)
         return api_error(GEMM_ERR_INVALID_ARG, "unknown score");
     if (how->group_score != GEMM_GROUP_MAX && how->group_score != GEMM_GROUP_TOP2)

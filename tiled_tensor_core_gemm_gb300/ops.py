@@ -5,7 +5,9 @@ the weighted combination of the experts' rows.
 Each function checks shapes and types, allocates the outputs it is not given,
 and makes one call of the C ABI in include/gemm_ops.h (which has the formulas);
 every step of the computation runs in the library's CUDA kernels on the current
-stream (or ``stream``, a cudaStream_t as int).  There is no CPU path.
+stream (or ``stream``, a cudaStream_t as int).  There is no CPU path.  Inputs
+that are read row by row (x, logits, Y, grad) may be one row expanded over all;
+operands of a product and outputs may not (ValueError).
 
 A dense layer Y = X W^T (X: tokens x K, W: N x K) and its gradients, every
 operand read as it was stored:
@@ -121,12 +123,21 @@ def _cuda(first, *others):
     return index
 
 
-def _rows(name, t, rows, cols):
-    """Row pitch of a rows x cols tensor with unit stride along its columns."""
+def _rows(name, t, rows, cols, shared=False):
+    """Row pitch of a rows x cols tensor with unit stride along its columns.
+
+    shared: the operator reads row by row, so that the rows may be one row's
+    memory (a row expanded, as autograd hands back the gradient of a sum over
+    them); the pitch is then 0.  Matrices that are written or read by TMA may not.
+    """
     sr, sc = t.stride()
     if cols > 1 and sc != 1:
         raise ValueError(f"{name} must have unit stride along its columns")
-    return sr if rows > 1 and sr > 0 else (cols or 1)
+    if rows <= 1 or cols == 0:
+        return cols or 1
+    if sr == 0 and not shared:
+        raise ValueError(f"{name} must have rows of its own (it is one row expanded)")
+    return sr
 
 
 def _dense(name, t, shape, dtype):
@@ -139,18 +150,18 @@ def _major(name, t):
     rows, cols = t.shape[-2:]
     sr, sc = t.stride()[-2:]
     if sc == 1 or cols <= 1:
-        if rows <= 1:
+        if rows <= 1 or cols == 0:
             return max(cols, 1), 0
         if sc == 1 and sr >= cols:
             return sr, 0
-        if cols <= 1 and sr != 1:
-            return max(sr, 1), 0
+        if cols == 1 and sr > 1:
+            return sr, 0
     if sr == 1 or rows <= 1:
-        if cols <= 1:
+        if cols <= 1 or rows == 0:
             return max(rows, 1), 1
         if sc >= rows:
             return sc, 1
-    raise ValueError(f"{name} must be row-major or the transpose of a row-major matrix")
+    raise ValueError(f"{name} must be row-major or the transpose of a row-major matrix, not expanded")
 
 
 def _scale(name, s, f32, extent, num_kb, k_dim, tiles_ok):
@@ -221,7 +232,7 @@ def quantize_block(x, block="row", dtype="e4m3", scatter=None, out_rows=None, st
     batch = shape[0] if dims == 3 else 1
     if n > 1 and stride[-1] != 1:
         raise ValueError("x must have unit stride along its columns")
-    ldx = max(stride[-2] if m > 1 else n, 1)
+    ldx = stride[-2] if m > 1 and n > 0 else n or 1     # (0: one row expanded, which is read as it is)
     rows, copies, slots = m, 1, None
     if scatter is not None:
         if dims != 2 or code != 0:
@@ -384,7 +395,7 @@ def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, 
     weights = empty(shape, dtype=torch.float32, device=device)
     order = empty(tokens * top_k, dtype=i32, device=device)
     offsets = empty(experts + 1, dtype=i32, device=device)
-    rc = lib.gemm_route(tokens, experts, kind, logits.data_ptr(), _rows("logits", logits, tokens, experts),
+    rc = lib.gemm_route(tokens, experts, kind, logits.data_ptr(), _rows("logits", logits, tokens, experts, True),
                         bias.data_ptr() if bias is not None else None, how, indices.data_ptr(), weights.data_ptr(),
                         offsets.data_ptr(), order.data_ptr(), slots.data_ptr(), raw(index) if stream is None else stream)
     if rc:
@@ -410,7 +421,7 @@ def route_backward(grad_weights, logits, indices, score="softmax", renormalize=T
     _dense("indices", indices, shape, torch.int32)
     _dense("grad_weights", grad_weights, shape, torch.float32)
     out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-    rc = lib.gemm_route_backward(tokens, experts, kind, logits.data_ptr(), _rows("logits", logits, tokens, experts),
+    rc = lib.gemm_route_backward(tokens, experts, kind, logits.data_ptr(), _rows("logits", logits, tokens, experts, True),
                                  _how(shape[1], score, 1, 1, "max", renormalize, scale), indices.data_ptr(),
                                  grad_weights.data_ptr(), out.data_ptr(), experts or 1,
                                  raw(index) if stream is None else stream)
@@ -446,7 +457,7 @@ def combine(Y, slots, weights: Optional["torch.Tensor"] = None, out=None, stream
         raise TypeError(f"out must be a ({tokens}, {hidden}) {Y.dtype} tensor")
     else:
         ldo = _rows("out", out, tokens, hidden)
-    rc = lib.gemm_combine(tokens, top_k, hidden, rows, kind, Y.data_ptr(), _rows("Y", Y, rows, hidden),
+    rc = lib.gemm_combine(tokens, top_k, hidden, rows, kind, Y.data_ptr(), _rows("Y", Y, rows, hidden, True),
                           slots.data_ptr(), weights.data_ptr() if weights is not None else None, out.data_ptr(), ldo,
                           raw(index) if stream is None else stream)
     if rc:
@@ -489,7 +500,7 @@ def combine_backward(grad, Y, slots, weights, order=None, stream=None):
             dY = torch.zeros((rows, hidden), dtype=Y.dtype, device=Y.device)
     dw = torch.empty(shape, dtype=torch.float32, device=Y.device)
     rc = lib.gemm_combine_backward(tokens, top_k, hidden, rows, kind, grad.data_ptr(),
-                                   _rows("grad", grad, tokens, hidden), Y.data_ptr(), _rows("Y", Y, rows, hidden),
+                                   _rows("grad", grad, tokens, hidden, True), Y.data_ptr(), _rows("Y", Y, rows, hidden, True),
                                    slots.data_ptr(), weights.data_ptr(), order.data_ptr() if order is not None else None,
                                    dY.data_ptr(), hidden or 1, dw.data_ptr(), raw(index) if stream is None else stream)
     if rc:
