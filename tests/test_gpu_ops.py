@@ -846,3 +846,36 @@ def test_expanded_rows_are_refused_where_they_are_written_or_go_through_tma():
                  lambda: tg.combine(randn(8, 64), slots, out=one)):
         with pytest.raises(ValueError, match="expanded"):
             call()
+
+
+# ------------------------------------------------ NaN and infinity through an activation ---
+# on this device: tiles of 16 columns, the same with K in ranges, 64 columns, 128 x 128, and the two
+# pair tiles; the last has a pitch of C that TMA cannot store to
+@pytest.mark.parametrize("M,N,K", [(6, 200, 400), (6, 256, 4096), (50, 300, 1024), (140, 200, 400), (2600, 2296, 1000),
+                                   (2000, 2001, 2100)])
+@pytest.mark.parametrize("act", ("relu", "gelu"))
+@pytest.mark.parametrize("out", ("f32", "bf16"))
+def test_scaled_a_nan_or_infinity_passes_the_activation(M, N, K, act, out):
+    x = randn(M, K, seed=300)
+    x[2, 130], x[4, 259] = math.nan, math.inf
+    A, sa = tg.quantize_block(x, "row")
+    B, sb = made(N, K, "tile", "e4m3", 310)
+    got = tg.gemm_scaled(A, sa, B.t(), sb.t(), act=act, out=out)
+    keep = [i for i in range(M) if i not in (2, 4)]
+    assert bool(got[2].isnan().all()) and bool(got[4].isnan().all())
+    check_product(got[keep], A[keep], B.t(), sa[keep], sb.t(), out, act=act)
+
+
+@pytest.mark.parametrize("counts", ([1, 5, 0, 3], [60, 70, 0, 100], [300, 0, 257, 129]))
+@pytest.mark.parametrize("act", ("relu", "gelu"))
+def test_experts_a_nan_or_infinity_passes_the_activation(counts, act):
+    E, R, N, K = len(counts), sum(counts), 260, 300
+    x = randn(R, K, seed=320)
+    x[2, 130], x[4, 259] = math.nan, math.inf
+    A, sa = tg.quantize_block(x, "row")
+    W, sw = tg.quantize_block(randn(E, N, K, seed=321), "tile")
+    off = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    got = tg.gemm_experts(A, sa, W.transpose(1, 2), sw.transpose(1, 2), off, act=act)
+    assert bool(got[2].isnan().all()) and bool(got[4].isnan().all())
+    keep = [i for i in range(R) if i not in (2, 4)]
+    assert bool(torch.isfinite(got[keep]).all())

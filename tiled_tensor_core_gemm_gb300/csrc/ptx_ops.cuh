@@ -45,6 +45,13 @@ __device__ __forceinline__ void mma_f8_sw128(uint32_t d_tmem, uint32_t pd, uint3
             ::"r"(d_tmem), "r"(pd), "r"(qd), "r"(kHigh), "r"(idesc), "r"(acc) : "memory");
 }
 
+// max(x, 0) that keeps a NaN (fmaxf gives 0 for it).
+__device__ __forceinline__ float relu_nan(float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // 2^x to about 2^-22 relative; 0 for x below -126.
 __device__ __forceinline__ float exp2_approx(float x) {
     float r;

@@ -333,7 +333,7 @@ __device__ __forceinline__ float finish(const EpiParams &e, float acc, float old
     float y = e.alpha * acc;
     if (e.beta != 0.f) y = fmaf(e.beta, old, y);
     y += bias;
-    if (e.act == GEMM_ACT_RELU) y = fmaxf(y, 0.f);
+    if (e.act == GEMM_ACT_RELU) y = ptx::relu_nan(y);
     else if (e.act == GEMM_ACT_GELU) y = gelu2(make_float2(y, y)).x;
     return y;
 }
@@ -433,7 +433,7 @@ __device__ __forceinline__ void write_rows(const ScaledParams &p, const CUtensor
             }
             if (p.epi.act == GEMM_ACT_RELU) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) acc[c] = fmaxf(acc[c], 0.f);
+                for (int c = 0; c < 32; ++c) acc[c] = ptx::relu_nan(acc[c]);
             } else if (p.epi.act == GEMM_ACT_GELU) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
