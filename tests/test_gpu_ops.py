@@ -879,3 +879,23 @@ def test_experts_a_nan_or_infinity_passes_the_activation(counts, act):
     assert bool(got[2].isnan().all()) and bool(got[4].isnan().all())
     keep = [i for i in range(R) if i not in (2, 4)]
     assert bool(torch.isfinite(got[keep]).all())
+
+
+# expf within 2 units in the last place twice, four additions and divisions, three products, each half a
+# unit: under 16 * 2^-24 of the gradient itself (and what is below the type's normal numbers)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_route_backward_of_large_sigmoid_logits_is_relatively_exact(dtype):
+    k = 16
+    x = torch.linspace(-30, 30, 61, device="cuda").to(dtype)[torch.randperm(61, generator=gen(90), device="cuda")]
+    x = torch.stack([x.roll(i) for i in range(61)])
+    idx = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :k].to(torch.int32)    # 15 .. 30
+    idx[::2] = torch.sort(x, dim=1, stable=True).indices[::2, :k].to(torch.int32)              # -30 .. -15
+    g = randn(61, k, seed=91)
+    got = tg.route_backward(g, x, idx, score="sigmoid", renormalize=False, scale=2.0).double()
+    sel = x.double().gather(1, idx.long())
+    want = torch.zeros_like(x, dtype=torch.float64)
+    want.scatter_(1, idx.long(), 2.0 * g.double() * torch.sigmoid(sel) * torch.sigmoid(-sel))
+    half = 0.0 if dtype == torch.float32 else HALF[dtype]
+    tol = (16 * 2.0 ** -24 + half) * want.abs() + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+    assert bool(((got - want).abs() <= tol).all())
+    assert bool((got.gather(1, idx.long()) != 0).all()) or dtype == torch.float16

@@ -4,7 +4,7 @@
 //   s = softmax(x) or 1 / (1 + exp(-x)),  key = s + b (x itself without b),
 //   w_j = scale * s_j / sum_i s_i  over the chosen experts (or scale * s_j).
 //   ds_j = scale * (g_j - sum_i g_i s_i / Z) / Z, Z = sum_i s_i (or scale * g_j),
-//   dx = s * (ds - sum ds * s)  (softmax)  or  ds * s * (1 - s)  (sigmoid).
+//   dx = s * (ds - sum ds * s)  (softmax)  or  ds * s(x) * s(-x)  (sigmoid).
 //
 // One warp takes a token and holds its row in registers, four neighbouring
 // experts a lane and step.  Keys are compared as unsigned integers in the order
@@ -526,9 +526,11 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteParams p
         ds[i + 3] = v.w;
     }
     if (p.score == GEMM_SCORE_SIGMOID) {
-        // (only the chosen experts' scores count)
+        // s (1 - s), for the chosen experts only.  1 - s is the sigmoid of -x: from the
+        // rounded s it would lose its digits as x grows, and be 0 from x = 17 on.
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s[i] = ds[i] != 0.f ? score_of(p.score, x[i], m, z) : 0.f;
+        for (int i = 0; i < EPL; ++i)
+            s[i] = ds[i] != 0.f ? score_of(p.score, x[i], m, z) * (1.f / (1.f + expf(x[i]))) : 0.f;
     }
     T *out = static_cast<T *>(p.dlogits) + (int64_t)t * p.ldd;
 #pragma unroll
@@ -537,8 +539,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteParams p
         struct alignas(4 * sizeof(T)) V4 { T v[4]; } v;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float d = p.score == GEMM_SCORE_SIGMOID ? ds[i + k] * s[i + k] * (1.f - s[i + k])
-                                                          : s[i + k] * (ds[i + k] - sum);
+            const float d = p.score == GEMM_SCORE_SIGMOID ? ds[i + k] * s[i + k] : s[i + k] * (ds[i + k] - sum);
             v.v[k] = OpType<T>::down(d);
         }
         if (p.d_wide && e < p.experts) {
