@@ -114,8 +114,9 @@ GEMM_API int gemm_run_scaled(int64_t M, int64_t N, int64_t K, int dtype, const v
  *                b_scale_expert elements further each
  *   epi          alpha, activation and output type; beta 0 and no bias
  * B's base, pitch and b_expert must be multiples of 16 bytes
- * (GEMM_ERR_UNSUPPORTED otherwise: weights are laid out once); A is copied
- * into a workspace where it is not.  At most 1024 experts.
+ * (GEMM_ERR_UNSUPPORTED otherwise: weights are laid out once; an expert of one
+ * stored row has no pitch); A is copied into a workspace where it is not.  At
+ * most 1024 experts.
  */
 GEMM_API int gemm_run_experts(int64_t rows, int64_t N, int64_t K, int64_t experts, int dtype, const void *A,
                               int64_t lda, const gemm_block_scale_t *a_scale, const int32_t *offsets, const void *B,

@@ -899,3 +899,15 @@ def test_route_backward_of_large_sigmoid_logits_is_relatively_exact(dtype):
     tol = (16 * 2.0 ** -24 + half) * want.abs() + (2.0 ** -25 if dtype == torch.float16 else 0.0)
     assert bool(((got - want).abs() <= tol).all())
     assert bool((got.gather(1, idx.long()) != 0).all()) or dtype == torch.float16
+
+
+@pytest.mark.parametrize("counts", ([3, 0, 9], [200, 1, 300]))
+@pytest.mark.parametrize("N,K,major", [(1, 100, "k"), (77, 1, "n"), (1, 1, "k"), (1, 1, "n"), (1, 333, "n"), (77, 1, "k")])
+def test_experts_of_one_row_or_column(counts, N, K, major):
+    E, R = len(counts), sum(counts)
+    off = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    A, sa = made(R, K, "row", "e4m3", 270)
+    W, sw = tg.quantize_block(randn(E, *((N, K) if major == "k" else (K, N)), seed=271), "tile")
+    if major == "k":
+        W, sw = W.transpose(1, 2), sw.transpose(1, 2)
+    check_experts(tg.gemm_experts(A, sa, W, sw, off), A, sa, W, sw, off, "f32")

@@ -284,3 +284,12 @@ def test_a_pitch_of_zero_is_for_matrices_that_are_only_read(lib):
                  lambda: backward(ldd=0), lambda: scaled(lib, lda=0), lambda: scaled(lib, ldc=0),
                  lambda: experts(lib, lda=0), lambda: experts(lib, ldc=0)):
         refused(call(), "leading")
+
+
+def test_experts_of_one_stored_row_have_no_pitch(lib):
+    # N = 1, K-major, and K = 1, N-major, at extents that are no multiple of 16
+    for kw in (dict(N=1, K=100, lda=112, ldb=100, be=112, ldc=1), dict(N=77, K=1, lda=16, ldb=77, be=80, bm=0, ldc=77)):
+        rc = experts(lib, **kw)
+        assert rc != tg.GEMM_ERR_UNSUPPORTED and "16 bytes" not in tg.gemm_last_error()
+    assert experts(lib, N=1, K=100, lda=112, ldb=100, be=100, ldc=1) == tg.GEMM_ERR_UNSUPPORTED
+    assert experts(lib, N=2, K=100, lda=112, ldb=100, be=256, ldc=2) == tg.GEMM_ERR_UNSUPPORTED

@@ -1315,11 +1315,12 @@ int gemm_run_experts(int64_t rows, int64_t N, int64_t K, int64_t experts, int dt
     if ((rc = check_scale("b_scale", b_scale, true, N, num_kb, experts, b_scale_expert, &spans[5]))) return rc;
     if (rows == 0 || N == 0) return GEMM_OK;
     plan_operand(&a);
-    if (num_kb > 0 && ((uintptr_t)B % 16 != 0 || ldb % 16 != 0 || b_expert % 16 != 0))
+    if (b.rows <= 1) b.ld = round_up(b.cols, 16);       // (the pitch of a single row is nobody's)
+    if (num_kb > 0 && ((uintptr_t)B % 16 != 0 || b.ld % 16 != 0 || b_expert % 16 != 0))
         return api_error(GEMM_ERR_UNSUPPORTED, "B's base, pitch and b_expert must be multiples of 16 bytes");
     int sms = 0;
     if ((rc = op_check(spans, 6, &sms))) return rc;
-    b.ld_use = ldb;
+    b.ld_use = b.ld;
     ScaledPlan pl = plan_experts(rows, N, num_kb, experts, b_major != 0, b_scale->block == 128, sms);
     if (!pl.swap) pl.qvec = b_scale->block != 128;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
