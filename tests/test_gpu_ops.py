@@ -911,3 +911,43 @@ def test_experts_of_one_row_or_column(counts, N, K, major):
     if major == "k":
         W, sw = W.transpose(1, 2), sw.transpose(1, 2)
     check_experts(tg.gemm_experts(A, sa, W, sw, off), A, sa, W, sw, off, "f32")
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import torch
+import tiled_tensor_core_gemm_gb300 as tg
+gen = torch.Generator(device="cuda")
+gen.manual_seed(1)
+rand = lambda *s: torch.randn(s, generator=gen, device="cuda")
+logits, more, x = rand(300, 16), rand(300, 16), rand(300, 256).to(torch.bfloat16)
+held = torch.zeros(300 * 257, dtype=torch.uint8, device="cuda")
+def layer():
+    r = tg.route(logits, 3)                                       # takes a workspace
+    a = held.view(300, 257)[:, :256].view(torch.float8_e4m3fn)    # TMA cannot address its rows: another
+    one = torch.ones(300, 2, device="cuda")
+    q, s = tg.quantize_block(x, "row")
+    return r, tg.gemm_scaled(a, one, q.t(), s.t())
+held.copy_(rand(300 * 257).to(torch.float8_e4m3fn).view(torch.uint8))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    r, c = layer()
+logits.copy_(more)
+for _ in range(3):
+    graph.replay()
+torch.cuda.synchronize()
+got, gc = [t.clone() for t in r], c.clone()
+want, wc = layer()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(gc, wc)
+assert bool(torch.isfinite(wc).all())
+print("equal")
+"""
+
+
+def test_the_first_call_may_be_in_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "equal" in run.stdout, run.stderr[-2000:]

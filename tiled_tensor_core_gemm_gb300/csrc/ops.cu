@@ -17,16 +17,22 @@ cudaError_t op_malloc(void **p, size_t bytes, int dev, cudaStream_t stream) {
             props.allocType = cudaMemAllocationTypePinned;
             props.location.type = cudaMemLocationTypeDevice;
             props.location.id = dev;
-            cudaMemPool_t made = nullptr;
-            cudaError_t e = cudaMemPoolCreate(&made, &props);
+            // The first call may come while this or another thread captures a graph.
+            // Creating a pool is not a stream's work, so the capture need not forbid it.
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+            cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
             if (e != cudaSuccess) return e;
-            uint64_t keep = 256ull << 20;
-            e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
-            if (e != cudaSuccess) {
-                cudaMemPoolDestroy(made);
-                return e;
+            cudaMemPool_t made = nullptr;
+            e = cudaMemPoolCreate(&made, &props);
+            if (e == cudaSuccess) {
+                uint64_t keep = 256ull << 20;
+                e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
+                if (e != cudaSuccess) cudaMemPoolDestroy(made);
             }
-            pools[dev] = made;
+            const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+            if (e == cudaSuccess) pools[dev] = made;
+            if (e == cudaSuccess) e = back;
+            if (e != cudaSuccess) return e;
         }
         pool = pools[dev];
     }
