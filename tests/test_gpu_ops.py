@@ -951,3 +951,42 @@ def test_the_first_call_may_be_in_a_capture():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     run = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and "equal" in run.stdout, run.stderr[-2000:]
+
+
+# Tensors that end where their allocation does (each is one of its own here), at sizes no multiple of 16 bytes.
+ROWS_THAT_END_THEIR_ALLOCATION = """
+import torch
+import tiled_tensor_core_gemm_gb300 as tg
+gen = torch.Generator(device="cuda")
+gen.manual_seed(1)
+rand = lambda *s: torch.randn(s, generator=gen, device="cuda")
+def roomy(t):
+    held = torch.zeros(t.numel() + 64, dtype=t.dtype, device="cuda")
+    held[:t.numel()] = t.reshape(-1)
+    return held[:t.numel()].view(t.shape)
+def same(a, b):
+    plain = lambda t: t.clone(memory_format=torch.contiguous_format).view(torch.uint8)
+    return all(torch.equal(plain(x), plain(y)) for x, y in zip(a, b))
+for dtype in (torch.float32, torch.bfloat16, torch.float16):
+    for T, k, H in ((1, 1, 5), (3, 1, 77), (5, 2, 131), (37, 3, 1001)):
+        y, g, w = rand(T * k, H).to(dtype), rand(T, H).to(dtype), rand(T, k)
+        slots = torch.randperm(T * k, generator=gen, device="cuda").view(T, k).to(torch.int32)
+        assert y.numel() * y.element_size() % 16 and y.data_ptr() % 256 == 0
+        assert same([tg.combine(y, slots, w)], [tg.combine(roomy(y), slots, w)])
+        assert same(tg.combine_backward(g, y, slots, w), tg.combine_backward(roomy(g), roomy(y), slots, w))
+        for block in ("row", "col", "tile"):
+            assert same(tg.quantize_block(y, block), tg.quantize_block(roomy(y), block))
+        assert same(tg.quantize_block(g, "row", scatter=slots), tg.quantize_block(roomy(g), "row", scatter=slots))
+torch.cuda.synchronize()
+print("equal")
+"""
+
+
+def test_rows_that_end_their_allocation():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", ROWS_THAT_END_THEIR_ALLOCATION], cwd=root, capture_output=True, text=True,
+                         timeout=300, env=dict(os.environ, PYTORCH_NO_CUDA_MEMORY_CACHING="1"))
+    assert run.returncode == 0 and "equal" in run.stdout, run.stderr[-2000:]

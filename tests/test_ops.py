@@ -3,6 +3,7 @@ functions refuse, before any CUDA call, and what they do for nothing."""
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -293,3 +294,52 @@ def test_experts_of_one_stored_row_have_no_pitch(lib):
         assert rc != tg.GEMM_ERR_UNSUPPORTED and "16 bytes" not in tg.gemm_last_error()
     assert experts(lib, N=1, K=100, lda=112, ldb=100, be=100, ldc=1) == tg.GEMM_ERR_UNSUPPORTED
     assert experts(lib, N=2, K=100, lda=112, ldb=100, be=256, ldc=2) == tg.GEMM_ERR_UNSUPPORTED
+
+
+# The blocks a shifted load touches (from the aligned address at or before the first element, 16 bytes at a
+# time, while they hold an element), for every chunk of eight of the last row, against the allocation's end.
+ACCESS_PROGRAM = r"""
+#include "ops.h"
+#include <cstdio>
+using namespace tcgemm;
+int main() {
+    const uint64_t base = 1 << 20;
+    long exact = 0, shifted = 0;
+    for (int elem = 2; elem <= 4; elem += 2)
+        for (int off = 0; off < 16; off += elem)
+            for (int cols = 1; cols <= 40; ++cols)
+                for (int slack = 0; slack <= 20; ++slack) {
+                    OpSpan s = {"X", reinterpret_cast<void *>(base + off), (uint64_t)cols * elem, elem, false};
+                    s.memory_end = base + off + s.bytes + slack;
+                    uint64_t last = 0;
+                    for (int c = 0; c < cols; c += 8) {
+                        const uint64_t at = base + off + (uint64_t)c * elem, have = cols - c < 8 ? cols - c : 8;
+                        for (uint64_t b = at & ~15ull; b < at + have * elem; b += 16) last = b + 16;
+                    }
+                    const int how = op_access(false, &s, 1);
+                    if (op_access(true, &s, 1) != kOpWide || how != (last > s.memory_end ? kOpExact : kOpShifted)) {
+                        printf("elem %d off %d cols %d slack %d: %d\n", elem, off, cols, slack, how);
+                        return 1;
+                    }
+                    ++(how == kOpExact ? exact : shifted);
+                }
+    OpSpan two[2] = {{"Y", reinterpret_cast<void *>(base), 64, 2, false}, {"Z", reinterpret_cast<void *>(base + 128), 10, 2, false}};
+    two[0].memory_end = two[1].memory_end = base + 138;
+    if (op_access(false, two, 1) != kOpShifted || op_access(false, two, 2) != kOpExact) return 1;
+    two[1].bytes = 0;
+    if (op_access(false, two, 2) != kOpShifted) return 1;
+    printf("%ld exact, %ld shifted\n", exact, shifted);
+    return exact && shifted ? 0 : 1;
+}
+"""
+
+
+def test_shifted_loads_are_not_taken_past_the_end_of_an_allocation(tmp_path):
+    src = tmp_path / "access.cpp"
+    src.write_text(ACCESS_PROGRAM)
+    cuda = os.path.dirname(os.path.dirname(tgbuild._nvcc()))
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(ROOT, "include"),
+                    "-I", os.path.join(ROOT, "tiled_tensor_core_gemm_gb300", "csrc"),
+                    "-I", os.path.join(cuda, "include"), str(src), "-o", str(tmp_path / "access")], check=True)
+    run = subprocess.run([str(tmp_path / "access")], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout

@@ -23,7 +23,7 @@ constexpr int kThreads = 512;  // at most
 // Rows of a token taken together (their loads in flight at once), and the blocks
 // of kThreads an SM is to hold: what fits the registers.
 template <typename T> constexpr int chunk_of() { return sizeof(T) == 2 ? 8 : 4; }
-template <typename T, bool WIDE> constexpr int blocks_of() { return sizeof(T) == 2 && WIDE ? 2 : 1; }
+template <typename T, int ACCESS> constexpr int blocks_of() { return sizeof(T) == 2 && ACCESS == kOpWide ? 2 : 1; }
 
 struct CombineParams {
     const void *Y, *grad;
@@ -51,8 +51,8 @@ __device__ __forceinline__ void pair_of(const CombineParams &p, int64_t t, int j
 
 // Units are (token, segment of the hidden dimension); a block strides over them
 // and has the next unit's slots and weights on their way while it sums this one.
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_kernel(const CombineParams p) {
+template <typename T, int ACCESS>
+__global__ void __launch_bounds__(kThreads, (blocks_of<T, ACCESS>())) combine_kernel(const CombineParams p) {
     constexpr int kChunk = chunk_of<T>();
     pdl_enter();
     const int lane = threadIdx.x & 31, j_of = lane & (kChunk - 1);
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_kern
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) {
                 const int32_t s = __shfl_sync(0xffffffffu, slot, j);
-                y[j] = op_load8<WIDE, T>(Y + (int64_t)(s < 0 ? 0 : s) * p.ldy + h, s < 0 ? 0 : have);
+                y[j] = op_load8<ACCESS, T>(Y + (int64_t)(s < 0 ? 0 : s) * p.ldy + h, s < 0 ? 0 : have);
             }
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) {
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_kern
         OpVec8<T> o;
 #pragma unroll
         for (int k = 0; k < 8; ++k) o.v[k] = OpType<T>::down(acc[k]);
-        op_store8<WIDE, T>(static_cast<T *>(p.out) + t * p.ldo + h, o, have);
+        op_store8<ACCESS == kOpWide, T>(static_cast<T *>(p.out) + t * p.ldo + h, o, have);
         slot = next_slot;
         weight = next_weight;
     }
@@ -116,8 +116,8 @@ __device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
 }
 
 // A block takes a token at a time, striding over them.
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_backward_kernel(const CombineParams p) {
+template <typename T, int ACCESS>
+__global__ void __launch_bounds__(kThreads, (blocks_of<T, ACCESS>())) combine_backward_kernel(const CombineParams p) {
     constexpr int kChunk = chunk_of<T>();
     pdl_enter();
     __shared__ float s_part[2][kThreads / 32][8];
@@ -140,12 +140,12 @@ __global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_back
             for (int j = 0; j < 8; ++j) dot[j] = 0.f;
             for (int64_t h = (int64_t)threadIdx.x * 8; h - threadIdx.x * 8 < p.hidden; h += (int64_t)blockDim.x * 8) {
                 const int have = h < p.hidden ? (int)(p.hidden - h < 8 ? p.hidden - h : 8) : 0;
-                const OpVec8<T> g = op_load8<WIDE, T>(G + h, have);
+                const OpVec8<T> g = op_load8<ACCESS, T>(G + h, have);
                 OpVec8<T> y[kChunk];
 #pragma unroll
                 for (int j = 0; j < kChunk; ++j) {
                     const int32_t s = __shfl_sync(0xffffffffu, slot, j);
-                    y[j] = op_load8<WIDE, T>(Y + (int64_t)(s < 0 ? 0 : s) * p.ldy + h, s < 0 ? 0 : have);
+                    y[j] = op_load8<ACCESS, T>(Y + (int64_t)(s < 0 ? 0 : s) * p.ldy + h, s < 0 ? 0 : have);
                 }
 #pragma unroll
                 for (int j = 0; j < kChunk; ++j) {
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_back
                         d.v[k] = OpType<T>::down(w * gk);
                         dot[j] = fmaf(gk, OpType<T>::up(y[j].v[k]), dot[j]);
                     }
-                    op_store8<WIDE, T>(D + (int64_t)s * p.ldo + h, d, have);
+                    op_store8<ACCESS == kOpWide, T>(D + (int64_t)s * p.ldo + h, d, have);
                 }
             }
             const float sum = warp_sum8(dot, lane);
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, (blocks_of<T, WIDE>())) combine_back
 #pragma unroll
                 for (int k = 0; k < 8; ++k) z.v[k] = OpType<T>::down(0.f);
                 for (int64_t h = (int64_t)threadIdx.x * 8; h < p.hidden; h += (int64_t)blockDim.x * 8)
-                    op_store8<WIDE, T>(row + h, z, (int)(p.hidden - h < 8 ? p.hidden - h : 8));
+                    op_store8<ACCESS == kOpWide, T>(row + h, z, (int)(p.hidden - h < 8 ? p.hidden - h : 8));
             }
         }
         slot = next_slot;
@@ -229,7 +229,7 @@ int gemm_combine(int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows, in
         return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
     if (tokens == 0 || hidden == 0) return GEMM_OK;
     const int eb = op_type_bytes(type);
-    const OpSpan spans[] = {{"Y", Y, op_extent(rows, hidden, ldy, eb), eb, false},
+    OpSpan spans[] = {{"Y", Y, op_extent(rows, hidden, ldy, eb), eb, false},
                             {"slots", slots, (uint64_t)(tokens * top_k) * 4, 4, false},
                             {"weights", weights, weights ? (uint64_t)(tokens * top_k) * 4 : 0, 4, false},
                             {"out", out, op_extent(tokens, hidden, ldo, eb), eb, true}};
@@ -251,7 +251,7 @@ int gemm_combine(int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows, in
     p.segments = (int)((hidden + threads * 8 - 1) / (threads * 8));
     const dim3 grid = grid_for(tokens * p.segments, threads, sms);
     const cudaError_t e = op_by_type(type, [&](auto t) {
-        return op_by_flag(wide, [&](auto w) {
+        return op_by_access(op_access(wide, spans, 1), [&](auto w) {
             return launch_pdl(combine_kernel<decltype(t), decltype(w)::value>, grid, dim3(threads), 0,
                               reinterpret_cast<cudaStream_t>(stream_), p);
         });
@@ -273,7 +273,7 @@ int gemm_combine_backward(int64_t tokens, int64_t top_k, int64_t hidden, int64_t
     if (tokens == 0) return GEMM_OK;
     const int eb = op_type_bytes(type);
     const uint64_t pairs = (uint64_t)(tokens * top_k) * 4;
-    const OpSpan spans[] = {{"grad", grad, op_extent(tokens, hidden, ldg, eb), eb, false},
+    OpSpan spans[] = {{"grad", grad, op_extent(tokens, hidden, ldg, eb), eb, false},
                             {"Y", Y, op_extent(rows, hidden, ldy, eb), eb, false},
                             {"slots", slots, pairs, 4, false},
                             {"weights", weights, pairs, 4, false},
@@ -300,7 +300,7 @@ int gemm_combine_backward(int64_t tokens, int64_t top_k, int64_t hidden, int64_t
     const bool wide = hidden % 8 == 0 && op_wide(Y, ldy, eb) && op_wide(grad, ldg, eb) && op_wide(dY, ldd, eb);
     const int threads = threads_for(hidden);
     const cudaError_t e = op_by_type(type, [&](auto t) {
-        return op_by_flag(wide, [&](auto w) {
+        return op_by_access(op_access(wide, spans, 2), [&](auto w) {
             return launch_pdl(combine_backward_kernel<decltype(t), decltype(w)::value>, grid_for(tokens, threads, sms),
                               dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream_), p);
         });

@@ -39,7 +39,7 @@ cudaError_t op_malloc(void **p, size_t bytes, int dev, cudaStream_t stream) {
     return cudaMallocFromPoolAsync(p, bytes, pool, stream);
 }
 
-int op_check(const OpSpan *spans, int count, int *sms) {
+int op_check(OpSpan *spans, int count, int *sms) {
     char msg[256];
     for (int i = 0; i < count; ++i) {
         const OpSpan &s = spans[i];
@@ -76,8 +76,11 @@ int op_check(const OpSpan *spans, int count, int *sms) {
         std::snprintf(msg, sizeof msg, "this library is built for sm_103a only (device is sm_%d%d)", major, minor);
         return api_error(GEMM_ERR_UNSUPPORTED, msg);
     }
+    uint64_t begin;
     for (int i = 0; i < count; ++i)
-        if (spans[i].bytes && (rc = api_check_device_span(spans[i].name, spans[i].p, spans[i].bytes, dev))) return rc;
+        if (spans[i].bytes && (rc = api_check_device_span_range(spans[i].name, spans[i].p, spans[i].bytes, dev, &begin,
+                                                                &spans[i].memory_end)))
+            return rc;
     if (sms) *sms = n;
     return GEMM_OK;
 }

@@ -78,7 +78,7 @@ __device__ __forceinline__ uint2 scaled8(const OpVec8<T> &x, float inv, int e5m2
     return to_fp8x8(f, e5m2);
 }
 
-template <typename T, int BLOCK, bool WIDE, bool SCATTER = false>
+template <typename T, int BLOCK, int ACCESS, bool SCATTER = false>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_kernel(const QuantParams p) {
     pdl_enter();
     __shared__ float s_max[16][kTile];   // [row group][column]; tiles use one value a warp
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_ke
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int64_t r = r0 + ty + 16 * i;
-        x[i] = op_load8<WIDE, T>(X + r * p.ldx + c, r < p.rows ? have : 0);
+        x[i] = op_load8<ACCESS, T>(X + r * p.ldx + c, r < p.rows ? have : 0);
     }
 
     float inv8[8];           // 1 / scale of its rows (row blocks) or columns (column blocks)
@@ -253,7 +253,7 @@ extern "C" int gemm_quantize_block(int64_t batch, int64_t rows, int64_t cols, in
         (s_rows > 1 && s_row == 0) || (nb > 1 && s_col == 0))
         return api_error(GEMM_ERR_INVALID_ARG, "scales overlap (s_row, s_col)");
     const int eb = op_type_bytes(type);
-    const OpSpan spans[] = {
+    OpSpan spans[] = {
         {"X", X, (uint64_t)(batch - 1) * x_stride * eb + op_extent(rows, cols, ldx, eb), eb, false},
         {"Q", Q, (uint64_t)(batch - 1) * q_stride + op_extent(q_rows, cols, ldq, 1), 1, true},
         {"S", S, ((uint64_t)(batch - 1) * s_batch + (uint64_t)(s_rows - 1) * s_row + (uint64_t)(nb - 1) * s_col + 1) * 4,
@@ -289,9 +289,9 @@ extern "C" int gemm_quantize_block(int64_t batch, int64_t rows, int64_t cols, in
     const dim3 grid((unsigned)tiles, (unsigned)batch, 1);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const cudaError_t e = op_by_type(type, [&](auto t) {
-        return op_by_flag(wide, [&](auto w) {
+        return op_by_access(op_access(wide, spans, 1), [&](auto w) {
             using T = decltype(t);
-            constexpr bool W = decltype(w)::value;
+            constexpr int W = decltype(w)::value;
             if (slots)
                 return launch_pdl(quantize_kernel<T, GEMM_BLOCK_ROW, W, true>, grid, dim3(kQThreads), 0, stream, p);
             if (block == GEMM_BLOCK_ROW)

@@ -618,7 +618,7 @@ int gemm_route(int64_t tokens, int64_t experts, int type, const void *logits, in
         return api_error(GEMM_ERR_INVALID_ARG, "offsets, order and slots are all given or all NULL");
     const int eb = op_type_bytes(type);
     const uint64_t pairs = (uint64_t)(tokens * how->top_k) * 4;
-    const OpSpan spans[] = {{"logits", logits, op_extent(tokens, experts, ldl, eb), eb, false},
+    OpSpan spans[] = {{"logits", logits, op_extent(tokens, experts, ldl, eb), eb, false},
                             {"bias", bias, bias && tokens > 0 ? (uint64_t)experts * 4 : 0, 4, false},
                             {"indices", indices, pairs, 4, true},
                             {"weights", weights, pairs, 4, true},
@@ -712,7 +712,7 @@ int gemm_route_backward(int64_t tokens, int64_t experts, int type, const void *l
     if (tokens == 0) return GEMM_OK;
     const int eb = op_type_bytes(type);
     const uint64_t pairs = (uint64_t)(tokens * how->top_k) * 4;
-    const OpSpan spans[] = {{"logits", logits, op_extent(tokens, experts, ldl, eb), eb, false},
+    OpSpan spans[] = {{"logits", logits, op_extent(tokens, experts, ldl, eb), eb, false},
                             {"indices", indices, pairs, 4, false},
                             {"grad", grad, pairs, 4, false},
                             {"dlogits", dlogits, op_extent(tokens, experts, ldd, eb), eb, true}};
