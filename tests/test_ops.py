@@ -343,3 +343,30 @@ def test_shifted_loads_are_not_taken_past_the_end_of_an_allocation(tmp_path):
                     "-I", os.path.join(cuda, "include"), str(src), "-o", str(tmp_path / "access")], check=True)
     run = subprocess.run([str(tmp_path / "access")], capture_output=True, text=True)
     assert run.returncode == 0, run.stdout
+
+
+# ------------------------------------------------ footprints past 64 bits ---
+FAR = (1 << 28) + 1        # rows that, 2^36 elements apart, come round to the first one in 64 bits
+LD = 1 << 36
+
+
+def test_footprints_that_do_not_fit_64_bits_are_refused(lib):
+    q = dict(rows=FAR, X=1 << 20, Q=1 << 50, S=1 << 54, s_col=1 << 29)
+    far = [
+        quant(lib, ldx=LD, **q), quant(lib, ldq=LD, **q), quant(lib, block=2, batch=2, qs=1 << 46, s_batch=1 << 46,
+                                                                 **dict(q, s_row=LD, s_col=1, ldq=1 << 10)),
+    ]
+    assert far == [BAD] * 3
+    for kw, frag in ((dict(ldx=LD), "X: extent"), (dict(ldq=LD), "Q: extent"), (dict(batch=1 << 15, xs=1 << 46, rows=256,
+                     qs=1 << 17, s_batch=1 << 31, type_=0), "X: extent"), (dict(s_row=LD), "S: extent")):
+        refused(quant(lib, **dict(q, **kw)), frag)
+    refused(combine(lib, T=1, R=FAR, ldy=LD), "Y: extent")
+    refused(combine(lib, T=FAR, ldo=LD), "out: extent")
+    refused(route(lib, T=FAR, ldl=LD), "logits: extent")
+    refused(scaled(lib, M=FAR, lda=LD), "A: extent")
+    refused(scaled(lib, N=FAR, ldc=1 << 29, ldb=LD), "B: extent")
+    refused(scaled(lib, M=FAR, ldc=LD), "C: extent")
+    refused(scaled(lib, M=FAR, sa=bs(si=LD)), "a_scale: extent")
+    refused(scaled(lib, N=FAR, ldc=1 << 29, sb=bs(P << 9, si=LD)), "b_scale: extent")
+    refused(experts(lib, N=FAR, ldb=LD, ldc=1 << 29, E=2), "B: extent")
+    refused(experts(lib, rows=FAR, sa=bs(si=LD)), "a_scale: extent")

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <cstdio>
+#include <initializer_list>
 #include <type_traits>
 
 #include "gemm_ops.h"
@@ -26,9 +27,32 @@ struct OpSpan {
     uint64_t memory_end = 0;   // op_check: where the allocation that holds it ends
 };
 
+// Steps along one dimension of a strided array.
+struct OpDim {
+    int64_t count, stride;
+};
+
+// Elements from the first of a strided array to behind its last (0: it has none).
+// What does not fit 64 bits (sizes and strides may be 2^31 and 2^46) is the largest
+// value: no extent wraps round to a small one.
+inline uint64_t op_reach(std::initializer_list<OpDim> dims) {
+    unsigned __int128 n = 1;
+    for (const OpDim &d : dims) {
+        if (d.count <= 0) return 0;
+        n += (unsigned __int128)(d.count - 1) * (unsigned __int128)d.stride;
+    }
+    return n > UINT64_MAX ? UINT64_MAX : (uint64_t)n;
+}
+
+// The same in bytes.
+inline uint64_t op_bytes(std::initializer_list<OpDim> dims, int elem) {
+    const uint64_t n = op_reach(dims);
+    return n > UINT64_MAX / (uint64_t)elem ? UINT64_MAX : n * (uint64_t)elem;
+}
+
 // The last byte touched + 1 of `rows` rows of `cols` elements, `ld` apart.
 inline uint64_t op_extent(int64_t rows, int64_t cols, int64_t ld, int elem) {
-    return rows > 0 && cols > 0 ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * (uint64_t)elem : 0;
+    return op_bytes({{rows, ld}, {cols, 1}}, elem);
 }
 
 // The pitch of a matrix that is only read, row by row: 0 (one row stands for

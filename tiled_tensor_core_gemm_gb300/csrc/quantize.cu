@@ -245,19 +245,19 @@ extern "C" int gemm_quantize_block(int64_t batch, int64_t rows, int64_t cols, in
     }
     if (batch == 0 || rows == 0 || cols == 0 || (slots && out_rows == 0)) return GEMM_OK;
     const int64_t q_rows = slots ? out_rows : rows, s_rows = slots ? out_rows : mb;
-    if (batch > 1 && (q_stride < (rows - 1) * ldq + cols ||
-                      s_batch < (s_rows - 1) * s_row + (nb - 1) * s_col + 1))
+    if (batch > 1 && ((uint64_t)q_stride < op_reach({{rows, ldq}, {cols, 1}}) ||
+                      (uint64_t)s_batch < op_reach({{s_rows, s_row}, {nb, s_col}})))
         return api_error(GEMM_ERR_INVALID_ARG, "matrices of Q or S overlap");
     // distinct scales: one stride must step over the whole of the other
-    if ((s_rows > 1 && nb > 1 && !(s_row > (nb - 1) * s_col || s_col > (s_rows - 1) * s_row)) ||
+    if ((s_rows > 1 && nb > 1 && (uint64_t)s_row < op_reach({{nb, s_col}}) &&
+         (uint64_t)s_col < op_reach({{s_rows, s_row}})) ||
         (s_rows > 1 && s_row == 0) || (nb > 1 && s_col == 0))
         return api_error(GEMM_ERR_INVALID_ARG, "scales overlap (s_row, s_col)");
     const int eb = op_type_bytes(type);
     OpSpan spans[] = {
-        {"X", X, (uint64_t)(batch - 1) * x_stride * eb + op_extent(rows, cols, ldx, eb), eb, false},
-        {"Q", Q, (uint64_t)(batch - 1) * q_stride + op_extent(q_rows, cols, ldq, 1), 1, true},
-        {"S", S, ((uint64_t)(batch - 1) * s_batch + (uint64_t)(s_rows - 1) * s_row + (uint64_t)(nb - 1) * s_col + 1) * 4,
-         4, true},
+        {"X", X, op_bytes({{batch, x_stride}, {rows, ldx}, {cols, 1}}, eb), eb, false},
+        {"Q", Q, op_bytes({{batch, q_stride}, {q_rows, ldq}, {cols, 1}}, 1), 1, true},
+        {"S", S, op_bytes({{batch, s_batch}, {s_rows, s_row}, {nb, s_col}}, 4), 4, true},
         {"slots", slots, slots ? (uint64_t)(rows * copies) * 4 : 0, 4, false}};
     const int rc = op_check(spans, 4, nullptr);
     if (rc) return rc;

@@ -1042,12 +1042,7 @@ int check_scale(const char *name, const gemm_block_scale_t *s, bool tile_ok, int
         return api_error(GEMM_ERR_INVALID_ARG, msg);
     }
     const int64_t n = s->block == 128 ? cdiv(extent, 128) : extent;
-    *span = OpSpan{name, s->scale,
-                   num_kb > 0 && n > 0 && experts > 0
-                       ? ((uint64_t)(num_kb - 1) * s->stride_k + (uint64_t)(n - 1) * s->stride_i +
-                          (uint64_t)(experts - 1) * stride_e + 1) * 4
-                       : 0,
-                   4, false};
+    *span = OpSpan{name, s->scale, op_bytes({{num_kb, s->stride_k}, {n, s->stride_i}, {experts, stride_e}}, 4), 4, false};
     return GEMM_OK;
 }
 
@@ -1306,9 +1301,8 @@ int gemm_run_experts(int64_t rows, int64_t N, int64_t K, int64_t experts, int dt
     if (b_expert < 0 || b_expert > (1LL << 39)) return api_error(GEMM_ERR_INVALID_ARG, "b_expert out of range");
     const int64_t num_kb = cdiv(K, kBlockK);
     const int ob = epi.active ? op_type_bytes(epi.out) : 4;
-    const uint64_t one = op_extent(b.rows, b.cols, ldb, 1);
     OpSpan spans[6] = {{"A", A, op_extent(rows, K, lda, 1), 1, false},
-                       {"B", B, one ? (uint64_t)(experts - 1) * b_expert + one : 0, 1, false},
+                       {"B", B, op_bytes({{experts, b_expert}, {b.rows, ldb}, {b.cols, 1}}, 1), 1, false},
                        {"C", C, op_extent(rows, N, ldc, ob), ob, true},
                        {"offsets", offsets, (uint64_t)(experts + 1) * 4, 4, false}};
     if ((rc = check_scale("a_scale", a_scale, false, rows, num_kb, 1, 0, &spans[4]))) return rc;
