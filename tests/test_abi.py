@@ -572,3 +572,20 @@ def test_torch_wrappers_check_their_tensors_before_the_library():
     with pytest.raises(ValueError, match="CUDA tensors"):
         tg.gemm_grouped([A], [B])
     assert tg.gemm_grouped([], []) == []
+
+
+def test_footprints_that_do_not_fit_64_bits_are_refused():
+    # 2^28 + 1 rows 2^36 elements apart come round to the first one in 64 bits
+    far, ld, P = (1 << 28) + 1, 1 << 36, 1 << 40
+    lib = tg.load_library()
+    for kw in (dict(M=far, lda=ld), dict(M=far, ldc=ld), dict(K=far, lda=1 << 29, ldb=ld)):
+        a = dict(M=64, N=64, K=64, lda=64, ldb=64, ldc=64)
+        a.update(kw)
+        for dt in (tg.GEMM_FP32, tg.GEMM_BF16, tg.GEMM_E4M3):
+            assert tg.gemm_run(a["M"], a["N"], a["K"], dt, P, a["lda"], P << 2, a["ldb"], P << 4, a["ldc"]) == tg.GEMM_ERR_INVALID_ARG
+            assert "2^59" in tg.gemm_last_error()
+        assert lib.gemm_run_tf32_static(a["M"], a["N"], a["K"], P, a["lda"], P << 2, a["ldb"], P << 4, a["ldc"], None) == tg.GEMM_ERR_INVALID_ARG
+        assert "2^59" in tg.gemm_last_error()
+        g = tg.GemmGroup(a["M"], a["N"], a["K"], P, a["lda"], P << 2, a["ldb"], P << 4, a["ldc"], None)
+        assert tg.gemm_run_grouped(tg.GEMM_BF16, [g]) == tg.GEMM_ERR_INVALID_ARG
+        assert "2^59" in tg.gemm_last_error()

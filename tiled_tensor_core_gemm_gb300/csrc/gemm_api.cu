@@ -488,6 +488,13 @@ static int validate(int64_t M, int64_t N, int64_t K, int dtype, const void *A, i
     const int64_t kLdMax = 1LL << 36;
     if (lda > kLdMax || ldb > kLdMax || ldc > kLdMax)
         return fail(GEMM_ERR_INVALID_ARG, "leading dimension above 2^36 elements");
+    // (rows x pitch may pass 64 bits; the checks against the allocations reckon in them)
+    auto too_far = [](int64_t rows, int64_t cols, int64_t ld) {
+        return (unsigned __int128)(rows > 0 ? rows - 1 : 0) * (unsigned __int128)ld + (unsigned __int128)cols > (1ull << 59);
+    };
+    if (too_far(M, K, lda) || too_far(K, N, ldb) || too_far(M, N, ldc))
+        return fail(GEMM_ERR_INVALID_ARG, "a matrix spans more than 2^59 elements (lda=%lld ldb=%lld ldc=%lld)", (long long)lda,
+                    (long long)ldb, (long long)ldc);
     if (M > 0 && N > 0) {
         if (!C) return fail(GEMM_ERR_INVALID_ARG, "C is NULL");
         if (K > 0 && (!A || !B)) return fail(GEMM_ERR_INVALID_ARG, "A or B is NULL");
