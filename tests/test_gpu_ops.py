@@ -990,3 +990,69 @@ def test_rows_that_end_their_allocation():
     run = subprocess.run([sys.executable, "-c", ROWS_THAT_END_THEIR_ALLOCATION], cwd=root, capture_output=True, text=True,
                          timeout=300, env=dict(os.environ, PYTORCH_NO_CUDA_MEMORY_CACHING="1"))
     assert run.returncode == 0 and "equal" in run.stdout, run.stderr[-2000:]
+
+
+# ------------------------------------------------------------ forms and their corners ---
+# rows an expert on average: tiles of 16 and of 64 columns, 128 x 128, pairs of 256 x 192 (short K) and, with
+# one scale a column, of 256 x 256
+@pytest.mark.parametrize("counts,N,K,w_block", [
+    ([3, 0, 9, 1], 150, 260, "tile"), ([40, 33, 0, 61], 300, 390, "tile"), ([90, 128, 0, 100], 260, 520, "tile"),
+    ([300, 0, 257, 640], 520, 300, "tile"), ([300, 129, 0, 555], 520, 300, "row")])
+@pytest.mark.parametrize("to,out,act,alpha", [("e5m2", "f16", "none", 0.5), ("e5m2", "f32", "relu", -1.5),
+                                              ("e4m3", "bf16", "relu", 0.25), ("e4m3", "f16", "gelu", -0.5)])
+def test_experts_types_activations_and_guarded_c(counts, N, K, w_block, to, out, act, alpha):
+    E, R = len(counts), sum(counts)
+    off = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    A, sa = made(R, K, "row", to, 400)
+    W, sw = tg.quantize_block(randn(E, N, K, seed=410), w_block, to)
+    W, sw = W.transpose(1, 2), sw.transpose(1, 2)
+    for pad, offset in ((0, 0), (1, 0), (8, 3)):
+        flat = torch.full((2 * GUARD + offset + R * (N + pad),), math.nan, dtype=OUT[out], device="cuda")
+        inside = slice(GUARD + offset, GUARD + offset + R * (N + pad))
+        C = flat[inside].view(R, N + pad)[:, :N]
+        assert tg.gemm_experts(A, sa, W, sw, off, C=C, alpha=alpha, act=act, out=out) is C
+        lo = 0
+        for e, n in enumerate(counts):
+            if n:
+                check_product(C[lo:lo + n], A[lo:lo + n], W[e], sa[lo:lo + n], sw[e], out, alpha, act=act)
+            lo += n
+        rest = flat.clone()
+        rest[inside].view(R, N + pad)[:, :N] = math.nan
+        assert bool(rest.isnan().all())
+
+
+@pytest.mark.parametrize("T", (0, 1, 100, 200))
+def test_route_without_the_order(T):
+    import ctypes
+    from tiled_tensor_core_gemm_gb300 import ops
+    x = spread_logits(max(T, 1), 48, torch.float32, 430)[:T]
+    want = tg.route(x, 5, score="sigmoid", scale=2.5)
+    idx, w = torch.full((T + 1, 5), 77, dtype=torch.int32, device="cuda"), torch.full((T + 1, 5), 7.0, device="cuda")
+    how = ops.RouteHow(5, 1, 1, 1, 0, 1, 2.5)
+    s = torch.cuda.current_stream().cuda_stream
+    rc = tg.load_library().gemm_route(T, 48, 0, x.data_ptr(), 48, None, ctypes.byref(how), idx.data_ptr(), w.data_ptr(),
+                                      None, None, None, s)
+    assert rc == tg.GEMM_OK, tg.gemm_last_error()
+    assert torch.equal(idx[:T], want.indices) and torch.equal(w[:T], want.weights)
+    assert bool((idx[T:] == 77).all()) and bool((w[T:] == 7.0).all())
+
+
+@pytest.mark.parametrize("act", ("none", "relu", "gelu"))
+def test_scaled_epilogue_of_extreme_sums(act):
+    # sums far past the activation's flat ends, and a whole row of zeros
+    for M in (4, 150):
+        A, sa = made(M, 256, "row", "e4m3", 440)
+        B, sb = made(130, 256, "tile", "e4m3", 450)
+        sa = sa.clone()
+        sa[1], sa[2], sa[3] = 1e6, 0.0, 1e-12
+        check_product(tg.gemm_scaled(A, sa, B.t(), sb.t(), act=act), A, B.t(), sa, sb.t(), "f32", act=act)
+
+
+@pytest.mark.parametrize("rows", (20, 500))
+def test_experts_that_share_their_weights(rows):
+    E, N, K = 4, 260, 300
+    A, sa = made(rows, K, "row", "e4m3", 460)
+    W, sw = tg.quantize_block(randn(N, K, seed=461), "tile")
+    W, sw = W.t()[None].expand(E, K, N), sw.t()[None].expand(E, 3, 3)
+    off = torch.tensor([0, rows // 4, rows // 4 + 3, rows - 7, rows], dtype=torch.int32, device="cuda")
+    check_experts(tg.gemm_experts(A, sa, W, sw, off), A, sa, W, sw, off, "f32")
