@@ -2,10 +2,10 @@
 // cores" section 13.10: bias, activation, residual add or a type cast applied
 // to the accumulator before the store):
 //   y = act(alpha * acc + beta * C_old + bias[col]),  stored as the output type.
-// Every kernel that writes C (the tensor-core epilogue warps, the split-K
-// reduction, the SIMT kernel, the K = 0 fill) goes through epi_write, so the
-// arithmetic is the same on every path: FP32 throughout, one
-// round-to-nearest-even conversion at the store.
+// Every kernel of gemm.h's entries that writes C uses epi_value and the stores
+// below: the same arithmetic on each path, FP32 throughout, one conversion (to
+// nearest even) at the store.  The block-scaled product (scaled.cu) has a GELU
+// of its own, and a ReLU that keeps a NaN, for which fmaxf here gives 0.
 #pragma once
 
 #include <cuda_bf16.h>
