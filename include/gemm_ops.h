@@ -78,7 +78,9 @@ typedef struct {
  *                         sum_{k in kb} A[m][k] * B[k][n] + beta * C + bias[n]).
  *
  * Products within a K-block are exact and summed in FP32 in Tensor Memory; the
- * scaled blocks are summed in FP32 registers.
+ * scaled blocks are summed in FP32 registers, the two scales' product formed
+ * first (it must be finite).  The activations keep a NaN (gemm_run_ex's ReLU
+ * gives 0 for one).
  *
  *   dtype        GEMM_E4M3 or GEMM_E5M2, both operands
  *   A, lda       a_major 0: row-major, element (m, k) at A[m * lda + k],

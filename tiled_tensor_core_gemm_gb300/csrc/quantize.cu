@@ -13,8 +13,11 @@
 // rounded from the registers.  It is bound by HBM: one read of X, one write of
 // q (one per copy when a row goes to its experts' rows) and of the scales.
 //
-// Measured on GB300, BF16 to E4M3: 8191 x 5120 by columns 23.5 us (127 MB, 5.4
-// TB/s, 80% of a plain copy); 8192 x 4096 by rows to eight rows each 67 us (344 MB,
+// Measured on GB300, BF16 to E4M3: 8192 x 4096 by rows 19 to 20 us and by tiles
+// 21 (101 MB, 5.3 and 4.8 TB/s; 15 us at a plain copy's rate: about five go to
+// filling and draining the launch's 4.5 rounds of blocks, for eight FP32 matrices
+// of 4096 x 2048 by tiles take 51 us, 336 MB at 6.5 TB/s); 8191 x 5120 by columns
+// 23.5 us (127 MB, 5.4 TB/s); 8192 x 4096 by rows to eight rows each 67 us (344 MB,
 // 5.1 TB/s: four fifths of it writes, in 128-byte pieces).
 #include <cuda_fp8.h>
 

@@ -15,8 +15,8 @@
 // it, scaled, to sums kept in registers.  NBUF accumulators rotate, so the MMAs
 // of the next blocks run meanwhile.
 //
-// What bounds it (GB300, 8192^3 in 256 x 256 tiles on CTA pairs, 452 us = 2.4
-// PFLOP/s, 64% of the FP8 rate): the epilogue warps.  Per K-block of 128 x 256
+// What bounds it (GB300, 8192^3 in 256 x 256 tiles on CTA pairs, 452 to 475 us
+// over runs and boxes = 2.3 to 2.4 PFLOP/s, 60 to 63% of the FP8 rate): the epilogue warps.  Per K-block of 128 x 256
 // the MMAs take 520 cycles of an SM back to back and the kernel 850 to 900: of an
 // epilogue warp's own 850, about 100 to find the MMAs complete, 270 to read the
 // accumulator (two loads of 32 columns in flight), 260 for the multiply-adds (two
@@ -730,7 +730,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
         // One scale for 128 columns: each thread reads its row's and the columns'
         // straight from memory, two K-blocks ahead.  In 192 columns a tile's first are
         // asked for before the epilogue of the one before (in 256 the registers they
-        // hold there would be spilled: 463 -> 572 us at 8192^3).
+        // hold there would be spilled: 463 -> 572 us at 8192^3, one run).
         constexpr bool kEarly = BN == 192;
         const float *row_at = nullptr, *col_at = nullptr;              // of the K-block two further
         float row_even = 0.f, col_even = 0.f, row_odd = 0.f, col_odd = 0.f;
@@ -1064,7 +1064,7 @@ uint32_t idesc_of(int dtype, int bn, int cg, int p_mn, int q_mn) {
 //   128 x 128                             1.25 a K-block, 5 a tile
 //   256 x 256, 256 x 192 on a CTA pair    1.5, 1.3 a K-block, 13.5, 7.7 a tile
 // and 8 or 9 more for K cut in 2 or 4 ranges (the cluster's exchange: measured
-// 2.4 us; 8 ranges cost 9 us and are never taken).  Both sides measured, in us:
+// 2.4 us; 8 ranges cost 9 us and are never taken).  Both sides measured in one run, in us:
 // 256 columns 463 at 8192^3, 107 at 8192 x 8192 x 1024, 28 at 2048^3; 192 columns
 // (three warpgroups' sums, half the epilogue) 517, 103 and 31.
 ScaledPlan plan_product(int64_t M, int64_t N, int64_t num_kb, bool a_col, bool b_col, bool b_tile, int sms) {

@@ -278,6 +278,7 @@ def gemm_scaled(A, a_scale, B, b_scale, C=None, alpha=1.0, beta=0.0, bias=None, 
     or (ceil(M/128), ceil(K/128)); b_scale: (ceil(K/128), N) or (ceil(K/128),
     ceil(N/128)); any strides.  out: C's type, "f32", "bf16" or "f16"
     (allocated if None; beta must then be 0).  bias: N float32 values or None.
+    The activations keep a NaN.
     """
     torch, tg, lib, _, fp8, outs, raw = _tables()
     if A.dim() != 2 or B.dim() != 2 or a_scale.dim() != 2 or b_scale.dim() != 2:
