@@ -15,9 +15,9 @@
 // it, scaled, to sums kept in registers.  NBUF accumulators rotate, so the MMAs
 // of the next blocks run meanwhile.
 //
-// What bounds it (GB300, 8192^3 in 256 x 256 tiles on CTA pairs, 452 to 475 us
-// over runs and boxes = 2.3 to 2.4 PFLOP/s, 60 to 63% of the FP8 rate): the epilogue warps.  Per K-block of 128 x 256
-// the MMAs take 520 cycles of an SM back to back and the kernel 850 to 900: of an
+// What bounds it (GB300, 8192^3 in 256 x 256 tiles on CTA pairs, 450 to 482 us
+// over runs = 2.3 to 2.4 PFLOP/s, 59 to 64% of the FP8 rate): the epilogue
+// warps.  Per K-block of 128 x 256 the MMAs take 520 cycles of an SM back to back and the kernel 850 to 900: of an
 // epilogue warp's own 850, about 100 to find the MMAs complete, 270 to read the
 // accumulator (two loads of 32 columns in flight), 260 for the multiply-adds (two
 // warps a scheduler, 128 cycles each), the rest hand-over and lookups, each of
