@@ -295,11 +295,18 @@ GEMM_API int gemm_get_status(struct CUstream_st *stream);
  *   "trace_addr"     device address of a trace buffer, 0 = off (see
  *                    gemm_trace_record_t below); "trace_records" its
  *                    capacity in records
+ *   "product_bn"     columns of a tile of the row-wise 16-bit products
+ *                    (gemm_project.h): 128 (one CTA) or 256 (a CTA pair)
+ *   "product_splits" K ranges (1, 2, 4) of their tiles of few tokens, where
+ *                    that many fit one round of clusters
+ *   "loss_columns"   vocabulary entries a piece of the projection's loss
+ *                    takes, a multiple of 64
  *   "wait_timeout_ms" bound on every in-kernel wait (default 2000)
  *   "debug_stall_mma" test hook: 1 makes the tensor-core kernel's MMA thread
  *                    first wait on a barrier nothing arrives at, so the wait
  *                    expires and gemm_get_status() reports GEMM_ERR_TIMEOUT
- *                    (so does the block-scaled product's, gemm_ops.h)
+ *                    (so do the block-scaled product's, gemm_ops.h, and
+ *                    the 16-bit products', gemm_project.h)
  * Returns GEMM_ERR_INVALID_ARG for an unknown key or an out-of-range value.
  */
 GEMM_API int gemm_set_option(const char *key, int64_t value);

@@ -32,7 +32,7 @@ import ctypes
 import os
 import threading
 
-from . import ops
+from . import ops, projection
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libtcgemm.so")
@@ -138,6 +138,7 @@ def load_library():
         lib.gemm_run_grouped.argtypes = [ctypes.c_int, i64, ctypes.POINTER(GemmGroup), ctypes.POINTER(GemmEpilogue), p]
         lib.gemm_run_grouped.restype = ctypes.c_int
         ops.declare(lib)
+        projection.declare(lib)
         _lib = lib
         return lib
 
@@ -342,3 +343,5 @@ def gemm_grouped(As, Bs, Cs=None, biases=None, alpha=1.0, beta=0.0, act="none", 
 
 from .ops import (Routing, combine, combine_backward, gemm_experts, gemm_scaled, quantize_block, route,  # noqa: E402
                   route_backward)
+from .projection import (AdapterPlan, adapter_plan, gemm_adapters, gemm_adapters_backward, project_loss,  # noqa: E402
+                         project_loss_backward)

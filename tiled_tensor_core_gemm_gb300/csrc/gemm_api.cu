@@ -430,6 +430,15 @@ int gemm_set_option(const char *key, int64_t v) {
     } else if (!std::strcmp(key, "tc_b_major")) {
         if (v < 0 || v > 2) return fail(GEMM_ERR_INVALID_ARG, "tc_b_major must be 0, 1 or 2");
         g_opt.tc_b_major = (int)v;
+    } else if (!std::strcmp(key, "product_bn")) {
+        if (v != 0 && v != 128 && v != 256) return fail(GEMM_ERR_INVALID_ARG, "product_bn must be 0, 128 or 256");
+        g_opt.product_bn = (int)v;
+    } else if (!std::strcmp(key, "product_splits")) {
+        if (v != 0 && v != 1 && v != 2 && v != 4) return fail(GEMM_ERR_INVALID_ARG, "product_splits must be 0, 1, 2 or 4");
+        g_opt.product_splits = (int)v;
+    } else if (!std::strcmp(key, "loss_columns")) {
+        if (v < 0 || v > (1 << 24) || v % 64) return fail(GEMM_ERR_INVALID_ARG, "loss_columns must be a multiple of 64 in [0, 2^24]");
+        g_opt.loss_columns = (int)v;
     } else if (!std::strcmp(key, "debug_stall_mma")) {
         if (v < 0 || v > 1) return fail(GEMM_ERR_INVALID_ARG, "debug_stall_mma must be 0 or 1");
         g_opt.debug_stall_mma = (int)v;
@@ -469,6 +478,9 @@ int64_t gemm_get_option(const char *key) {
     if (!std::strcmp(key, "wait_timeout_ms")) return o.wait_timeout_ms;
     if (!std::strcmp(key, "trace_addr")) return o.trace_addr;
     if (!std::strcmp(key, "trace_records")) return o.trace_records;
+    if (!std::strcmp(key, "product_bn")) return o.product_bn;
+    if (!std::strcmp(key, "product_splits")) return o.product_splits;
+    if (!std::strcmp(key, "loss_columns")) return o.loss_columns;
     if (!std::strcmp(key, "debug_stall_mma")) return o.debug_stall_mma;
     return -1;
 }
@@ -701,6 +713,7 @@ int gemm_get_status(struct CUstream_st *stream_) {
     uint32_t w[4] = {0, 0, 0, 0};
     e = tc_read_and_clear_status(w);
     if (e == cudaSuccess && w[0] == 0) e = scaled_read_and_clear_status(w);
+    if (e == cudaSuccess && w[0] == 0) e = project_read_and_clear_status(w);
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
     if (w[0] != 0) {
         static const char *roles[] = {"?", "producer", "mma", "epilogue", "drain", "scales"};

@@ -1,0 +1,445 @@
+// The output projection's loss and its gradients: the C entries, and the kernels
+// around the products of project.cu.
+//
+// Forward: one product H . W^T whose epilogue keeps, for each token and part of 128
+// (64 in single-CTA tiles) columns, the maximum and the sum of the exponentials;
+// loss_finish joins the parts.  What bounds it is the product: 2 T V D flops, or W
+// once from memory where the tokens are few.  The parts are 8 bytes for each 128
+// logits, 1/32 of what keeping them in 16 bits would write.
+//
+// Backward, the vocabulary in pieces: the piece's logits again with the gradient of
+// the softmax as epilogue (16 bits, to a workspace), then dH += d W and dW = d^T H,
+// the latter reading d and H as they lie (both MN-major).  6 T V D flops; dH's sums
+// are read and written once a piece in FP32.
+#include <algorithm>
+
+#include "gemm_project.h"
+#include "project.h"
+
+namespace tcgemm {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kFinishWarps = 16;
+
+__device__ __forceinline__ bool counted(const void *labels, int label_bytes, int64_t t, int64_t V) {
+    const int64_t y = label_bytes == 8 ? __ldg(static_cast<const long long *>(labels) + t)
+                                       : (int64_t)__ldg(static_cast<const int32_t *>(labels) + t);
+    return y >= 0 && y < V;
+}
+
+// Joins a row's (maximum, sum) with another's.
+__device__ __forceinline__ void join(float2 &a, float2 b) {
+    const float top = fmaxf(a.x, b.x), base = top == -INFINITY ? 0.f : top;
+    a.y = a.y * exp2f(a.x - base) + b.y * exp2f(b.x - base);
+    a.x = top;
+}
+
+// 32 tokens a block, one a lane; the warps share the parts, and join theirs in the
+// order of the warps.
+__global__ void __launch_bounds__(32 * kFinishWarps)
+loss_finish(int64_t T, int64_t V, int parts, const float2 *__restrict__ part, const float *__restrict__ sums,
+            const float *__restrict__ hits, const void *labels, int label_bytes, gemm_loss_t how, float *loss, float *lse) {
+    pdl_enter();
+    __shared__ float2 soft[kFinishWarps][32];
+    __shared__ float plain[kFinishWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+    float2 m = make_float2(-INFINITY, 0.f);
+    float s = 0.f;
+    if (t < T) {
+#pragma unroll 4
+        for (int i = warp; i < parts; i += kFinishWarps) {
+            join(m, __ldg(part + (int64_t)i * T + t));
+            if (sums) s += __ldg(sums + (int64_t)i * T + t);
+        }
+    }
+    soft[warp][lane] = m;
+    plain[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || t >= T) return;
+    for (int w = 1; w < kFinishWarps; ++w) {
+        join(m, soft[w][lane]);
+        s += plain[w][lane];
+    }
+    const float total = kLn2 * (m.x + log2f(m.y));
+    lse[t] = total;
+    if (!loss) return;
+    float l = 0.f;
+    if (counted(labels, label_bytes, t, V)) {
+        l = total - (1.f - how.smoothing) * __ldg(hits + t) + how.z_loss * total * total;
+        if (how.smoothing != 0.f) l -= how.smoothing / (float)V * s;
+    }
+    loss[t] = l;
+}
+
+// FP16: the power of two that brings the largest |d| just below 2^15, and its
+// inverse.  |d| is at most |grad| (1 + 2 a |lse|) (p and the target are in [0, 1],
+// the cap's slope too).
+__global__ void __launch_bounds__(1024)
+loss_scale(int64_t T, int64_t V, const float *__restrict__ grad, int64_t grad_stride, const float *__restrict__ lse,
+           const void *labels, int label_bytes, float z_loss, float *scale) {
+    pdl_enter();
+    __shared__ float most[32];
+    float m = 0.f;
+    for (int64_t t = threadIdx.x; t < T; t += 1024)
+        if (counted(labels, label_bytes, t, V))
+            m = fmaxf(m, fabsf(__ldg(grad + t * grad_stride)) * (1.f + 2.f * z_loss * fabsf(__ldg(lse + t))));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    m = most[threadIdx.x];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (threadIdx.x == 0) {
+        int e = 0;
+        if (m > 0.f && m < INFINITY) e = 14 - ilogbf(m);
+        e = max(-100, min(100, e));
+        scale[0] = ldexpf(1.f, e);
+        scale[1] = ldexpf(1.f, -e);
+    }
+}
+
+// Per token what the logits' gradient takes (project.cu: take_gradient): lse in base
+// 2, grad (1 + 2 a lse), grad, and whether the token counts; and H's row, at a pitch
+// TMA can address, zero for a token that does not count, so that nothing it holds
+// (padding may be anything) reaches dW as 0 x NaN.
+template <int ACCESS, typename E>
+__global__ void __launch_bounds__(256)
+loss_rows(int64_t T, int64_t V, int D, const E *__restrict__ H, int64_t ldh, E *__restrict__ out, int64_t ldo,
+          const float *__restrict__ grad, int64_t grad_stride, const float *__restrict__ lse, const void *labels,
+          int label_bytes, float z_loss, const float *scale, float4 *rows) {
+    pdl_enter();
+    const int per = (D + 7) / 8;
+    const float f = scale ? __ldg(scale) : 1.f;
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        const bool has = counted(labels, label_bytes, t, V);
+        if (threadIdx.x == 0) {
+            const float l = __ldg(lse + t), g = f * __ldg(grad + t * grad_stride);
+            rows[t] = has ? make_float4(l * kLog2e, g * fmaf(2.f * z_loss, l, 1.f), g, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int c = threadIdx.x; c < per; c += 256)
+            op_store8<true>(out + t * ldo + 8 * c, op_load8<ACCESS>(H + t * ldh + 8 * c, has ? min(8, D - 8 * c) : 0), 8);
+    }
+}
+
+int no_memory(uint64_t bytes, cudaError_t e) {
+    cudaGetLastError();
+    char msg[128];
+    std::snprintf(msg, sizeof msg, "workspace of %llu bytes: %s", (unsigned long long)bytes, cudaGetErrorString(e));
+    return api_error(GEMM_ERR_NO_MEMORY, msg);
+}
+
+// Parts of one stream-ordered allocation, each on 256 bytes.
+struct Workspace {
+    uint64_t bytes = 0;
+    uint8_t *base = nullptr;
+    uint64_t add(uint64_t n) {
+        const uint64_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
+    }
+    int make(cudaStream_t stream) {
+        int dev = 0;
+        cudaGetDevice(&dev);
+        void *p = nullptr;
+        const cudaError_t e = op_malloc(&p, bytes ? bytes : 256, dev, stream);
+        if (e != cudaSuccess) return no_memory(bytes, e);
+        base = static_cast<uint8_t *>(p);
+        return GEMM_OK;
+    }
+    int done(int rc, cudaStream_t stream) {
+        const cudaError_t e = cudaFreeAsync(base, stream);
+        return rc ? rc : op_launched("cudaFreeAsync", e);
+    }
+};
+
+struct LossArgs {
+    int64_t T, V, D;
+    int type;
+    const void *H;
+    int64_t ldh;
+    const void *W;
+    int64_t ldw;
+    int w_major;
+    const void *labels;
+    int label_bytes;
+    gemm_loss_t how;
+    bool pack_h, pack_w;       // TMA cannot address them
+    uint64_t h_lo, h_hi, w_lo, w_hi;
+};
+
+int check_args(LossArgs *a, int dtype, const gemm_loss_t *how) {
+    const int64_t kMax = 0x7fffffffLL - 512, kLdMax = 1LL << 36;
+    if (dtype != GEMM_BF16 && dtype != GEMM_FP16) return api_error(GEMM_ERR_INVALID_ARG, "dtype must be BF16 or FP16");
+    a->type = dtype == GEMM_BF16 ? GEMM_OUT_BF16 : GEMM_OUT_F16;
+    if (a->T < 0 || a->V < 1 || a->D < 0 || a->T > kMax || a->V > kMax || a->D > kMax)
+        return api_error(GEMM_ERR_INVALID_ARG, "size negative or out of range (V must be at least 1)");
+    if (a->w_major != 0 && a->w_major != 1) return api_error(GEMM_ERR_INVALID_ARG, "w_major is 0 or 1");
+    if (a->label_bytes != 4 && a->label_bytes != 8) return api_error(GEMM_ERR_INVALID_ARG, "label_bytes is 4 or 8");
+    const int64_t w_cols = a->w_major ? a->V : a->D;
+    if (a->ldh < std::max<int64_t>(a->D, 1) || a->ldw < std::max<int64_t>(w_cols, 1) || a->ldh > kLdMax || a->ldw > kLdMax)
+        return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
+    a->how = how ? *how : gemm_loss_t{0.f, 0.f, 0.f};
+    if (!(a->how.softcap >= 0.f) || a->how.softcap > 1e30f || (a->how.softcap > 0.f && a->how.softcap < 1e-30f) ||
+        !(a->how.smoothing >= 0.f && a->how.smoothing < 1.f) || !(a->how.z_loss >= 0.f) || a->how.z_loss > 1e30f)
+        return api_error(GEMM_ERR_INVALID_ARG, "softcap, smoothing or z_loss out of range");
+    return GEMM_OK;
+}
+
+OpSpan h_span(const LossArgs &a) { return OpSpan{"H", a.H, op_extent(a.T, a.D, a.ldh, 2), 2, false}; }
+OpSpan w_span(const LossArgs &a) {
+    return OpSpan{"W", a.W, a.w_major ? op_extent(a.D, a.V, a.ldw, 2) : op_extent(a.V, a.D, a.ldw, 2), 2, false};
+}
+OpSpan label_span(const LossArgs &a) {
+    return OpSpan{"labels", a.labels, (uint64_t)a.T * (uint64_t)a.label_bytes, a.label_bytes, false};
+}
+
+// Which operands have to be copied, and the allocations they lie in.
+int plan_packs(LossArgs *a) {
+    if (a->T <= 1) a->ldh = op_round_up(std::max<int64_t>(a->D, 1), 8);
+    const int64_t w_rows = a->w_major ? a->D : a->V, w_cols = a->w_major ? a->V : a->D;
+    if (w_rows <= 1) a->ldw = op_round_up(std::max<int64_t>(w_cols, 1), 8);
+    a->pack_h = !op_wide(a->H, a->ldh, 2) && a->D > 0;
+    a->pack_w = !op_wide(a->W, a->ldw, 2) && a->D > 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int rc = GEMM_OK;
+    const OpSpan h = h_span(*a), w = w_span(*a);
+    if (a->pack_h) rc = api_check_device_span_range("H", a->H, h.bytes, dev, &a->h_lo, &a->h_hi);
+    if (rc == GEMM_OK && a->pack_w) rc = api_check_device_span_range("W", a->W, w.bytes, dev, &a->w_lo, &a->w_hi);
+    return rc;
+}
+
+// Vocabulary entries a piece takes, a multiple of 256 below V; V rounded up
+// otherwise.
+int64_t piece_columns(int64_t V, int64_t want) {
+    const int64_t forced = options_snapshot().loss_columns;
+    if (forced) want = forced;
+    return std::min(std::max<int64_t>(want, 64), op_round_up(V, 64));
+}
+
+int64_t packed_w_bytes(const LossArgs &a, int64_t piece) {
+    if (!a.pack_w) return 0;
+    return 2 * (a.w_major ? a.D * op_round_up(piece, 8) : piece * op_round_up(a.D, 8));
+}
+
+// Entries [v0, v0 + n) of W as TMA can read them (copied to `to` where it cannot).
+int piece_of_w(const LossArgs &a, int64_t v0, int64_t n, void *to, ProductOperand *out, cudaStream_t stream) {
+    const uint16_t *src = static_cast<const uint16_t *>(a.W) + (a.w_major ? v0 : v0 * a.ldw);
+    out->p = src;
+    out->rows = n;
+    out->ld = a.ldw;
+    out->mn = a.w_major;
+    if (!a.pack_w) return GEMM_OK;
+    out->p = to;
+    out->ld = op_round_up(a.w_major ? n : a.D, 8);
+    return op_launched("operand pack", pack_rows_launch(src, a.ldw, to, out->ld, a.w_major ? a.D : n, a.w_major ? n : a.D, 2,
+                                                        a.w_lo, a.w_hi, stream));
+}
+
+ProductLoss loss_of(const LossArgs &a) {
+    ProductLoss l;
+    l.labels = a.labels;
+    l.label_bytes = a.label_bytes;
+    l.vocab = a.V;
+    l.softcap = a.how.softcap;
+    l.eps_v = a.how.smoothing / (float)a.V;
+    l.one_eps = 1.f - a.how.smoothing;
+    l.want_sum = a.how.smoothing != 0.f;
+    return l;
+}
+
+}  // namespace
+}  // namespace tcgemm
+
+using namespace tcgemm;
+
+extern "C" {
+
+int gemm_project_loss(int64_t T, int64_t V, int64_t D, int dtype, const void *H, int64_t ldh, const void *W, int64_t ldw,
+                      int w_major, const void *labels, int label_bytes, const gemm_loss_t *how, float *loss, float *lse,
+                      struct CUstream_st *stream_) {
+    api_clear_error();
+    LossArgs a = {T, V, D, 0, H, ldh, W, ldw, w_major, labels, label_bytes, {}, false, false, 0, 0, 0, 0};
+    int rc = check_args(&a, dtype, how);
+    if (rc) return rc;
+    OpSpan spans[5] = {h_span(a), w_span(a), label_span(a), {"loss", loss, loss ? (uint64_t)T * 4 : 0, 4, true},
+                       {"lse", lse, (uint64_t)T * 4, 4, true}};
+    if (T == 0) return GEMM_OK;
+    int sms = 0;
+    if ((rc = op_check(spans, 5, &sms))) return rc;
+    if ((rc = plan_packs(&a))) return rc;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    // in one piece, unless W has to be copied (256 MB at a time)
+    const int64_t piece = piece_columns(V, a.pack_w ? std::max<int64_t>(256, (1LL << 27) / std::max<int64_t>(D, 1) / 256 * 256) : V);
+    const ProductPlan plan = product_plan_rows(T, std::min(piece, V), D, sms);
+    const int part_cols = product_part_columns(plan);
+    int64_t parts = 0;
+    for (int64_t v = 0; v < V; v += piece) parts += op_cdiv(std::min(piece, V - v), part_cols);
+    if (parts > 0x7fffffffLL) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
+    const int64_t h_pitch = a.pack_h ? op_round_up(D, 8) : a.ldh;
+    Workspace ws;
+    const uint64_t at_parts = ws.add((uint64_t)parts * T * 8), at_sums = ws.add(a.how.smoothing != 0.f ? (uint64_t)parts * T * 4 : 0),
+                   at_hits = ws.add((uint64_t)T * 4), at_h = ws.add(a.pack_h ? (uint64_t)T * h_pitch * 2 : 0),
+                   at_w = ws.add((uint64_t)packed_w_bytes(a, piece));
+    if ((rc = ws.make(stream))) return rc;
+    ProductCall c;
+    c.epilogue = kEpiStats;
+    c.type = a.type;
+    c.I = T;
+    c.K = D;
+    c.plan = plan;
+    c.p = {H, T, h_pitch, 0};
+    if (a.pack_h) {
+        c.p.p = ws.base + at_h;
+        rc = op_launched("operand pack", pack_rows_launch(H, a.ldh, ws.base + at_h, h_pitch, T, D, 2, a.h_lo, a.h_hi, stream));
+    }
+    c.loss = loss_of(a);
+    c.loss.hits = reinterpret_cast<float *>(ws.base + at_hits);
+    int64_t part = 0;
+    for (int64_t v = 0; rc == GEMM_OK && v < V; v += piece) {
+        c.J = std::min(piece, V - v);
+        rc = piece_of_w(a, v, c.J, ws.base + at_w, &c.q, stream);
+        if (rc) break;
+        c.loss.first = v;
+        c.loss.parts = reinterpret_cast<float2 *>(ws.base + at_parts) + part * T;
+        c.loss.sums = reinterpret_cast<float *>(ws.base + at_sums) + part * T;
+        part += op_cdiv(c.J, part_cols);
+        rc = product_launch(c, sms, stream);
+    }
+    if (rc == GEMM_OK)
+        rc = op_launched("loss", launch_pdl(loss_finish, dim3((unsigned)op_cdiv(T, 32)), dim3(32 * kFinishWarps), 0, stream, T, V,
+                                            (int)parts, reinterpret_cast<const float2 *>(ws.base + at_parts),
+                                            a.how.smoothing != 0.f ? reinterpret_cast<const float *>(ws.base + at_sums) : nullptr,
+                                            reinterpret_cast<const float *>(ws.base + at_hits), labels, label_bytes, a.how, loss,
+                                            lse));
+    return ws.done(rc, stream);
+}
+
+int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const float *grad, int64_t grad_stride,
+                               const void *H, int64_t ldh, const void *W, int64_t ldw, int w_major, const void *labels,
+                               int label_bytes, const gemm_loss_t *how, const float *lse, void *dH, int64_t lddh, void *dW,
+                               int64_t lddw, struct CUstream_st *stream_) {
+    api_clear_error();
+    LossArgs a = {T, V, D, 0, H, ldh, W, ldw, w_major, labels, label_bytes, {}, false, false, 0, 0, 0, 0};
+    int rc = check_args(&a, dtype, how);
+    if (rc) return rc;
+    const int64_t kLdMax = 1LL << 36, dw_rows = w_major ? D : V, dw_cols = w_major ? V : D;
+    if (grad_stride != 0 && grad_stride != 1) return api_error(GEMM_ERR_INVALID_ARG, "grad_stride is 0 or 1");
+    if ((dH && (lddh < std::max<int64_t>(D, 1) || lddh > kLdMax)) || (dW && (lddw < std::max<int64_t>(dw_cols, 1) || lddw > kLdMax)))
+        return api_error(GEMM_ERR_INVALID_ARG, "leading dimension out of range");
+    OpSpan spans[7] = {h_span(a),
+                       w_span(a),
+                       label_span(a),
+                       {"grad", grad, T ? (uint64_t)((T - 1) * grad_stride + 1) * 4 : 0, 4, false},
+                       {"lse", lse, (uint64_t)T * 4, 4, false},
+                       {"dH", dH, dH ? op_extent(T, D, lddh, 2) : 0, 2, true},
+                       {"dW", dW, dW ? op_extent(dw_rows, dw_cols, lddw, 2) : 0, 2, true}};
+    if (D == 0 || (!dH && !dW)) return GEMM_OK;
+    int sms = 0;
+    if ((rc = op_check(spans, 7, &sms))) return rc;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (T == 0) {
+        if (!dW) return GEMM_OK;
+        return op_launched("cudaMemset2DAsync",
+                           cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)dw_cols * 2, (size_t)dw_rows, stream));
+    }
+    if ((rc = plan_packs(&a))) return rc;
+    const int et = a.type;
+    const bool f16 = et == GEMM_OUT_F16;
+    // A piece's d is at most 160 MB (the workspaces stay within what the pool keeps),
+    // and a multiple of 256 columns.
+    const int64_t piece = piece_columns(V, std::max<int64_t>(256, (160LL << 20) / 2 / std::max<int64_t>(T, 1) / 256 * 256));
+    const int64_t pieces = op_cdiv(V, piece), d_pitch = op_round_up(piece, 64), h_pitch = op_round_up(D, 8),
+                  acc_pitch = op_round_up(D, 64);
+    Workspace ws;
+    const uint64_t at_rows = ws.add((uint64_t)T * 16), at_scale = ws.add(8), at_h = ws.add((uint64_t)T * h_pitch * 2),
+                   at_d = ws.add((uint64_t)T * d_pitch * 2), at_w = ws.add((uint64_t)packed_w_bytes(a, piece)),
+                   at_acc = ws.add(dH && pieces > 1 ? (uint64_t)T * acc_pitch * 4 : 0);
+    if ((rc = ws.make(stream))) return rc;
+    float4 *rows = reinterpret_cast<float4 *>(ws.base + at_rows);
+    float *scale = reinterpret_cast<float *>(ws.base + at_scale), *acc = reinterpret_cast<float *>(ws.base + at_acc);
+    if (f16)
+        rc = op_launched("loss scale", launch_pdl(loss_scale, dim3(1), dim3(1024), 0, stream, T, V, grad, grad_stride, lse, labels,
+                                                  label_bytes, a.how.z_loss, scale));
+    const bool wide = op_wide(H, a.ldh, 2) && D % 8 == 0;
+    const int access = op_access(wide, &spans[0], 1);
+    if (rc == GEMM_OK)
+        rc = op_by_access(access, [&](auto acc_kind) {
+            auto go = [&](auto e) {
+                using E = decltype(e);
+                return op_launched("loss rows",
+                                   launch_pdl(loss_rows<decltype(acc_kind)::value, E>, dim3((unsigned)std::min<int64_t>(T, sms * 8)),
+                                              dim3(256), 0, stream, T, V, (int)D, static_cast<const E *>(H), a.ldh,
+                                              reinterpret_cast<E *>(ws.base + at_h), h_pitch, grad, grad_stride, lse, labels,
+                                              label_bytes, a.how.z_loss, (const float *)(f16 ? scale : nullptr), rows));
+            };
+            return f16 ? go(__half()) : go(__nv_bfloat16());
+        });
+    const ProductOperand h_rows = {ws.base + at_h, T, h_pitch, 0}, h_cols = {ws.base + at_h, D, h_pitch, 1};
+    int64_t n = 0;
+    for (int64_t v = 0; rc == GEMM_OK && v < V; v += piece, ++n) {
+        const int64_t cols = std::min(piece, V - v);
+        ProductOperand w;
+        if ((rc = piece_of_w(a, v, cols, ws.base + at_w, &w, stream))) break;
+        ProductCall d;
+        d.epilogue = kEpiDlogits;
+        d.type = et;
+        d.I = T;
+        d.J = cols;
+        d.K = D;
+        d.plan = product_plan_rows(T, cols, D, sms);
+        d.p = h_rows;
+        d.q = w;
+        d.C = ws.base + at_d;
+        d.ldc = d_pitch;
+        d.epi.active = 1;
+        d.epi.out = et;
+        d.loss = loss_of(a);
+        d.loss.first = v;
+        d.loss.rows = rows;
+        if ((rc = product_launch(d, sms, stream))) break;
+        if (dH) {
+            ProductCall c;
+            c.type = et;
+            c.I = T;
+            c.J = D;
+            c.K = cols;
+            c.plan = product_plan_rows(T, D, cols, sms);
+            c.p = {ws.base + at_d, T, d_pitch, 0};
+            c.q = {w.p, D, w.ld, w.mn ^ 1};       // (W's entries are the sum now)
+            c.old = n > 0 ? acc : nullptr;
+            c.ld_old = acc_pitch;
+            const bool last = n + 1 == pieces;
+            c.C = last ? dH : acc;
+            c.ldc = last ? lddh : acc_pitch;
+            c.epi.active = 1;
+            c.epi.out = last ? et : GEMM_OUT_F32;
+            c.alpha = f16 ? scale + 1 : nullptr;
+            if ((rc = product_launch(c, sms, stream))) break;
+        }
+        if (dW) {
+            const ProductOperand d_cols = {ws.base + at_d, cols, d_pitch, 1};
+            ProductCall c;
+            c.type = et;
+            c.I = w_major ? D : cols;
+            c.J = w_major ? cols : D;
+            c.K = T;
+            c.plan = product_plan_rows(c.I, c.J, T, sms);
+            c.p = w_major ? h_cols : d_cols;
+            c.q = w_major ? d_cols : h_cols;
+            c.C = static_cast<uint16_t *>(dW) + (w_major ? v : v * lddw);
+            c.ldc = lddw;
+            c.epi.active = 1;
+            c.epi.out = et;
+            c.alpha = f16 ? scale + 1 : nullptr;
+            if ((rc = product_launch(c, sms, stream))) break;
+        }
+    }
+    return ws.done(rc, stream);
+}
+
+}  // extern "C"

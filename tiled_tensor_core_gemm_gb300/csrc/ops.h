@@ -101,6 +101,8 @@ inline int op_launched(const char *what, cudaError_t e) {
 
 // Reads and clears the status word of the block-scaled product's kernel.
 cudaError_t scaled_read_and_clear_status(uint32_t words[4]);
+// The same of the 16-bit product's (project.cu).
+cudaError_t project_read_and_clear_status(uint32_t words[4]);
 
 #ifdef __CUDACC__
 // ----------------------------------------------------------------- vectors ---

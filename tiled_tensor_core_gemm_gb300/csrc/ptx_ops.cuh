@@ -45,6 +45,31 @@ __device__ __forceinline__ void mma_f8_sw128(uint32_t d_tmem, uint32_t pd, uint3
             ::"r"(d_tmem), "r"(pd), "r"(qd), "r"(kHigh), "r"(idesc), "r"(acc) : "memory");
 }
 
+// The same with 16-bit operands (both BF16 or both FP16, as idesc says).
+template <int CG>
+__device__ __forceinline__ void mma_f16_sw128(uint32_t d_tmem, uint32_t pd, uint32_t qd, uint32_t idesc, uint32_t acc) {
+    constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | ((uint32_t)kLayoutSw128 << 29);
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+            ::"r"(d_tmem), "r"(pd), "r"(qd), "r"(kHigh), "r"(idesc), "r"(acc) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}"
+            ::"r"(d_tmem), "r"(pd), "r"(qd), "r"(kHigh), "r"(idesc), "r"(acc) : "memory");
+}
+
+// 2-D tile load, completion counted on `bar` (of a CTA pair: a shared::cluster address).
+template <int CG>
+__device__ __forceinline__ void tma_load_2d_cg(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y) {
+    if (CG == 1) tma_load_2d(dst, m, bar, x, y);
+    else tma_load_2d_pair(dst, m, bar, x, y);
+}
+
 // max(x, 0) that keeps a NaN (fmaxf gives 0 for it).
 __device__ __forceinline__ float relu_nan(float x) {
     float r;
