@@ -98,6 +98,13 @@ struct Cfg {
     static constexpr int ROWS = kLanes * CG;
     static constexpr int COLS = BN / (EW / 4);             // columns of a thread
     static constexpr int THREADS = 128 + EW * 32;
+    // K-blocks an accumulator sums (0: all).  The tensor cores' long FP32 sums lose a
+    // little at every step (a loss over 4096 values off by 1.9e-6, against 4e-7 of an
+    // FP32 product); the statistics add accumulators of 8 x 64 in registers.
+    static constexpr int SEG = EPI == kEpiStats ? 8 : 0;
+    // Registers a thread after the first warpgroup has given some up (0: as launched).
+    static constexpr int GIVE = EPI == kEpiStats && COLS > 64 ? 56 : 0, TAKE = GIVE ? 224 : 0;
+    static_assert(GIVE == 0 || 128 * GIVE + EW * 32 * TAKE <= THREADS * 168, "the shares exceed the launch's registers");
     static constexpr int P_BYTES = kLanes * 128;
     static constexpr int Q_ROWS = BN / CG;                 // each CTA of a pair loads half of Q's rows
     static constexpr int Q_BYTES = (Q_ROWS < 64 ? 64 : Q_ROWS) * 128;
@@ -321,6 +328,20 @@ __device__ __forceinline__ void load_64(uint32_t src, float (&v)[64]) {
     }
 }
 
+// v += COLS columns of a thread's row, 32 at a time (one load in flight: the MMAs of
+// the next K-blocks take ten times as long, and a second would cost registers).
+template <int COLS>
+__device__ __forceinline__ void add_columns(uint32_t src, float (&v)[COLS]) {
+#pragma unroll
+    for (int c0 = 0; c0 < COLS; c0 += 32) {
+        uint32_t a[32];
+        ptx::tmem_ld_32x32b_x32(src + (uint32_t)c0, a);
+        ptx::tmem_wait_ld(a);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c0 + c] += __uint_as_float(a[c]);
+    }
+}
+
 // Rows of a box of 32 rows x 128 bytes in shared memory to C with ordinary stores.
 __device__ __forceinline__ void store_box_plain(const ProductParams &p, const Tile &T, uint32_t buf, int64_t i0,
                                                 int64_t jb, bool half, int lane) {
@@ -422,18 +443,52 @@ __device__ __forceinline__ void finish_row(const ProductParams &p, const Tile &T
     }
 }
 
+// tanh of the first 64 of v.  Logits mostly lie well inside their cap: while all of a
+// warp's are at most 1/2 the Taylor series up to x^13 is exact to rounding (the next
+// term is below 4e-8) and takes 7 multiply-adds, where tanhf takes about 25
+// instructions with two special-function calls.
+template <int N>
+__device__ __forceinline__ void tanh_64(float (&v)[N]) {
+    float most = 0.f;
+#pragma unroll
+    for (int c = 0; c < 64; ++c) most = fmaxf(most, fabsf(v[c]));
+    if (__all_sync(0xffffffffu, most <= 0.5f)) {
+        auto both = [](float c) { return make_float2(c, c); };
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+            const float2 x = make_float2(v[c], v[c + 1]), q = __fmul2_rn(x, x);
+            float2 r = both(21844.f / 6081075.f);
+            r = __ffma2_rn(r, q, both(-1382.f / 155925.f));
+            r = __ffma2_rn(r, q, both(62.f / 2835.f));
+            r = __ffma2_rn(r, q, both(-17.f / 315.f));
+            r = __ffma2_rn(r, q, both(2.f / 15.f));
+            r = __ffma2_rn(r, q, both(-1.f / 3.f));
+            r = __ffma2_rn(__fmul2_rn(r, q), x, x);
+            v[c] = r.x;
+            v[c + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) v[c] = tanhf(v[c]);
+    }
+}
+
 // Running maximum (in base 2) and sum of a row's exponentials.
 struct Softmax {
     float top = -INFINITY, sum = 0.f, plain = 0.f;
 };
 
-// Takes 64 logits from column j of the projection on, of which the first `have`
-// exist.  `at`: the label's place among them, or outside [0, 64).
-__device__ __forceinline__ void take_logits(const ProductParams &p, float (&v)[64], int have, int at, Softmax &s,
+// Takes the first 64 of v, logits of neighbouring columns, of which the first `have`
+// exist (and changes them).  `at`: the label's place among them, or outside [0, 64).
+template <int N>
+__device__ __forceinline__ void take_logits(const ProductParams &p, float (&v)[N], int have, int at, Softmax &s,
                                             float &hit) {
     if (p.softcap != 0.f) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) v[c] = p.softcap * tanhf(v[c] * p.inv_softcap);
+        for (int c = 0; c < 64; ++c) v[c] *= p.inv_softcap;
+        tanh_64(v);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) v[c] *= p.softcap;
     }
     if (p.want_sum) {
         float a = 0.f, b = 0.f;
@@ -484,8 +539,11 @@ __device__ __forceinline__ void take_gradient(const ProductParams &p, float (&v)
     const float lse = row.x, a = row.y, flat = row.z * p.eps_v;
     if (p.softcap != 0.f) {
 #pragma unroll
+        for (int c = 0; c < 64; ++c) v[c] *= p.inv_softcap;
+        tanh_64(v);
+#pragma unroll
         for (int c = 0; c < 64; ++c) {
-            const float u = tanhf(v[c] * p.inv_softcap);
+            const float u = v[c];
             const float d = fmaf(ptx::exp2_approx(fmaf(p.softcap * u, kLog2e, -lse)), a, -flat);
             v[c] = (c == at ? d - row.z * p.one_eps : d) * fmaf(-u, u, 1.f);
         }
@@ -570,6 +628,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
     const int unit = (int)blockIdx.x / share, units = (int)gridDim.x / share;
 
     if (warp == 0) {
+        if constexpr (Cf::GIVE != 0) ptx::regs_give_back<Cf::GIVE>();
         // ---------------------------------------------------------- TMA producer
         // (the whole warp, one elected thread issuing)
         Ring<Cf::STAGES> at;
@@ -579,89 +638,116 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
             const Tile T = tile_at<BN, Cf::ROWS, kSwapped>(p, t, crank);
             if (T.none) continue;
             const int i0 = T.i0 + (int)rank * kLanes, j0 = T.j0 + (int)rank * Cf::Q_ROWS;
-            WarpList list = {nullptr, 0};
-            if (p.mode == kModeGradient) {
-                list.p = p.lists + T.e * p.granules;
-                list.count = (T.kb1 + p.granule_blocks - 1) / p.granule_blocks;
-            } else if (p.mode != kModePlain) {
-                list.p = p.slots + (int64_t)T.g * p.max_slots;
-                list.count = T.slots;
-            }
-            for (int kb = T.kb0; kb < T.kb1; ++kb) {
-                if (!wait_warp(empty(at.slot), at.lap ^ 1u, bounds, kRoleProducer, t)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t fb = full(at.slot), sp = ring0 + (uint32_t)(at.slot * Cf::STAGE), sq = sp + Cf::P_BYTES;
-                const uint32_t to = kPair ? ptx::mapa_shared(fb, 0) : fb;     // a pair's bytes count in the leader
-                const bool add = p.mode == kModeAdd && kb >= p.num_kb;
-                if (add || p.mode == kModeLow) {
-                    // boxes of `box` rows of the adapters', one slot's (or half of one of 128) each
-                    const int pitch = 1 << p.pitch_log2, box = add ? min(pitch, kBlockK) : pitch;
-                    const int row0 = add ? (kb - p.num_kb) * kBlockK : T.i0;
-                    const int boxes = min((add ? kBlockK : kLanes), (T.slots << p.pitch_log2) - row0) / box;
-                    // B^: N-major chunks of 64 columns; A^: K-major rows
-                    constexpr int kAddChunks = kSwapped ? kLanes / 64 : Cf::Q_CHUNKS;
-                    if (add && !waited) {
-                        ptx::pdl_wait();
-                        waited = true;
-                    }
-                    if (ptx::elect_one()) {
-                        const uint32_t bytes =
-                            add ? (uint32_t)(boxes * box * 128 * kAddChunks + (kSwapped ? Cf::Q_ROWS * 128 : Cf::P_BYTES))
-                                : (uint32_t)(boxes * box * 128 + Cf::Q_ROWS * 128);
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(fb, bytes * CG);
-                        if (add) {
-                            if (kSwapped) ptx::tma_load_2d_cg<CG>(sq, &tmLow, to, row0, j0);
-                            else ptx::tma_load_2d_cg<CG>(sp, &tmLow, to, row0, i0);
-                        } else {
-                            ptx::tma_load_2d_cg<CG>(sq, &tmQ, to, kb * kBlockK, j0);
-                        }
-                    }
-                    __syncwarp();
-                    for (int u = 0; u < boxes; ++u) {
-                        const int r = row0 + u * box, ad = list.at(r >> p.pitch_log2), in = r & (pitch - 1);
-                        if (ptx::elect_one()) {
-                            if (add) {
-#pragma unroll
-                                for (int c = 0; c < kAddChunks; ++c)
-                                    ptx::tma_load_3d<CG>((kSwapped ? sp : sq) + (uint32_t)(c * kChunkBytes + u * box * 128),
-                                                         &tmAd, to, (kSwapped ? i0 : j0) + 64 * c, in, ad);
-                            } else {
-                                ptx::tma_load_3d<CG>(sp + (uint32_t)(u * box * 128), &tmAd, to, kb * kBlockK, 0, ad);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                } else {
-                    int k0 = kb * kBlockK, jx = j0;
-                    if (p.mode == kModeGradient) {
-                        // 64 tokens of a granule on the list, and the adapter's slot in it
-                        const int n = kb / p.granule_blocks, entry = list.at(n);
-                        k0 = (entry >> 8) * p.granule + (kb - n * p.granule_blocks) * kBlockK;
-                        jx = (entry & 255) << p.pitch_log2;
-                    }
-                    if (ptx::elect_one()) {
-                        if (rank == 0)
-                            ptx::mbar_arrive_expect_tx(fb, (uint32_t)(Cf::P_BYTES + (p.q_mn ? Cf::Q_BYTES : Cf::Q_ROWS * 128)) * CG);
-                        if (p.p_mn) {
-                            ptx::tma_load_2d_cg<CG>(sp, &tmP, to, i0, k0);
-                            ptx::tma_load_2d_cg<CG>(sp + kChunkBytes, &tmP, to, i0 + 64, k0);
-                        } else {
-                            ptx::tma_load_2d_cg<CG>(sp, &tmP, to, k0, i0);
-                        }
-                        if (p.q_mn) {
-#pragma unroll
-                            for (int c = 0; c < Cf::Q_CHUNKS; ++c)
-                                ptx::tma_load_2d_cg<CG>(sq + (uint32_t)(c * kChunkBytes), &tmQ, to, jx + 64 * c, k0);
-                        } else {
-                            ptx::tma_load_2d_cg<CG>(sq, &tmQ, to, k0, j0);
-                        }
-                    }
-                    __syncwarp();
-                }
+            uint32_t fb = 0, sp = 0, sq = 0, to = 0;
+            // The next ring slot: its barrier, where its operands go, and (of a pair the
+            // leader's) the barrier their bytes count on.
+            auto next_slot = [&]() {
+                if (!wait_warp(empty(at.slot), at.lap ^ 1u, bounds, kRoleProducer, t)) return ok = false;
+                fb = full(at.slot);
+                sp = ring0 + (uint32_t)(at.slot * Cf::STAGE);
+                sq = sp + Cf::P_BYTES;
+                to = kPair ? ptx::mapa_shared(fb, 0) : fb;
                 at.step();
                 ++issued;
+                return true;
+            };
+            if (kSwapped && p.mode == kModeLow) {
+                // the adapters of the tile's lanes: at most eight boxes of `pitch` rows
+                const int pitch = 1 << p.pitch_log2, boxes = min(kLanes, T.i1 - T.i0) >> p.pitch_log2;
+                const int s = (T.i0 >> p.pitch_log2) + (int)lane;
+                const int mine = (int)lane < boxes ? __ldg(p.slots + (int64_t)T.g * p.max_slots + s) : 0;
+                int ad[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) ad[u] = __shfl_sync(0xffffffffu, mine, u);
+                const uint32_t bytes = (uint32_t)((boxes << p.pitch_log2) * 128 + Cf::Q_ROWS * 128);
+                for (int kb = T.kb0; kb < T.kb1 && next_slot(); ++kb) {
+                    if (ptx::elect_one()) {
+                        ptx::mbar_arrive_expect_tx(fb, bytes);
+                        ptx::tma_load_2d(sq, &tmQ, fb, kb * kBlockK, j0);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            if (u < boxes) ptx::tma_load_3d<1>(sp + (uint32_t)(u * pitch * 128), &tmAd, fb, kb * kBlockK, 0, ad[u]);
+                    }
+                    __syncwarp();
+                }
+                continue;
+            }
+            if (kSwapped && p.mode == kModeGradient) {
+                // 64 tokens of a granule on the list at a time, and the adapter's slot in it
+                const int log2_blocks = 31 - __clz(p.granule_blocks);
+                WarpList list = {p.lists + T.e * p.granules, (T.kb1 + p.granule_blocks - 1) >> log2_blocks};
+                for (int kb = T.kb0; kb < T.kb1; ++kb) {
+                    const int entry = list.at(kb >> log2_blocks);
+                    const int k0 = (entry >> 8) * p.granule + (kb & (p.granule_blocks - 1)) * kBlockK;
+                    const int jx = (entry & 255) << p.pitch_log2;
+                    if (!next_slot()) break;
+                    if (ptx::elect_one()) {
+                        ptx::mbar_arrive_expect_tx(fb, (uint32_t)(Cf::P_BYTES + Cf::Q_BYTES));
+                        ptx::tma_load_2d(sp, &tmP, fb, i0, k0);
+                        ptx::tma_load_2d(sp + kChunkBytes, &tmP, fb, i0 + 64, k0);
+#pragma unroll
+                        for (int c = 0; c < Cf::Q_CHUNKS; ++c)
+                            ptx::tma_load_2d(sq + (uint32_t)(c * kChunkBytes), &tmQ, fb, jx + 64 * c, k0);
+                    }
+                    __syncwarp();
+                }
+                continue;
+            }
+            const uint32_t bytes = (uint32_t)(Cf::P_BYTES + (p.q_mn ? Cf::Q_BYTES : Cf::Q_ROWS * 128)) * CG;
+            const int own_kb1 = p.mode == kModeAdd ? min(T.kb1, p.num_kb) : T.kb1;
+            for (int kb = T.kb0; kb < own_kb1 && next_slot(); ++kb) {
+                if (ptx::elect_one()) {
+                    const int k0 = kb * kBlockK;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(fb, bytes);
+                    if (p.p_mn) {
+                        ptx::tma_load_2d_cg<CG>(sp, &tmP, to, i0, k0);
+                        ptx::tma_load_2d_cg<CG>(sp + kChunkBytes, &tmP, to, i0 + 64, k0);
+                    } else {
+                        ptx::tma_load_2d_cg<CG>(sp, &tmP, to, k0, i0);
+                    }
+                    if (p.q_mn) {
+#pragma unroll
+                        for (int c = 0; c < Cf::Q_CHUNKS; ++c)
+                            ptx::tma_load_2d_cg<CG>(sq + (uint32_t)(c * kChunkBytes), &tmQ, to, j0 + 64 * c, k0);
+                    } else {
+                        ptx::tma_load_2d_cg<CG>(sq, &tmQ, to, k0, j0);
+                    }
+                }
+                __syncwarp();
+            }
+            if constexpr (EPI == kEpiSwapped || EPI == kEpiRows) {
+                if (!ok || p.mode != kModeAdd || T.kb1 <= p.num_kb) continue;
+                if (!waited) ptx::pdl_wait();
+                waited = true;
+                // low, and up to four boxes of `box` rows of the adapters' (a slot's, or half
+                // of one of 128) in N-major chunks of 64 columns
+                constexpr int kAddChunks = kSwapped ? kLanes / 64 : Cf::Q_CHUNKS;
+                const int box = min(1 << p.pitch_log2, kBlockK), log2_box = min(p.pitch_log2, 6);
+                WarpList list = {p.slots + (int64_t)T.g * p.max_slots, T.slots};
+                for (int kb = max(T.kb0, p.num_kb); kb < T.kb1; ++kb) {
+                    const int row0 = (kb - p.num_kb) * kBlockK;
+                    const int boxes = min(kBlockK, (T.slots << p.pitch_log2) - row0) >> log2_box;
+                    int ad[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) ad[u] = u < boxes ? list.at((row0 + u * box) >> p.pitch_log2) : 0;
+                    if (!next_slot()) break;
+                    if (ptx::elect_one()) {
+                        const uint32_t some = (uint32_t)(boxes * box * 128 * kAddChunks + (kSwapped ? Cf::Q_ROWS * 128 : Cf::P_BYTES)) * CG;
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(fb, some);
+                        if (kSwapped) ptx::tma_load_2d_cg<CG>(sq, &tmLow, to, row0, j0);
+                        else ptx::tma_load_2d_cg<CG>(sp, &tmLow, to, row0, i0);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (u < boxes) {
+#pragma unroll
+                                for (int c = 0; c < kAddChunks; ++c)
+                                    ptx::tma_load_3d<CG>((kSwapped ? sp : sq) + (uint32_t)(c * kChunkBytes + u * box * 128), &tmAd,
+                                                         to, (kSwapped ? i0 : j0) + 64 * c, row0 & ((1 << p.pitch_log2) - 1),
+                                                         ad[u]);
+                            }
+                    }
+                    __syncwarp();
+                }
             }
         }
         if (!waited) ptx::pdl_wait();      // (this grid ends after the one it depends on)
@@ -686,6 +772,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
         }
         __syncwarp();
     } else if (warp == 1) {
+        if constexpr (Cf::GIVE != 0) ptx::regs_give_back<Cf::GIVE>();
         // ------------------------------------------------------------ MMA issuer
         if (rank == 0) {
             Ring<Cf::STAGES> at;
@@ -702,11 +789,12 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
             if (p.debug_stall) ok = wait_warp(acce(0), 0u, Bounds{abort_flag, p.timeout_ns / 2}, kRoleMma, unit);
             for (int t = unit; ok && t < p.num_tiles; t += units) {
                 const Tile T = tile_at<BN, Cf::ROWS, kSwapped>(p, t, crank);
-                if (T.none || T.kb0 >= T.kb1) continue;
-                if (!wait_warp(acce(acc.slot), acc.lap ^ 1u, bounds, kRoleMma, t)) break;
-                const uint32_t d = tmem + (uint32_t)(acc.slot * BN);
+                if (T.none) continue;
+                int start = T.kb0;                 // of the accumulator's K-blocks
                 for (int kb = T.kb0; kb < T.kb1; ++kb) {
-                    if (!wait_warp(full(at.slot), at.lap, bounds, kRoleMma, t)) {
+                    const bool end = kb + 1 == T.kb1 || (Cf::SEG && kb + 1 == start + Cf::SEG);
+                    if ((kb == start && !wait_warp(acce(acc.slot), acc.lap ^ 1u, bounds, kRoleMma, t)) ||
+                        !wait_warp(full(at.slot), at.lap, bounds, kRoleMma, t)) {
                         ok = false;
                         break;
                     }
@@ -715,7 +803,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                         // (in a cluster the address has the CTA's rank above its 18 bits)
                         const uint32_t sp = ((ring0 + (uint32_t)(at.slot * Cf::STAGE)) & 0x3FFFFu) >> 4,
                                        sq = sp + Cf::P_BYTES / 16;
-                        const uint32_t first = kb == T.kb0 ? 0u : 1u;
+                        const uint32_t d = tmem + (uint32_t)(acc.slot * BN), first = kb == start ? 0u : 1u;
                         if (p.mode == kModeAdd && kb >= p.num_kb) {
                             // low is K-major, the adapters' rows are N-major; 16 values of K for
                             // each 16 rows of the slots there are
@@ -733,7 +821,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                         }
                         if (kPair) ptx::mma_commit_pair(empty(at.slot), 0x3);
                         else ptx::mma_commit(empty(at.slot));
-                        if (kb + 1 == T.kb1) {
+                        if (end) {
                             if (kPair) ptx::mma_commit_pair(accf(acc.slot), 0x3);
                             else ptx::mma_commit(accf(acc.slot));
                         }
@@ -742,14 +830,17 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                     last_bar = empty(at.slot);
                     last_parity = at.lap;
                     at.step();
+                    if (end) {
+                        acc.step();
+                        start = kb + 1;
+                    }
                 }
-                if (!ok) break;
-                acc.step();
             }
             if (*abort_flag && last_bar) wait_landed(last_bar, last_parity, p.timeout_ns);
         }
         __syncwarp();
     } else if (warp >= 4) {
+        if constexpr (Cf::TAKE != 0) ptx::regs_take<Cf::TAKE>();
         // -------------------------------------------------------------- epilogue
         if (p.early) {
             ptx::pdl_wait();
@@ -766,6 +857,48 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
             const Tile T = tile_at<BN, Cf::ROWS, kSwapped>(p, t, crank);
             if (T.none) continue;
             const bool have = T.kb0 < T.kb1;         // (an empty sum is zero)
+            if constexpr (EPI == kEpiStats) {
+                const int64_t i0 = (int64_t)T.i0 + (int)(rank * kLanes + quarter * 32), i = i0 + lane;
+                const int64_t j0 = (int64_t)T.j0 + col0;
+                const bool live = i0 < T.i1 && j0 < T.j1;
+                float v[Cf::COLS];
+#pragma unroll
+                for (int c = 0; c < Cf::COLS; ++c) v[c] = 0.f;
+                bool ok = true;
+                for (int kb = T.kb0; kb < T.kb1; kb += Cf::SEG) {
+                    if (!(ok = wait_warp(accf(acc.slot), acc.lap, bounds, kRoleEpilogue, t))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t src = tbase + (uint32_t)(acc.slot * BN), back = acce_to + 8u * (uint32_t)acc.slot;
+                    if (live) add_columns<Cf::COLS>(src, v);
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (kPair) ptx::mbar_arrive_peer_if(back, lane == 0);
+                    else ptx::mbar_arrive_if(back, lane == 0);
+                    acc.step();
+                }
+                if (!ok) break;
+                if (!live) continue;
+                Softmax soft;
+                const int64_t label = i < T.i1 ? label_column(p, i) : -(1LL << 40);
+#pragma unroll 1
+                for (int s = 0; s < Cf::COLS / 64; ++s) {
+                    const int64_t j = j0 + 64 * s;
+                    if (j >= T.j1) break;
+                    const int64_t rel = label - j;
+                    const int place = rel >= 0 && rel < 64 && rel < T.j1 - j ? (int)rel : -1;
+                    float hit = 0.f;
+                    take_logits(p, v, T.j1 - j < 64 ? (int)(T.j1 - j) : 64, place, soft, hit);
+                    if (place >= 0) p.hits[i] = hit;
+#pragma unroll
+                    for (int c = 0; c + 64 < Cf::COLS; ++c) v[c] = v[c + 64];
+                }
+                if (i < T.i1) {
+                    const int64_t at = j0 / Cf::COLS * p.I + i;
+                    p.parts[at] = make_float2(soft.top, soft.sum);
+                    if (p.want_sum) p.sums[at] = soft.plain;
+                }
+                continue;
+            }
             if (have && !wait_warp(accf(acc.slot), acc.lap, bounds, kRoleEpilogue, t)) break;
             ptx::tc_fence_after();
             const uint32_t src = tbase + (uint32_t)(acc.slot * BN), back = acce_to + 8u * (uint32_t)acc.slot;
@@ -808,13 +941,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 // steps of 64 columns that hold anything of C
                 int steps = i0 < T.i1 && j0 < T.j1 ? (int)((T.j1 - j0 + 63) / 64 < Cf::COLS / 64 ? (T.j1 - j0 + 63) / 64 : Cf::COLS / 64) : 0;
                 if (steps == 0 && have) release();
-                Softmax soft;
-                float hit = 0.f;
                 float4 info = make_float4(0.f, 0.f, 0.f, 0.f);
                 int64_t label = -(1LL << 40);
-                if constexpr (EPI == kEpiStats) {
-                    if (steps && i < T.i1) label = label_column(p, i);
-                }
                 if constexpr (EPI == kEpiDlogits) {
                     if (steps && i < T.i1) {
                         info = __ldg(p.rows + i);
@@ -832,37 +960,26 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
 #pragma unroll
                         for (int c = 0; c < 64; ++c) v[c] = 0.f;
                     }
-                    const int64_t rel = label - j;
-                    const int place = rel >= 0 && rel < 64 ? (int)rel : -1;
-                    if constexpr (EPI == kEpiStats) {
-                        take_logits(p, v, T.j1 - j < 64 ? (int)(T.j1 - j) : 64, place, soft, hit);
-                        if (place >= 0 && j + place < T.j1) p.hits[i] = hit;
-                    } else {
-                        if constexpr (EPI == kEpiDlogits) {
-                            // (a row without a label gives nothing, whatever its logits are)
-                            if (__any_sync(0xffffffffu, info.w != 0.f)) take_gradient(p, v, info, place);
-                            if (info.w == 0.f) {
+                    if constexpr (EPI == kEpiDlogits) {
+                        const int64_t rel = label - j;
+                        // (a row without a label gives nothing, whatever its logits are)
+                        if (__any_sync(0xffffffffu, info.w != 0.f))
+                            take_gradient(p, v, info, rel >= 0 && rel < 64 ? (int)rel : -1);
+                        if (info.w == 0.f) {
 #pragma unroll
-                                for (int c = 0; c < 64; ++c) v[c] = 0.f;
-                            }
-                        } else {
-                            finish_row(p, T, i, j, alpha, v);
+                            for (int c = 0; c < 64; ++c) v[c] = 0.f;
                         }
-                        store_64(p, &tmC, T, i0, j, v, out_buf, (int)lane);
+                    } else {
+                        finish_row(p, T, i, j, alpha, v);
                     }
-                }
-                if constexpr (EPI == kEpiStats) {
-                    if (steps && i < T.i1) {
-                        const int64_t at = j0 / Cf::COLS * p.I + i;
-                        p.parts[at] = make_float2(soft.top, soft.sum);
-                        if (p.want_sum) p.sums[at] = soft.plain;
-                    }
+                    store_64(p, &tmC, T, i0, j, v, out_buf, (int)lane);
                 }
                 if (have) acc.step();
             }
         }
-    } else if (p.early) {
-        ptx::pdl_wait();
+    } else {
+        if constexpr (Cf::GIVE != 0) ptx::regs_give_back<Cf::GIVE>();
+        if (p.early) ptx::pdl_wait();
     }
 
     // Before the CTA's shared memory goes, its TMA stores must have read it.
