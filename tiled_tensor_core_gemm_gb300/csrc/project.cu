@@ -52,6 +52,7 @@ constexpr int kLanes = 128;
 constexpr int kBlockK = 64;
 constexpr int kSmemMax = 232448;
 constexpr int kCtrlBytes = 1024;
+constexpr int kSlotBlocks = 2;             // K-blocks of a ring slot
 constexpr int kChunkBytes = 64 * 128;      // an MN-major chunk: 64 rows of K x 64 values
 constexpr int kBoxBytes = 4096;            // 32 rows x 128 bytes of C
 constexpr float kLog2e = 1.4426950408889634f;
@@ -109,14 +110,18 @@ struct Cfg {
     static constexpr int Q_ROWS = BN / CG;                 // each CTA of a pair loads half of Q's rows
     static constexpr int Q_BYTES = (Q_ROWS < 64 ? 64 : Q_ROWS) * 128;
     static constexpr int Q_CHUNKS = Q_ROWS < 64 ? 1 : Q_ROWS / 64;
-    static constexpr int STAGE = P_BYTES + Q_BYTES;
+    static constexpr int BLOCK = P_BYTES + Q_BYTES;
+    // A ring slot is two K-blocks: what a slot costs its producer and its MMA warp to
+    // wait for, announce and hand on (about 500 cycles each, whatever the tile) is as
+    // much as a 256 x 256 pair's MMAs of one K-block take, and twice a smaller tile's.
+    static constexpr int STAGE = kSlotBlocks * BLOCK;
     static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
     static constexpr int OUT_BYTES = SWAPPED ? 2048 : EPI == kEpiStats ? 0 : kBoxBytes;
     static constexpr int FIXED = 1024 + kCtrlBytes + EW * OUT_BYTES;
     static constexpr int FIT = (kSmemMax - FIXED) / STAGE;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
-    static_assert(STAGES >= 4 && SMEM <= kSmemMax, "ring");
+    static_assert(STAGES >= 3 && SMEM <= kSmemMax, "ring");
     static_assert((2 * STAGES + 4) * 8 + 16 <= kCtrlBytes, "barrier area");
     static_assert(2 * BN <= 512, "two accumulators");
     static_assert(!SWAPPED || kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
@@ -179,7 +184,10 @@ struct Tile {
     int i0, i1, j0, j1;
     int e, g, slots;           // the adapter; the granule and its slots
     int kb0, kb1;
+    int own;                   // where the operands' own K-blocks end and the adapters' begin
     bool none;                 // nothing to do: no slot reaches these lanes
+    // K-blocks of the ring slot that begins with kb (never of both kinds).
+    __device__ __forceinline__ int slot_blocks(int kb) const { return min(kSlotBlocks, (kb < own ? own : kb1) - kb); }
 };
 
 template <int BN, int ROWS, bool SWAPPED>
@@ -219,6 +227,7 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank
     const int each = (total + p.splits - 1) / p.splits;
     T.kb0 = min(total, crank * each);
     T.kb1 = min(total, T.kb0 + each);
+    T.own = p.mode == kModeAdd ? min(T.kb1, p.num_kb) : T.kb1;
     return T;
 }
 
@@ -660,13 +669,19 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
 #pragma unroll
                 for (int u = 0; u < 8; ++u) ad[u] = __shfl_sync(0xffffffffu, mine, u);
                 const uint32_t bytes = (uint32_t)((boxes << p.pitch_log2) * 128 + Cf::Q_ROWS * 128);
-                for (int kb = T.kb0; kb < T.kb1 && next_slot(); ++kb) {
+                for (int kb = T.kb0; kb < T.kb1 && next_slot(); kb += kSlotBlocks) {
+                    const int n = T.slot_blocks(kb);
                     if (ptx::elect_one()) {
-                        ptx::mbar_arrive_expect_tx(fb, bytes);
-                        ptx::tma_load_2d(sq, &tmQ, fb, kb * kBlockK, j0);
+                        ptx::mbar_arrive_expect_tx(fb, bytes * n);
 #pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            if (u < boxes) ptx::tma_load_3d<1>(sp + (uint32_t)(u * pitch * 128), &tmAd, fb, kb * kBlockK, 0, ad[u]);
+                        for (int s = 0; s < kSlotBlocks; ++s) {
+                            if (s >= n) break;
+                            const int k0 = (kb + s) * kBlockK;
+                            ptx::tma_load_2d(sq + s * Cf::BLOCK, &tmQ, fb, k0, j0);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                if (u < boxes) ptx::tma_load_3d<1>(sp + (uint32_t)(s * Cf::BLOCK + u * pitch * 128), &tmAd, fb, k0, 0, ad[u]);
+                        }
                     }
                     __syncwarp();
                 }
@@ -676,41 +691,55 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 // 64 tokens of a granule on the list at a time, and the adapter's slot in it
                 const int log2_blocks = 31 - __clz(p.granule_blocks);
                 WarpList list = {p.lists + T.e * p.granules, (T.kb1 + p.granule_blocks - 1) >> log2_blocks};
-                for (int kb = T.kb0; kb < T.kb1; ++kb) {
-                    const int entry = list.at(kb >> log2_blocks);
-                    const int k0 = (entry >> 8) * p.granule + (kb & (p.granule_blocks - 1)) * kBlockK;
-                    const int jx = (entry & 255) << p.pitch_log2;
+                for (int kb = T.kb0; kb < T.kb1; kb += kSlotBlocks) {
+                    const int n = T.slot_blocks(kb);
+                    int k0[kSlotBlocks], jx[kSlotBlocks];
+#pragma unroll
+                    for (int s = 0; s < kSlotBlocks; ++s) {
+                        const int k = min(kb + s, T.kb1 - 1), entry = list.at(k >> log2_blocks);
+                        k0[s] = (entry >> 8) * p.granule + (k & (p.granule_blocks - 1)) * kBlockK;
+                        jx[s] = (entry & 255) << p.pitch_log2;
+                    }
                     if (!next_slot()) break;
                     if (ptx::elect_one()) {
-                        ptx::mbar_arrive_expect_tx(fb, (uint32_t)(Cf::P_BYTES + Cf::Q_BYTES));
-                        ptx::tma_load_2d(sp, &tmP, fb, i0, k0);
-                        ptx::tma_load_2d(sp + kChunkBytes, &tmP, fb, i0 + 64, k0);
+                        ptx::mbar_arrive_expect_tx(fb, (uint32_t)(Cf::BLOCK * n));
 #pragma unroll
-                        for (int c = 0; c < Cf::Q_CHUNKS; ++c)
-                            ptx::tma_load_2d(sq + (uint32_t)(c * kChunkBytes), &tmQ, fb, jx + 64 * c, k0);
+                        for (int s = 0; s < kSlotBlocks; ++s) {
+                            if (s >= n) break;
+                            ptx::tma_load_2d(sp + s * Cf::BLOCK, &tmP, fb, i0, k0[s]);
+                            ptx::tma_load_2d(sp + s * Cf::BLOCK + kChunkBytes, &tmP, fb, i0 + 64, k0[s]);
+#pragma unroll
+                            for (int c = 0; c < Cf::Q_CHUNKS; ++c)
+                                ptx::tma_load_2d(sq + (uint32_t)(s * Cf::BLOCK + c * kChunkBytes), &tmQ, fb, jx[s] + 64 * c, k0[s]);
+                        }
                     }
                     __syncwarp();
                 }
                 continue;
             }
             const uint32_t bytes = (uint32_t)(Cf::P_BYTES + (p.q_mn ? Cf::Q_BYTES : Cf::Q_ROWS * 128)) * CG;
-            const int own_kb1 = p.mode == kModeAdd ? min(T.kb1, p.num_kb) : T.kb1;
-            for (int kb = T.kb0; kb < own_kb1 && next_slot(); ++kb) {
+            for (int kb = T.kb0; kb < T.own && next_slot(); kb += kSlotBlocks) {
+                const int n = T.slot_blocks(kb);
                 if (ptx::elect_one()) {
-                    const int k0 = kb * kBlockK;
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(fb, bytes);
-                    if (p.p_mn) {
-                        ptx::tma_load_2d_cg<CG>(sp, &tmP, to, i0, k0);
-                        ptx::tma_load_2d_cg<CG>(sp + kChunkBytes, &tmP, to, i0 + 64, k0);
-                    } else {
-                        ptx::tma_load_2d_cg<CG>(sp, &tmP, to, k0, i0);
-                    }
-                    if (p.q_mn) {
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(fb, bytes * n);
 #pragma unroll
-                        for (int c = 0; c < Cf::Q_CHUNKS; ++c)
-                            ptx::tma_load_2d_cg<CG>(sq + (uint32_t)(c * kChunkBytes), &tmQ, to, j0 + 64 * c, k0);
-                    } else {
-                        ptx::tma_load_2d_cg<CG>(sq, &tmQ, to, k0, j0);
+                    for (int s = 0; s < kSlotBlocks; ++s) {
+                        if (s >= n) break;
+                        const int k0 = (kb + s) * kBlockK;
+                        const uint32_t dp = sp + s * Cf::BLOCK, dq = sq + s * Cf::BLOCK;
+                        if (p.p_mn) {
+                            ptx::tma_load_2d_cg<CG>(dp, &tmP, to, i0, k0);
+                            ptx::tma_load_2d_cg<CG>(dp + kChunkBytes, &tmP, to, i0 + 64, k0);
+                        } else {
+                            ptx::tma_load_2d_cg<CG>(dp, &tmP, to, k0, i0);
+                        }
+                        if (p.q_mn) {
+#pragma unroll
+                            for (int c = 0; c < Cf::Q_CHUNKS; ++c)
+                                ptx::tma_load_2d_cg<CG>(dq + (uint32_t)(c * kChunkBytes), &tmQ, to, j0 + 64 * c, k0);
+                        } else {
+                            ptx::tma_load_2d_cg<CG>(dq, &tmQ, to, k0, j0);
+                        }
                     }
                 }
                 __syncwarp();
@@ -724,27 +753,36 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 constexpr int kAddChunks = kSwapped ? kLanes / 64 : Cf::Q_CHUNKS;
                 const int box = min(1 << p.pitch_log2, kBlockK), log2_box = min(p.pitch_log2, 6);
                 WarpList list = {p.slots + (int64_t)T.g * p.max_slots, T.slots};
-                for (int kb = max(T.kb0, p.num_kb); kb < T.kb1; ++kb) {
-                    const int row0 = (kb - p.num_kb) * kBlockK;
-                    const int boxes = min(kBlockK, (T.slots << p.pitch_log2) - row0) >> log2_box;
-                    int ad[4];
+                for (int kb = max(T.kb0, p.num_kb); kb < T.kb1; kb += kSlotBlocks) {
+                    const int n = T.slot_blocks(kb);
+                    int boxes[kSlotBlocks], ad[kSlotBlocks][4], all = 0;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) ad[u] = u < boxes ? list.at((row0 + u * box) >> p.pitch_log2) : 0;
+                    for (int s = 0; s < kSlotBlocks; ++s) {
+                        const int row0 = (kb + s - p.num_kb) * kBlockK;
+                        boxes[s] = s < n ? min(kBlockK, (T.slots << p.pitch_log2) - row0) >> log2_box : 0;
+                        all += boxes[s];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) ad[s][u] = u < boxes[s] ? list.at((row0 + u * box) >> p.pitch_log2) : 0;
+                    }
                     if (!next_slot()) break;
                     if (ptx::elect_one()) {
-                        const uint32_t some = (uint32_t)(boxes * box * 128 * kAddChunks + (kSwapped ? Cf::Q_ROWS * 128 : Cf::P_BYTES)) * CG;
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(fb, some);
-                        if (kSwapped) ptx::tma_load_2d_cg<CG>(sq, &tmLow, to, row0, j0);
-                        else ptx::tma_load_2d_cg<CG>(sp, &tmLow, to, row0, i0);
+                        constexpr int kLow = kSwapped ? Cf::Q_ROWS * 128 : Cf::P_BYTES;
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)(all * box * 128 * kAddChunks + n * kLow) * CG);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            if (u < boxes) {
+                        for (int s = 0; s < kSlotBlocks; ++s) {
+                            if (s >= n) break;
+                            const int row0 = (kb + s - p.num_kb) * kBlockK;
+                            ptx::tma_load_2d_cg<CG>((kSwapped ? sq : sp) + s * Cf::BLOCK, &tmLow, to, row0, kSwapped ? j0 : i0);
 #pragma unroll
-                                for (int c = 0; c < kAddChunks; ++c)
-                                    ptx::tma_load_3d<CG>((kSwapped ? sp : sq) + (uint32_t)(c * kChunkBytes + u * box * 128), &tmAd,
-                                                         to, (kSwapped ? i0 : j0) + 64 * c, row0 & ((1 << p.pitch_log2) - 1),
-                                                         ad[u]);
-                            }
+                            for (int u = 0; u < 4; ++u)
+                                if (u < boxes[s]) {
+#pragma unroll
+                                    for (int c = 0; c < kAddChunks; ++c)
+                                        ptx::tma_load_3d<CG>(
+                                            (kSwapped ? sp : sq) + (uint32_t)(s * Cf::BLOCK + c * kChunkBytes + u * box * 128), &tmAd,
+                                            to, (kSwapped ? i0 : j0) + 64 * c, row0 & ((1 << p.pitch_log2) - 1), ad[s][u]);
+                                }
+                        }
                     }
                     __syncwarp();
                 }
@@ -791,8 +829,9 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 const Tile T = tile_at<BN, Cf::ROWS, kSwapped>(p, t, crank);
                 if (T.none) continue;
                 int start = T.kb0;                 // of the accumulator's K-blocks
-                for (int kb = T.kb0; kb < T.kb1; ++kb) {
-                    const bool end = kb + 1 == T.kb1 || (Cf::SEG && kb + 1 == start + Cf::SEG);
+                for (int kb = T.kb0, next; kb < T.kb1; kb = next) {
+                    next = kb + T.slot_blocks(kb);
+                    const bool end = next == T.kb1 || (Cf::SEG && next == start + Cf::SEG);
                     if ((kb == start && !wait_warp(acce(acc.slot), acc.lap ^ 1u, bounds, kRoleMma, t)) ||
                         !wait_warp(full(at.slot), at.lap, bounds, kRoleMma, t)) {
                         ok = false;
@@ -804,20 +843,29 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                         const uint32_t sp = ((ring0 + (uint32_t)(at.slot * Cf::STAGE)) & 0x3FFFFu) >> 4,
                                        sq = sp + Cf::P_BYTES / 16;
                         const uint32_t d = tmem + (uint32_t)(acc.slot * BN), first = kb == start ? 0u : 1u;
-                        if (p.mode == kModeAdd && kb >= p.num_kb) {
+                        if (kb >= T.own) {
                             // low is K-major, the adapters' rows are N-major; 16 values of K for
                             // each 16 rows of the slots there are
-                            const int steps = min(4, ((T.slots << p.pitch_log2) - (kb - p.num_kb) * kBlockK) / 16);
                             const uint32_t pd = sp | ((kSwapped ? 512u : 1u) << 16), qd = sq | ((kSwapped ? 1u : 512u) << 16);
                             constexpr uint32_t ps = kSwapped ? 128u : 2u, qs = kSwapped ? 2u : 128u;
-                            for (int kk = 0; kk < steps; ++kk)
-                                ptx::mma_f16_sw128<CG>(d, pd + ps * (uint32_t)kk, qd + qs * (uint32_t)kk, p.idesc_add,
-                                                       kk != 0 ? 1u : first);
+                            for (int k = kb; k < next; ++k) {
+                                const int steps = min(4, ((T.slots << p.pitch_log2) - (k - p.num_kb) * kBlockK) / 16);
+                                const uint32_t at_block = (uint32_t)((k - kb) * (Cf::BLOCK / 16));
+                                for (int kk = 0; kk < steps; ++kk)
+                                    ptx::mma_f16_sw128<CG>(d, pd + at_block + ps * (uint32_t)kk, qd + at_block + qs * (uint32_t)kk,
+                                                           p.idesc_add, kk != 0 || k != kb ? 1u : first);
+                            }
                         } else {
                             const uint32_t pd = sp | p_lead, qd = sq | q_lead;
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                ptx::mma_f16_sw128<CG>(d, pd + p_step * kk, qd + q_step * kk, p.idesc, kk != 0 ? 1u : first);
+                            for (int s = 0; s < kSlotBlocks; ++s) {
+                                if (kb + s >= next) break;
+                                const uint32_t at_block = (uint32_t)(s * (Cf::BLOCK / 16));
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    ptx::mma_f16_sw128<CG>(d, pd + at_block + p_step * kk, qd + at_block + q_step * kk, p.idesc,
+                                                           kk != 0 || s != 0 ? 1u : first);
+                            }
                         }
                         if (kPair) ptx::mma_commit_pair(empty(at.slot), 0x3);
                         else ptx::mma_commit(empty(at.slot));
@@ -832,7 +880,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                     at.step();
                     if (end) {
                         acc.step();
-                        start = kb + 1;
+                        start = next;
                     }
                 }
             }
