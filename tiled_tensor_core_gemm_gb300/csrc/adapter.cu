@@ -216,7 +216,7 @@ int run_add(int64_t T, int64_t cols, int type, const Side &x, const void *W, int
     c.epilogue = swap ? kEpiSwapped : kEpiRows;
     const ProductOperand w = {W, cols, ldw, w_k_major ? 0 : 1}, t = {x.p, T, x.ld, 0};
     c.plan = swap ? few : rows;
-    if (!swap && ad.granule < 128 * c.plan.cg) c.plan = {128, 1, 1};
+    if (!swap && ad.granule < 128 * c.plan.cg) c.plan.bn = 128, c.plan.cg = 1;
     c.I = swap ? cols : T;
     c.J = swap ? T : cols;
     c.p = swap ? w : t;

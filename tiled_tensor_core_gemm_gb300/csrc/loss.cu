@@ -125,6 +125,29 @@ loss_rows(int64_t T, int64_t V, int D, const E *__restrict__ H, int64_t ldh, E *
     }
 }
 
+// dH from the FP32 sums of its K ranges, in their order: four columns a thread.
+template <typename E>
+__global__ void __launch_bounds__(256)
+loss_join(int64_t T, int D, int parts, int64_t part_rows, const float *__restrict__ sums, int64_t pitch, E *__restrict__ out,
+          int64_t ldo) {
+    pdl_enter();
+    const int quads = (D + 3) / 4;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < T * quads; n += (int64_t)gridDim.x * 256) {
+        const int64_t t = n / quads;
+        const int c = (int)(n - t * quads) * 4;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const float4 x = __ldcs(reinterpret_cast<const float4 *>(sums + (s * part_rows + t) * pitch + c));
+            a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+        }
+        const float v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c + k < D) out[t * ldo + c + k] = OpType<E>::down(v[k]);
+    }
+}
+
 int no_memory(uint64_t bytes, cudaError_t e) {
     cudaGetLastError();
     char msg[128];
@@ -213,12 +236,12 @@ int plan_packs(LossArgs *a) {
     return rc;
 }
 
-// Vocabulary entries a piece takes, a multiple of 256 below V; V rounded up
-// otherwise.
-int64_t piece_columns(int64_t V, int64_t want) {
+// Vocabulary entries a piece takes: equal pieces of at most `most`, multiples of 256.
+int64_t piece_columns(int64_t V, int64_t most) {
     const int64_t forced = options_snapshot().loss_columns;
-    if (forced) want = forced;
-    return std::min(std::max<int64_t>(want, 64), op_round_up(V, 64));
+    if (forced) return std::min(forced, op_round_up(V, 64));
+    most = std::max<int64_t>(256, most / 256 * 256);
+    return std::min(most, op_round_up(op_cdiv(V, op_cdiv(V, most)), 256));
 }
 
 int64_t packed_w_bytes(const LossArgs &a, int64_t piece) {
@@ -274,7 +297,7 @@ int gemm_project_loss(int64_t T, int64_t V, int64_t D, int dtype, const void *H,
     if ((rc = plan_packs(&a))) return rc;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     // in one piece, unless W has to be copied (256 MB at a time)
-    const int64_t piece = piece_columns(V, a.pack_w ? std::max<int64_t>(256, (1LL << 27) / std::max<int64_t>(D, 1) / 256 * 256) : V);
+    const int64_t piece = piece_columns(V, a.pack_w ? (1LL << 27) / std::max<int64_t>(D, 1) : V + 256);
     const ProductPlan plan = product_plan_rows(T, std::min(piece, V), D, sms);
     const int part_cols = product_part_columns(plan);
     int64_t parts = 0;
@@ -350,15 +373,18 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
     if ((rc = plan_packs(&a))) return rc;
     const int et = a.type;
     const bool f16 = et == GEMM_OUT_F16;
-    // A piece's d is at most 160 MB (the workspaces stay within what the pool keeps),
-    // and a multiple of 256 columns.
-    const int64_t piece = piece_columns(V, std::max<int64_t>(256, (160LL << 20) / 2 / std::max<int64_t>(T, 1) / 256 * 256));
+    // A piece's d is at most 256 MB
+    const int64_t piece = piece_columns(V, (1LL << 27) / T);
     const int64_t pieces = op_cdiv(V, piece), d_pitch = op_round_up(piece, 64), h_pitch = op_round_up(D, 8),
                   acc_pitch = op_round_up(D, 64);
+    // dH = d . W sums over a long piece of the vocabulary into few tiles
+    const ProductPlan h_plan = product_plan_rows(T, D, std::min(piece, V), sms, 16);
+    const int64_t part_rows = op_round_up(T, 256);
+    const bool join = h_plan.parts > 1;
     Workspace ws;
     const uint64_t at_rows = ws.add((uint64_t)T * 16), at_scale = ws.add(8), at_h = ws.add((uint64_t)T * h_pitch * 2),
                    at_d = ws.add((uint64_t)T * d_pitch * 2), at_w = ws.add((uint64_t)packed_w_bytes(a, piece)),
-                   at_acc = ws.add(dH && pieces > 1 ? (uint64_t)T * acc_pitch * 4 : 0);
+                   at_acc = ws.add(!dH ? 0 : join ? (uint64_t)h_plan.parts * part_rows * acc_pitch * 4 : pieces > 1 ? (uint64_t)T * acc_pitch * 4 : 0);
     if ((rc = ws.make(stream))) return rc;
     float4 *rows = reinterpret_cast<float4 *>(ws.base + at_rows);
     float *scale = reinterpret_cast<float *>(ws.base + at_scale), *acc = reinterpret_cast<float *>(ws.base + at_acc);
@@ -398,6 +424,7 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
         d.ldc = d_pitch;
         d.epi.active = 1;
         d.epi.out = et;
+        d.padded = true;
         d.loss = loss_of(a);
         d.loss.first = v;
         d.loss.rows = rows;
@@ -408,12 +435,14 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
             c.I = T;
             c.J = D;
             c.K = cols;
-            c.plan = product_plan_rows(T, D, cols, sms);
+            c.plan = h_plan;
+            c.part_rows = part_rows;
             c.p = {ws.base + at_d, T, d_pitch, 0};
             c.q = {w.p, D, w.ld, w.mn ^ 1};       // (W's entries are the sum now)
             c.old = n > 0 ? acc : nullptr;
             c.ld_old = acc_pitch;
-            const bool last = n + 1 == pieces;
+            const bool last = n + 1 == pieces && !join;
+            c.padded = !last;
             c.C = last ? dH : acc;
             c.ldc = last ? lddh : acc_pitch;
             c.epi.active = 1;
@@ -438,6 +467,16 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
             c.alpha = f16 ? scale + 1 : nullptr;
             if ((rc = product_launch(c, sms, stream))) break;
         }
+    }
+    if (rc == GEMM_OK && dH && join) {
+        auto go = [&](auto e) {
+            using E = decltype(e);
+            return op_launched("loss join",
+                               launch_pdl(loss_join<E>, dim3((unsigned)std::min<int64_t>(op_cdiv(T * op_cdiv(D, 4), 256), sms * 8)),
+                                          dim3(256), 0, stream, T, (int)D, h_plan.parts, part_rows, (const float *)acc, acc_pitch,
+                                          static_cast<E *>(dH), lddh));
+        };
+        rc = f16 ? go(__half()) : go(__nv_bfloat16());
     }
     return ws.done(rc, stream);
 }

@@ -65,6 +65,7 @@ struct ProductParams {
     int tiles_i, tiles_j, num_tiles;
     int group_i;               // raster: lane tiles taken together
     int splits;                // CTAs of a cluster that share a tile's K
+    int k_parts, part_rows;    // K ranges whose sums go to C one below the other, part_rows apart
     int p_mn, q_mn;
     uint32_t idesc, idesc_add; // of the operands, and of low x adapters
     void *C;
@@ -183,6 +184,7 @@ template <int N> struct Ring {
 struct Tile {
     int i0, i1, j0, j1;
     int e, g, slots;           // the adapter; the granule and its slots
+    int down;                  // rows of C above this K range's
     int kb0, kb1;
     int own;                   // where the operands' own K-blocks end and the adapters' begin
     bool none;                 // nothing to do: no slot reaches these lanes
@@ -193,11 +195,11 @@ struct Tile {
 template <int BN, int ROWS, bool SWAPPED>
 __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank) {
     Tile T;
-    T.e = T.g = T.slots = 0;
+    T.e = T.g = T.slots = T.down = 0;
     T.none = false;
     T.i1 = p.I;
     T.j1 = p.J;
-    int total = p.num_kb;
+    int total = p.num_kb, ranges = p.splits, range = crank;
     if (p.mode == kModeLow) {
         // (the first lanes of every token tile first: most granules have few slots)
         const int ti = t / p.tiles_j;
@@ -213,6 +215,13 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank
         T.j0 = 0;
         total = __ldg(p.list_counts + T.e) * p.granule_blocks;
     } else {
+        if (!SWAPPED && p.k_parts > 1) {
+            const int tiles = p.tiles_i * p.tiles_j;
+            ranges = p.k_parts;
+            range = t / tiles;
+            t -= range * tiles;
+            T.down = range * p.part_rows;
+        }
         const int per = p.group_i * p.tiles_j, grp = t / per, first = grp * p.group_i;
         const int gi = min(p.group_i, p.tiles_i - first);
         const int in = t - grp * per;
@@ -224,8 +233,8 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank
             total += ((T.slots << p.pitch_log2) + kBlockK - 1) / kBlockK;
         }
     }
-    const int each = (total + p.splits - 1) / p.splits;
-    T.kb0 = min(total, crank * each);
+    const int each = (total + ranges - 1) / ranges;
+    T.kb0 = min(total, range * each);
     T.kb1 = min(total, T.kb0 + each);
     T.own = p.mode == kModeAdd ? min(T.kb1, p.num_kb) : T.kb1;
     return T;
@@ -405,7 +414,7 @@ __device__ __forceinline__ void store_64(const ProductParams &p, const CUtensorM
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                ptx::tma_store_2d(tmC, buf, (int)jb, (int)i0);
+                ptx::tma_store_2d(tmC, buf, (int)jb, (int)i0 + T.down);
                 ptx::bulk_commit_group();
             }
         } else {
@@ -424,7 +433,7 @@ __device__ __forceinline__ void finish_row(const ProductParams &p, const Tile &T
         for (int c = 0; c < 64; ++c) v[c] *= alpha;
     }
     if (p.old && i < T.i1) {
-        const float *o = p.old + i * p.ld_old + j;          // (rows start on 16 bytes, pitch a multiple of 64)
+        const float *o = p.old + (i + T.down) * p.ld_old + j;          // (rows start on 16 bytes, pitch a multiple of 64)
 #pragma unroll
         for (int c = 0; c < 64; c += 4) {
             if (j + c >= T.j1) break;
@@ -1182,18 +1191,32 @@ int encode_operand(CUtensorMap *m, const ProductOperand &o, int type, int64_t K,
 int product_part_columns(const ProductPlan &plan) { return plan.cg == 2 ? 128 : 64; }
 
 // Tile of a product with the tokens (or whatever else there is much of) on the
-// lanes, by the rounds of tiles and a tile's pace.
-ProductPlan product_plan_rows(int64_t I, int64_t J, int64_t K, int sms) {
-    const double kb = (double)op_cdiv(K, kBlockK);
-    const double pair = (double)op_cdiv(op_cdiv(I, 256) * op_cdiv(J, 256), sms / 2) * (kb * 2. + 12.);
-    const double one = (double)op_cdiv(op_cdiv(I, 128) * op_cdiv(J, 128), sms) * (kb * 1.1 + 8.);
-    ProductPlan pl;
-    pl.cg = pair <= one ? 2 : 1;
-    pl.bn = pl.cg == 2 ? 256 : 128;
+// lanes, and (most_parts > 1) into how many K ranges its tiles go, by the rounds of
+// tiles and a tile's pace, in us: 0.27 a K-block of a 256 x 256 pair (its MMAs) and
+// 0.3 of 128 x 128 (its operands from L2), and what does not overlap at a tile's
+// ends.  K ranges are for few tiles over a long K; their FP32 sums are written and
+// read again.
+ProductPlan product_plan_rows(int64_t I, int64_t J, int64_t K, int sms, int most_parts) {
+    const int64_t kb = op_cdiv(K, kBlockK);
     const Options opt = options_snapshot();
-    if (opt.product_bn == 256) pl = {256, 2, 1};
-    if (opt.product_bn == 128) pl = {128, 1, 1};
-    return pl;
+    ProductPlan best;
+    double least = 0.;
+    for (int cg = 2; cg >= 1; --cg) {
+        if (opt.product_bn && opt.product_bn != 128 * cg) continue;
+        const int64_t tiles = op_cdiv(I, 128 * cg) * op_cdiv(J, 128 * cg);
+        for (int parts = 1; parts <= most_parts; ++parts) {
+            if (parts > 1 && (kb < 8 * parts || (double)parts * I * J > 3.2e7)) break;
+            const double rounds = (double)op_cdiv(tiles * parts, sms / cg);
+            const double cost = rounds * (op_cdiv(kb, parts) * (cg == 2 ? 0.27 : 0.3) + (cg == 2 ? 2. : 1.5)) +
+                                (parts > 1 ? 4. + (double)parts * I * J * 8. / 5e6 : 0.);
+            if (best.bn && cost >= least) continue;
+            least = cost;
+            best.bn = 128 * cg;
+            best.cg = cg;
+            best.parts = parts;
+        }
+    }
+    return best;
 }
 
 // K ranges for `tiles` swapped tiles of bn columns.
@@ -1207,7 +1230,8 @@ static ProductPlan plan_splits(int bn, int64_t tiles, int64_t kb, int sms) {
         const double cost = (double)op_cdiv(tiles * splits, sms) * (op_cdiv(kb, splits) * pace + 3.) + (splits > 1 ? 6. : 0.);
         const bool forced = opt.product_splits == splits;
         if (best.bn && cost >= least && !forced) continue;
-        best = {bn, 1, splits};
+        best.bn = bn;
+        best.splits = splits;
         least = cost;
         if (forced) break;
     }
@@ -1243,13 +1267,15 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     p.num_kb = (int)op_cdiv(c.K, kBlockK);
     p.group_i = pl.cg == 2 ? 8 : 16;
     p.splits = pl.splits;
+    p.k_parts = std::max(1, pl.parts);
+    p.part_rows = p.k_parts > 1 ? (int)c.part_rows : 0;
     const ProductAdapters &ad = c.ad;
     int64_t ti = op_cdiv(c.I, kLanes * pl.cg), tj = op_cdiv(c.J, pl.bn);
     if (c.mode == kModeGradient) tj = ad.count;      // (an adapter's rank is one tile wide)
-    if (ti * tj * pl.splits > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
+    if (ti * tj * pl.splits * p.k_parts > kMax || (int64_t)p.k_parts * p.part_rows > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
     p.tiles_i = (int)ti;
     p.tiles_j = (int)tj;
-    p.num_tiles = (int)(ti * tj);
+    p.num_tiles = (int)(ti * tj * p.k_parts);
     if (p.num_tiles == 0) return GEMM_OK;
     p.p_mn = c.p.mn;
     p.q_mn = c.q.mn;
@@ -1309,10 +1335,10 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     if (c.epilogue != kEpiStats) {
         const int ob = op_type_bytes(p.epi.out);
         p.wide = op_wide(c.C, c.ldc, ob) && (c.c_stride * ob) % 16 == 0;
-        // (the logits' gradient goes to a workspace whose rows have room for whole boxes)
-        const int64_t cols = c.epilogue == kEpiDlogits ? op_round_up(c.J, 64) : c.J;
+        const int64_t cols = c.padded ? op_round_up(c.J, 64) : c.J;
         p.tma_store = !swapped && p.wide && (cols * ob) % 16 == 0;
-        if (p.tma_store && (rc = encode(&m.c, c.C, p.epi.out, c.I, cols, c.ldc, 32))) return rc;
+        const int64_t rows = p.k_parts > 1 ? (int64_t)p.k_parts * p.part_rows : c.I;
+        if (p.tma_store && (rc = encode(&m.c, c.C, p.epi.out, rows, cols, c.ldc, 32))) return rc;
     }
     const int64_t units = std::min<int64_t>(p.num_tiles, pl.splits > 1 ? p.num_tiles : sms / pl.cg);
     return launch_plan(pl, c.epilogue, m, p, (int)(units * pl.cg * pl.splits), stream);

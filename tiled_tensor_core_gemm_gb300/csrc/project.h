@@ -55,9 +55,10 @@ enum ProductMode : int {
 };
 enum ProductEpilogue : int { kEpiSwapped = 0, kEpiRows = 1, kEpiStats = 2, kEpiDlogits = 3 };
 
-// Lanes x columns of the tile, CTAs of it, K ranges.
+// Columns of the tile, CTAs of it, its K ranges within a cluster (swapped) or through
+// memory (row-wise).
 struct ProductPlan {
-    int bn = 0, cg = 1, splits = 1;
+    int bn = 0, cg = 1, splits = 1, parts = 1;
 };
 
 struct ProductCall {
@@ -71,6 +72,9 @@ struct ProductCall {
     void *C = nullptr;                     // swapped: C's columns are the lanes
     int64_t ldc = 0;
     int64_t c_stride = 0;                  // kModeGradient: between adapters' results
+    int64_t part_rows = 0;                 // plan.parts > 1: rows of C between the ranges' sums,
+                                           // at least I rounded up to 256
+    bool padded = false;                   // C's rows have room for 64 columns at a time
     EpiParams epi;
     const float *old = nullptr;            // FP32 sums to add (row-wise epilogue), pitch ld_old
     int64_t ld_old = 0;
@@ -83,7 +87,7 @@ struct ProductCall {
 int product_launch(const ProductCall &call, int sms, cudaStream_t stream);
 
 // Tiles and K ranges: see project.cu.
-ProductPlan product_plan_rows(int64_t I, int64_t J, int64_t K, int sms);
+ProductPlan product_plan_rows(int64_t I, int64_t J, int64_t K, int sms, int most_parts = 1);
 ProductPlan product_plan_tokens(int64_t tokens, int64_t cols, int64_t K, int sms);
 
 ProductPlan product_plan_low(int64_t tokens, int64_t lanes, int64_t K, int sms);
