@@ -297,8 +297,8 @@ GEMM_API int gemm_get_status(struct CUstream_st *stream);
  *                    capacity in records
  *   "product_bn"     columns of a tile of the row-wise 16-bit products
  *                    (gemm_project.h): 128 (one CTA) or 256 (a CTA pair)
- *   "product_splits" K ranges (1, 2, 4) of their tiles of few tokens, where
- *                    that many fit one round of clusters
+ *   "product_splits" K ranges (1..4) of their tiles of few tokens, where K
+ *                    has four blocks of 64 for each
  *   "loss_columns"   vocabulary entries a piece of the projection's loss
  *                    takes, a multiple of 64
  *   "wait_timeout_ms" bound on every in-kernel wait (default 2000)

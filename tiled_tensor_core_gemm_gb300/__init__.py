@@ -25,6 +25,15 @@ documentation):
     gemm_experts(A, a_scale, W, w_scale, offsets) -> C  one product per expert, sizes on the device
     route(logits, top_k) -> Routing, route_backward     tokens to experts, and the logits' gradient
     combine(Y, slots, weights) -> out, combine_backward the weighted sum of the experts' rows
+
+The products around a language model's weights in 16 bits (include/gemm_project.h;
+projection.py has their documentation):
+
+    project_loss(H, W, labels) -> (loss, lse)           cross entropy of H.W^T, the logits never stored
+    project_loss_backward(grad, ...) -> (dH, dW)
+    adapter_plan(ids, adapters) -> AdapterPlan          which tokens take which low-rank adapter
+    gemm_adapters(X, W, A, B, plan) -> C                a shared projection plus each token's adapter
+    gemm_adapters_backward(dY, ...) -> (dX, dA, dB)
 """
 from __future__ import annotations
 
@@ -56,7 +65,9 @@ OUT_TYPES = {"f32": GEMM_OUT_F32, "bf16": GEMM_OUT_BF16, "f16": GEMM_OUT_F16}
 EXPORTED = ("gemm_run", "gemm_last_error", "gemm_get_status", "gemm_set_option",
             "gemm_get_option", "gemm_plan", "gemm_version", "gemm_run_tf32_static", "gemm_run_ex",
             "gemm_run_grouped", "gemm_quantize_block", "gemm_run_scaled", "gemm_run_experts", "gemm_route",
-            "gemm_route_backward", "gemm_combine", "gemm_combine_backward")
+            "gemm_route_backward", "gemm_combine", "gemm_combine_backward", "gemm_project_loss",
+            "gemm_project_loss_backward", "gemm_adapter_plan_words", "gemm_adapter_plan", "gemm_adapters",
+            "gemm_adapters_backward")
 TF32_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024   # GEMM_TF32_STATIC_SCRATCH_BYTES in include/gemm.h
 
 

@@ -141,7 +141,8 @@ int check_sizes(int64_t T, int64_t N, int64_t K, int dtype, int64_t ldw, int w_m
     if (ad->count < 1 || ad->count > kMaxAdapters) return invalid("adapters must be in [1, 4096]");
     if (ad->rank < 1 || ad->rank > 128) return invalid("rank must be in [1, 128]");
     if (ad->lda < std::max<int64_t>(K, 1) || ad->ldb < std::max<int64_t>(N, 1) || ad->lda > kLdMax || ad->ldb > kLdMax ||
-        ad->a_stride < 0 || ad->b_stride < 0 || ad->a_stride > (1LL << 38) || ad->b_stride > (1LL << 38))
+        (ad->count > 1 && (ad->a_stride < std::max<int64_t>(K, 1) || ad->b_stride < std::max<int64_t>(N, 1))) || ad->a_stride < 0 ||
+        ad->b_stride < 0 || ad->a_stride > (1LL << 38) || ad->b_stride > (1LL << 38))
         return invalid("leading dimension or stride of the adapters out of range");
     return GEMM_OK;
 }

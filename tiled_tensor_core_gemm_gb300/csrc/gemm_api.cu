@@ -434,7 +434,7 @@ int gemm_set_option(const char *key, int64_t v) {
         if (v != 0 && v != 128 && v != 256) return fail(GEMM_ERR_INVALID_ARG, "product_bn must be 0, 128 or 256");
         g_opt.product_bn = (int)v;
     } else if (!std::strcmp(key, "product_splits")) {
-        if (v != 0 && v != 1 && v != 2 && v != 4) return fail(GEMM_ERR_INVALID_ARG, "product_splits must be 0, 1, 2 or 4");
+        if (v < 0 || v > 4) return fail(GEMM_ERR_INVALID_ARG, "product_splits must be in [0, 4]");
         g_opt.product_splits = (int)v;
     } else if (!std::strcmp(key, "loss_columns")) {
         if (v < 0 || v > (1 << 24) || v % 64) return fail(GEMM_ERR_INVALID_ARG, "loss_columns must be a multiple of 64 in [0, 2^24]");

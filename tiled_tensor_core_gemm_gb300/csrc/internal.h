@@ -27,7 +27,7 @@ struct Options {
     int tc_split_reduce = 0;   // 0 auto, 1 workspace + reduce kernel, 2 cluster shared memory
     int tc_split_lead = 0;     // two K ranges: percent of k-blocks in the first (0 auto, 50 even)
     int product_bn = 0;        // 0 auto, else 128/256: columns of the row-wise 16-bit product's tiles
-    int product_splits = 0;    // 0 auto, else 1/2/4 K ranges of its tiles of few tokens, where they fit
+    int product_splits = 0;    // 0 auto, else 1..4 K ranges of its tiles of few tokens
     int loss_columns = 0;      // 0 auto, else vocabulary entries a piece of the loss takes
     int wait_timeout_ms = 2000;
     int64_t trace_addr = 0;    // device address of a trace buffer (0: off)

@@ -35,32 +35,42 @@ __device__ __forceinline__ void join(float2 &a, float2 b) {
     a.x = top;
 }
 
-// 32 tokens a block, one a lane; the warps share the parts, and join theirs in the
-// order of the warps.
+// TOKENS tokens a block (fewer where there are few, so that blocks fill the SMs), the
+// threads of a token sharing its parts: joined within a warp by a butterfly, then over
+// the warps in their order, so the result does not depend on timing.
+template <int TOKENS>
 __global__ void __launch_bounds__(32 * kFinishWarps)
 loss_finish(int64_t T, int64_t V, int parts, const float2 *__restrict__ part, const float *__restrict__ sums,
             const float *__restrict__ hits, const void *labels, int label_bytes, gemm_loss_t how, float *loss, float *lse) {
     pdl_enter();
-    __shared__ float2 soft[kFinishWarps][32];
-    __shared__ float plain[kFinishWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+    __shared__ float2 soft[kFinishWarps][TOKENS];
+    __shared__ float plain[kFinishWarps][TOKENS];
+    constexpr int kWorkers = 32 * kFinishWarps / TOKENS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = threadIdx.x % TOKENS;
+    const int64_t t = (int64_t)blockIdx.x * TOKENS + mine;
     float2 m = make_float2(-INFINITY, 0.f);
     float s = 0.f;
     if (t < T) {
 #pragma unroll 4
-        for (int i = warp; i < parts; i += kFinishWarps) {
+        for (int i = threadIdx.x / TOKENS; i < parts; i += kWorkers) {
             join(m, __ldg(part + (int64_t)i * T + t));
             if (sums) s += __ldg(sums + (int64_t)i * T + t);
         }
     }
-    soft[warp][lane] = m;
-    plain[warp][lane] = s;
+#pragma unroll
+    for (int d = TOKENS; d < 32; d <<= 1) {
+        join(m, make_float2(__shfl_xor_sync(0xffffffffu, m.x, d), __shfl_xor_sync(0xffffffffu, m.y, d)));
+        s += __shfl_xor_sync(0xffffffffu, s, d);
+    }
+    if (lane < TOKENS) {
+        soft[warp][mine] = m;
+        plain[warp][mine] = s;
+    }
     __syncthreads();
-    if (warp != 0 || t >= T) return;
+    if (threadIdx.x >= TOKENS || t >= T) return;
     for (int w = 1; w < kFinishWarps; ++w) {
-        join(m, soft[w][lane]);
-        s += plain[w][lane];
+        join(m, soft[w][mine]);
+        s += plain[w][mine];
     }
     const float total = kLn2 * (m.x + log2f(m.y));
     lse[t] = total;
@@ -298,10 +308,9 @@ int gemm_project_loss(int64_t T, int64_t V, int64_t D, int dtype, const void *H,
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     // in one piece, unless W has to be copied (256 MB at a time)
     const int64_t piece = piece_columns(V, a.pack_w ? (1LL << 27) / std::max<int64_t>(D, 1) : V + 256);
-    const ProductPlan plan = product_plan_rows(T, std::min(piece, V), D, sms);
-    const int part_cols = product_part_columns(plan);
+    const ProductPlan plan = product_plan_stats(T, std::min(piece, V), D, !a.w_major, sms);
     int64_t parts = 0;
-    for (int64_t v = 0; v < V; v += piece) parts += op_cdiv(std::min(piece, V - v), part_cols);
+    for (int64_t v = 0; v < V; v += piece) parts += product_parts(plan, std::min(piece, V - v));
     if (parts > 0x7fffffffLL) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
     const int64_t h_pitch = a.pack_h ? op_round_up(D, 8) : a.ldh;
     Workspace ws;
@@ -330,15 +339,22 @@ int gemm_project_loss(int64_t T, int64_t V, int64_t D, int dtype, const void *H,
         c.loss.first = v;
         c.loss.parts = reinterpret_cast<float2 *>(ws.base + at_parts) + part * T;
         c.loss.sums = reinterpret_cast<float *>(ws.base + at_sums) + part * T;
-        part += op_cdiv(c.J, part_cols);
+        part += product_parts(plan, c.J);
         rc = product_launch(c, sms, stream);
     }
-    if (rc == GEMM_OK)
-        rc = op_launched("loss", launch_pdl(loss_finish, dim3((unsigned)op_cdiv(T, 32)), dim3(32 * kFinishWarps), 0, stream, T, V,
-                                            (int)parts, reinterpret_cast<const float2 *>(ws.base + at_parts),
-                                            a.how.smoothing != 0.f ? reinterpret_cast<const float *>(ws.base + at_sums) : nullptr,
-                                            reinterpret_cast<const float *>(ws.base + at_hits), labels, label_bytes, a.how, loss,
-                                            lse));
+    if (rc == GEMM_OK) {
+        auto finish = [&](auto tokens) {
+            constexpr int kTokens = decltype(tokens)::value;
+            return op_launched("loss", launch_pdl(loss_finish<kTokens>, dim3((unsigned)op_cdiv(T, kTokens)), dim3(32 * kFinishWarps), 0,
+                                                  stream, T, V, (int)parts, reinterpret_cast<const float2 *>(ws.base + at_parts),
+                                                  a.how.smoothing != 0.f ? reinterpret_cast<const float *>(ws.base + at_sums) : nullptr,
+                                                  reinterpret_cast<const float *>(ws.base + at_hits), labels, label_bytes, a.how,
+                                                  loss, lse));
+        };
+        if (T <= 256) rc = finish(std::integral_constant<int, 1>());
+        else if (T <= 2048) rc = finish(std::integral_constant<int, 8>());
+        else rc = finish(std::integral_constant<int, 32>());
+    }
     return ws.done(rc, stream);
 }
 

@@ -63,6 +63,7 @@ struct ProductParams {
     int mode;
     int I, J, num_kb;
     int tiles_i, tiles_j, num_tiles;
+    int width;                 // columns of a tile: BN, or (statistics) fewer
     int group_i;               // raster: lane tiles taken together
     int splits;                // CTAs of a cluster that share a tile's K
     int k_parts, part_rows;    // K ranges whose sums go to C one below the other, part_rows apart
@@ -93,7 +94,7 @@ struct ProductParams {
     unsigned long long timeout_ns;
 };
 
-template <int BN, int CG, int EPI>
+template <int BN, int CG, int EPI, int PROWS>
 struct Cfg {
     static constexpr bool SWAPPED = EPI == kEpiSwapped;
     static constexpr int EW = BN <= 32 ? 4 : 8;            // epilogue warps
@@ -107,11 +108,14 @@ struct Cfg {
     // Registers a thread after the first warpgroup has given some up (0: as launched).
     static constexpr int GIVE = EPI == kEpiStats && COLS > 64 ? 56 : 0, TAKE = GIVE ? 224 : 0;
     static_assert(GIVE == 0 || 128 * GIVE + EW * 32 * TAKE <= THREADS * 168, "the shares exceed the launch's registers");
-    static constexpr int P_BYTES = kLanes * 128;
+    // Rows of P a CTA loads.  With 32 the MMAs read what follows as further lanes,
+    // which nobody looks at: few tokens stream W through a ring that is nearly all W's.
+    static constexpr int P_BYTES = PROWS * 128;
     static constexpr int Q_ROWS = BN / CG;                 // each CTA of a pair loads half of Q's rows
     static constexpr int Q_BYTES = (Q_ROWS < 64 ? 64 : Q_ROWS) * 128;
     static constexpr int Q_CHUNKS = Q_ROWS < 64 ? 1 : Q_ROWS / 64;
     static constexpr int BLOCK = P_BYTES + Q_BYTES;
+    static_assert(PROWS == kLanes || (EPI == kEpiStats && Q_BYTES + P_BYTES >= kLanes * 128), "P's rows");
     // A ring slot is two K-blocks: what a slot costs its producer and its MMA warp to
     // wait for, announce and hand on (about 500 cycles each, whatever the tile) is as
     // much as a 256 x 256 pair's MMAs of one K-block take, and twice a smaller tile's.
@@ -226,7 +230,8 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank
         const int gi = min(p.group_i, p.tiles_i - first);
         const int in = t - grp * per;
         T.i0 = (first + in % gi) * ROWS;
-        T.j0 = in / gi * BN;
+        T.j0 = in / gi * p.width;
+        T.j1 = min(p.J, T.j0 + p.width);
         if (p.mode == kModeAdd) {
             T.g = (SWAPPED ? T.j0 : T.i0) / p.granule;
             T.slots = __ldg(p.counts + T.g);
@@ -575,12 +580,12 @@ __device__ __forceinline__ void take_gradient(const ProductParams &p, float (&v)
     }
 }
 
-template <int BN, int CG, int EPI>
-__global__ void __launch_bounds__((Cfg<BN, CG, EPI>::THREADS), 1)
+template <int BN, int CG, int EPI, int PROWS>
+__global__ void __launch_bounds__((Cfg<BN, CG, EPI, PROWS>::THREADS), 1)
 product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                const __grid_constant__ CUtensorMap tmLow, const __grid_constant__ CUtensorMap tmAd,
                const __grid_constant__ CUtensorMap tmC, const ProductParams p) {
-    using Cf = Cfg<BN, CG, EPI>;
+    using Cf = Cfg<BN, CG, EPI, PROWS>;
     constexpr bool kPair = CG == 2, kSwapped = Cf::SWAPPED;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -655,7 +660,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
         for (int t = unit; ok && t < p.num_tiles; t += units) {
             const Tile T = tile_at<BN, Cf::ROWS, kSwapped>(p, t, crank);
             if (T.none) continue;
-            const int i0 = T.i0 + (int)rank * kLanes, j0 = T.j0 + (int)rank * Cf::Q_ROWS;
+            const int i0 = T.i0 + (int)rank * kLanes, j0 = T.j0 + (int)rank * (p.width / CG);
             uint32_t fb = 0, sp = 0, sq = 0, to = 0;
             // The next ring slot: its barrier, where its operands go, and (of a pair the
             // leader's) the barrier their bytes count on.
@@ -726,7 +731,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 }
                 continue;
             }
-            const uint32_t bytes = (uint32_t)(Cf::P_BYTES + (p.q_mn ? Cf::Q_BYTES : Cf::Q_ROWS * 128)) * CG;
+            const uint32_t bytes = (uint32_t)(Cf::P_BYTES + (p.q_mn ? Cf::Q_BYTES : p.width / CG * 128)) * CG;
             for (int kb = T.kb0; kb < T.own && next_slot(); kb += kSlotBlocks) {
                 const int n = T.slot_blocks(kb);
                 if (ptx::elect_one()) {
@@ -934,7 +939,14 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                     acc.step();
                 }
                 if (!ok) break;
-                if (!live) continue;
+                const int64_t part = (T.j0 / p.width * (BN / Cf::COLS) + (int)half) * (int64_t)p.I + i;
+                if (!live) {
+                    if (i < T.i1) {              // a last tile of few columns: nothing in this half
+                        p.parts[part] = make_float2(-INFINITY, 0.f);
+                        if (p.want_sum) p.sums[part] = 0.f;
+                    }
+                    continue;
+                }
                 Softmax soft;
                 const int64_t label = i < T.i1 ? label_column(p, i) : -(1LL << 40);
 #pragma unroll 1
@@ -950,9 +962,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                     for (int c = 0; c + 64 < Cf::COLS; ++c) v[c] = v[c + 64];
                 }
                 if (i < T.i1) {
-                    const int64_t at = j0 / Cf::COLS * p.I + i;
-                    p.parts[at] = make_float2(soft.top, soft.sum);
-                    if (p.want_sum) p.sums[at] = soft.plain;
+                    p.parts[part] = make_float2(soft.top, soft.sum);
+                    if (p.want_sum) p.sums[part] = soft.plain;
                 }
                 continue;
             }
@@ -1050,7 +1061,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
         if (warp >= 4 && unit < p.num_tiles && *abort_flag == 0) {
             const Tile T = tile_at<BN, Cf::ROWS, kSwapped>(p, unit, crank);
             if (!T.none) {
-                const int per = BN / p.splits, c0 = crank * per, quads = per * (kLanes / 4);
+                const int c0 = BN * crank / p.splits, quads = (BN * (crank + 1) / p.splits - c0) * (kLanes / 4);
                 constexpr int kStep = Cf::EW * 32;
                 const int64_t cc = (int64_t)T.i0 + 4 * (int)lane;          // (a warp's lanes take a whole row of the tile)
                 float side[4];
@@ -1129,10 +1140,10 @@ struct Maps {
     CUtensorMap p, q, low, ad, c;
 };
 
-template <int BN, int CG, int EPI>
+template <int BN, int CG, int EPI, int PROWS = kLanes>
 int launch(const Maps &m, const ProductParams &p, int grid, cudaStream_t stream) {
-    using Cf = Cfg<BN, CG, EPI>;
-    auto kern = product_kernel<BN, CG, EPI>;
+    using Cf = Cfg<BN, CG, EPI, PROWS>;
+    auto kern = product_kernel<BN, CG, EPI, PROWS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
     if (e != cudaSuccess) return op_launched("cudaFuncSetAttribute", e);
     cudaLaunchConfig_t cfg = {};
@@ -1167,6 +1178,7 @@ int launch_plan(const ProductPlan &pl, int epilogue, const Maps &m, const Produc
         return launch<128, 1, kEpiSwapped>(m, p, grid, stream);
     }
     const bool pair = pl.cg == 2;
+    if (epilogue == kEpiStats && pair && pl.p_rows == 32) return launch<256, 2, kEpiStats, 32>(m, p, grid, stream);
     if (epilogue == kEpiStats)
         return pair ? launch<256, 2, kEpiStats>(m, p, grid, stream) : launch<128, 1, kEpiStats>(m, p, grid, stream);
     if (epilogue == kEpiDlogits)
@@ -1188,7 +1200,10 @@ int encode_operand(CUtensorMap *m, const ProductOperand &o, int type, int64_t K,
 
 }  // namespace
 
-int product_part_columns(const ProductPlan &plan) { return plan.cg == 2 ? 128 : 64; }
+int64_t product_parts(const ProductPlan &plan, int64_t cols) {
+    // (both kernels have two halves of epilogue warps)
+    return 2 * op_cdiv(cols, plan.width ? plan.width : plan.bn);
+}
 
 // Tile of a product with the tokens (or whatever else there is much of) on the
 // lanes, and (most_parts > 1) into how many K ranges its tiles go, by the rounds of
@@ -1219,22 +1234,30 @@ ProductPlan product_plan_rows(int64_t I, int64_t J, int64_t K, int sms, int most
     return best;
 }
 
-// K ranges for `tiles` swapped tiles of bn columns.
+// Few tokens stream the weights: the widest tiles that still take as few rounds
+// leave the last round no emptier than it must be (50021 x 2048: 196 tiles of 256
+// columns on 76 pairs are 2.6 rounds run as 3; of 224 columns 2.9).
+ProductPlan product_plan_stats(int64_t tokens, int64_t vocab, int64_t K, bool any, int sms) {
+    ProductPlan pl = product_plan_rows(tokens, vocab, K, sms);
+    if (!any || tokens > 256) return pl;
+    const int64_t units = sms / pl.cg, rounds = op_cdiv(op_cdiv(vocab, pl.bn), units);
+    const int64_t width = op_round_up(op_cdiv(vocab, rounds * units), 32);
+    pl.width = (int)std::min<int64_t>(std::max<int64_t>(width, pl.bn / 2 + 32), pl.bn);
+    if (tokens <= 32 && pl.cg == 2) pl.p_rows = 32;
+    return pl;
+}
+
+// K ranges for `tiles` swapped tiles of bn columns, `kb` K-blocks each: as many as
+// one round of clusters takes (a second round costs more than the ranges give:
+// 64 x 4096 x 12288 in 2 ranges 54 us, whole 41), while each has two slots' worth.
+// Measured at 64 x 4096 x 8192: whole 33 us, 2 ranges 29; 48 x 4096 x 4096: 35, 29,
+// 28 and 27 in 1 to 4.
 static ProductPlan plan_splits(int bn, int64_t tiles, int64_t kb, int sms) {
+    const int forced = options_snapshot().product_splits;
     ProductPlan best;
-    double least = 0.;
-    const double pace = bn <= 64 ? 1. : 1.2;
-    const Options opt = options_snapshot();
-    for (int splits = 1; splits <= 4; splits *= 2) {
-        if (splits > 1 && (tiles * splits > sms || kb < 2 * splits)) continue;
-        const double cost = (double)op_cdiv(tiles * splits, sms) * (op_cdiv(kb, splits) * pace + 3.) + (splits > 1 ? 6. : 0.);
-        const bool forced = opt.product_splits == splits;
-        if (best.bn && cost >= least && !forced) continue;
-        best.bn = bn;
-        best.splits = splits;
-        least = cost;
-        if (forced) break;
-    }
+    best.bn = bn;
+    for (int splits = 2; splits <= 4; ++splits)
+        if (kb >= 4 * splits && (forced ? forced == splits : tiles * splits <= sms)) best.splits = splits;
     return best;
 }
 
@@ -1270,7 +1293,8 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     p.k_parts = std::max(1, pl.parts);
     p.part_rows = p.k_parts > 1 ? (int)c.part_rows : 0;
     const ProductAdapters &ad = c.ad;
-    int64_t ti = op_cdiv(c.I, kLanes * pl.cg), tj = op_cdiv(c.J, pl.bn);
+    p.width = pl.width ? pl.width : pl.bn;
+    int64_t ti = op_cdiv(c.I, kLanes * pl.cg), tj = op_cdiv(c.J, p.width);
     if (c.mode == kModeGradient) tj = ad.count;      // (an adapter's rank is one tile wide)
     if (ti * tj * pl.splits * p.k_parts > kMax || (int64_t)p.k_parts * p.part_rows > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
     p.tiles_i = (int)ti;
@@ -1279,7 +1303,7 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     if (p.num_tiles == 0) return GEMM_OK;
     p.p_mn = c.p.mn;
     p.q_mn = c.q.mn;
-    p.idesc = idesc_of(c.type, pl.bn, pl.cg, p.p_mn, p.q_mn);
+    p.idesc = idesc_of(c.type, p.width, pl.cg, p.p_mn, p.q_mn);
     p.idesc_add = idesc_of(c.type, pl.bn, pl.cg, swapped ? 1 : 0, swapped ? 0 : 1);
     p.C = c.C;
     p.ldc = c.ldc;
@@ -1320,8 +1344,8 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     std::memset(&m, 0, sizeof m);
     int rc = GEMM_OK;
     if (c.mode == kModeGradient || p.num_kb > 0) {
-        if (c.mode != kModeLow) rc = encode_operand(&m.p, c.p, c.type, c.K, kLanes);
-        if (rc == GEMM_OK) rc = encode_operand(&m.q, c.q, c.type, c.K, pl.bn / pl.cg);
+        if (c.mode != kModeLow) rc = encode_operand(&m.p, c.p, c.type, c.K, pl.p_rows);
+        if (rc == GEMM_OK) rc = encode_operand(&m.q, c.q, c.type, c.K, p.width / pl.cg);
     }
     const int64_t low_cols = (int64_t)ad.max_slots * ad.pitch;
     if (rc == GEMM_OK && c.mode == kModeLow && p.num_kb > 0)

@@ -59,6 +59,8 @@ enum ProductEpilogue : int { kEpiSwapped = 0, kEpiRows = 1, kEpiStats = 2, kEpiD
 // memory (row-wise).
 struct ProductPlan {
     int bn = 0, cg = 1, splits = 1, parts = 1;
+    int p_rows = 128;          // rows of P a CTA loads: 128, or (statistics of few tokens) 32
+    int width = 0;             // statistics: columns a tile covers, up to bn (0: bn)
 };
 
 struct ProductCall {
@@ -93,8 +95,11 @@ ProductPlan product_plan_tokens(int64_t tokens, int64_t cols, int64_t K, int sms
 ProductPlan product_plan_low(int64_t tokens, int64_t lanes, int64_t K, int sms);
 ProductPlan product_plan_gradient(int64_t pitch, int64_t adapters, int64_t cols, int64_t tokens, int sms);
 
-// Columns of D that one part of the loss statistics covers.
-int product_part_columns(const ProductPlan &plan);
+// The same for the loss statistics; `any`: tiles may be of any width (W K-major).
+ProductPlan product_plan_stats(int64_t tokens, int64_t vocab, int64_t K, bool any, int sms);
+
+// Parts of the loss statistics that `cols` columns give.
+int64_t product_parts(const ProductPlan &plan, int64_t cols);
 
 inline int64_t op_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t op_round_up(int64_t a, int64_t b) { return op_cdiv(a, b) * b; }
