@@ -113,7 +113,8 @@ typedef struct {
  *
  * and without the middle term for a token that takes none.  The rank-wide
  * X[t] . A_i^T is scaled and rounded to `dtype` once; everything else is FP32 up to
- * the one rounding of C.
+ * the one rounding of C.  The workspace is T x min(256, count) x the rank rounded up
+ * to 16, 32, 64 or 128, in 16 bits.
  *
  *   X            T x K, pitch ldx >= K
  *   W            w_major 0: K rows of N values, pitch ldw >= N; 1: N rows of K,

@@ -657,3 +657,25 @@ def test_the_example_runs_them_together():
     # Two roundings to BF16 in a row on each way (half steps of 2^-8, 1.7e-3 rms each), three products deep, and
     # the loss's own d: under 1% of each gradient.
     assert all(v < 0.01 for v in found.values()), found
+
+
+def test_loss_past_32_bits():
+    # W and dW pass 2^31 elements; labels at both ends
+    T, V, D = 3, 530000, 4104
+    W = torch.empty((V, D), dtype=BF16, device="cuda")
+    for v in range(0, V, 50000):
+        W[v:v + 50000] = randn(min(50000, V - v), D, seed=v) * D ** -0.5
+    H, y = randn(T, D, seed=1).to(BF16), torch.tensor([V - 1, 0, V // 2], device="cuda")
+    loss, lse = tg.project_loss(H, W, y)
+    z = torch.cat([H.double() @ W[v:v + 50000].double().t() for v in range(0, V, 50000)], 1)
+    want = torch.logsumexp(z, 1)
+    # (the bounds above with D = max sum |h w| under 60)
+    assert float((lse - want).abs().max()) < 6e-4 + 1e-5
+    assert float((loss - (want - z.gather(1, y[:, None])[:, 0])).abs().max()) < 1.3e-3
+    _, dW = tg.project_loss_backward(torch.ones(T, device="cuda"), H, W, y, lse, want_H=False)
+    at = torch.tensor([0, 1, 523264, 523265, V // 2, V - 2, V - 1], device="cuda")
+    d = torch.exp(z - want[:, None])
+    d[torch.arange(T, device="cuda"), y] -= 1
+    exact = d[:, at].t() @ H.double()
+    bound = (U[BF16] * 2 + 1.5e-3) * (d[:, at].abs().t() @ H.double().abs()) + U[BF16] * exact.abs()
+    within(dW[at], exact, bound, "dW")
