@@ -90,6 +90,9 @@ struct ProductParams {
     float2 *parts;
     float *sums, *hits;
     const float4 *rows;
+    float *rests_out;
+    ProductRests rests;
+    int f16;                   // the operands' type
     int early, debug_stall;
     unsigned long long timeout_ns;
 };
@@ -496,6 +499,103 @@ __device__ __forceinline__ void tanh_64(float (&v)[N]) {
     }
 }
 
+// The label of token i as a column of this call's D (far outside it if it has none here).
+__device__ __forceinline__ int64_t label_column(const ProductParams &p, int64_t i) {
+    const int64_t y = p.label_bytes == 8 ? __ldg(static_cast<const long long *>(p.labels) + i)
+                                         : (int64_t)__ldg(static_cast<const int32_t *>(p.labels) + i);
+    return y < 0 ? -(1LL << 40) : y - p.first;
+}
+
+// v += f * eight neighbouring 16-bit values (on 16 bytes).
+__device__ __forceinline__ void add_eight(const ProductParams &p, const uint4 &w, float f, float *v) {
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float lo, hi;
+        epi_unpack2(p.f16 ? GEMM_OUT_F16 : GEMM_OUT_BF16, q[k], lo, hi);
+        v[2 * k] = fmaf(f, lo, v[2 * k]);
+        v[2 * k + 1] = fmaf(f, hi, v[2 * k + 1]);
+    }
+}
+
+// The first of p.rests.count ascending labels that is not below y.
+__device__ __forceinline__ int first_label(const ProductParams &p, int64_t y) {
+    int lo = 0, hi = (int)p.rests.count;
+    while (lo < hi) {
+        const int mid = (int)(((unsigned)lo + (unsigned)hi) >> 1);
+        if (__ldg(p.rests.labels + mid) < y) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// What rounding took from the label entries of d (ProductRests), on 64 columns from j
+// on of row i.
+__device__ __forceinline__ void add_rests(const ProductParams &p, const Tile &T, int64_t i, int64_t j, int lane, float (&v)[64]) {
+    const ProductRests &r = p.rests;
+    const uint16_t *m = static_cast<const uint16_t *>(r.m);
+    const int have = (int)(T.j1 - j < 64 ? T.j1 - j : 64);
+    // eight columns at a time of a row on 16 bytes; what is left of it one by one
+    auto add_row = [&](const uint16_t *at, float f) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 8) {
+            if (c + 8 <= have) {
+                add_eight(p, __ldg(reinterpret_cast<const uint4 *>(at + c)), f, v + c);
+            } else if (c < have) {
+#pragma unroll
+                for (int k = 0; k < 7; ++k) {
+                    float lo = 0.f, hi;
+                    if (c + k < have) epi_unpack2(p.f16 ? GEMM_OUT_F16 : GEMM_OUT_BF16, __ldg(at + c + k), lo, hi);
+                    v[c + k] = fmaf(f, lo, v[c + k]);
+                }
+            }
+        }
+    };
+    if (r.kind == 1) {
+        const int64_t y = i < T.i1 ? label_column(p, i) : -1;
+        if (y < 0 || y >= r.cols) return;
+        const float f = __ldg(r.rests + i);
+        if (r.m_major == 0) {
+            add_row(m + y * r.ld + j, f);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+                float lo = 0.f, hi;
+                if (c < have) epi_unpack2(p.f16 ? GEMM_OUT_F16 : GEMM_OUT_BF16, __ldg(m + (j + c) * r.ld + y), lo, hi);
+                v[c] = fmaf(f, lo, v[c]);
+            }
+        }
+    } else if (r.kind == 2) {
+        if (i >= T.i1) return;
+        const int64_t y = p.first + i;
+        for (int k = first_label(p, y); k < r.count && __ldg(r.labels + k) == y; ++k) {
+            const int t = __ldg(r.tokens + k);
+            add_row(m + (int64_t)t * r.ld + j, __ldg(r.rests + t));
+        }
+    } else {
+        // (columns j + lane and j + 32 + lane; each column's tokens are the same for all rows)
+        int from[2], count[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t y = p.first + j + 32 * h + lane;
+            from[h] = 32 * h + lane < have ? first_label(p, y) : 0;
+            count[h] = 32 * h + lane < have ? first_label(p, y + 1) - from[h] : 0;
+        }
+        if (!__any_sync(0xffffffffu, count[0] + count[1] > 0)) return;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+            const int k0 = __shfl_sync(0xffffffffu, from[c >> 5], c & 31), n = __shfl_sync(0xffffffffu, count[c >> 5], c & 31);
+#pragma unroll 1
+            for (int k = k0; k < k0 + n; ++k) {
+                const int t = __ldg(r.tokens + k);
+                float lo = 0.f, hi;
+                if (i < T.i1) epi_unpack2(p.f16 ? GEMM_OUT_F16 : GEMM_OUT_BF16, __ldg(m + (int64_t)t * r.ld + i), lo, hi);
+                v[c] = fmaf(__ldg(r.rests + t), lo, v[c]);
+            }
+        }
+    }
+}
+
 // Running maximum (in base 2) and sum of a row's exponentials.
 struct Softmax {
     float top = -INFINITY, sum = 0.f, plain = 0.f;
@@ -548,13 +648,6 @@ __device__ __forceinline__ void take_logits(const ProductParams &p, float (&v)[N
     }
     s.sum = fmaf(s.sum, ptx::exp2_approx(s.top - base), a + b);
     s.top = top;
-}
-
-// The label of token i as a column of this call's D (far outside it if it has none here).
-__device__ __forceinline__ int64_t label_column(const ProductParams &p, int64_t i) {
-    const int64_t y = p.label_bytes == 8 ? __ldg(static_cast<const long long *>(p.labels) + i)
-                                         : (int64_t)__ldg(static_cast<const int32_t *>(p.labels) + i);
-    return y < 0 ? -(1LL << 40) : y - p.first;
 }
 
 // 64 logits to their gradient times the row's factors (loss.cu: rows).
@@ -758,7 +851,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 }
                 __syncwarp();
             }
-            if constexpr (EPI == kEpiSwapped || EPI == kEpiRows) {
+            if constexpr (EPI == kEpiSwapped || EPI == kEpiRows) {   // (the others have no adapters)
                 if (!ok || p.mode != kModeAdd || T.kb1 <= p.num_kb) continue;
                 if (!waited) ptx::pdl_wait();
                 waited = true;
@@ -1037,7 +1130,16 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
 #pragma unroll
                             for (int c = 0; c < 64; ++c) v[c] = 0.f;
                         }
+                        if (rel >= 0 && rel < 64) {
+                            float d = 0.f;
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) d = c == (int)rel ? v[c] : d;
+                            p.rests_out[i] = d - (p.f16 ? __half2float(__float2half_rn(d)) : __bfloat162float(__float2bfloat16_rn(d)));
+                        }
                     } else {
+                        if constexpr (EPI == kEpiRests) {
+                            if (T.down == 0) add_rests(p, T, i, j, (int)lane, v);
+                        }
                         finish_row(p, T, i, j, alpha, v);
                     }
                     store_64(p, &tmC, T, i0, j, v, out_buf, (int)lane);
@@ -1183,6 +1285,8 @@ int launch_plan(const ProductPlan &pl, int epilogue, const Maps &m, const Produc
         return pair ? launch<256, 2, kEpiStats>(m, p, grid, stream) : launch<128, 1, kEpiStats>(m, p, grid, stream);
     if (epilogue == kEpiDlogits)
         return pair ? launch<256, 2, kEpiDlogits>(m, p, grid, stream) : launch<128, 1, kEpiDlogits>(m, p, grid, stream);
+    if (epilogue == kEpiRests)
+        return pair ? launch<256, 2, kEpiRests>(m, p, grid, stream) : launch<128, 1, kEpiRests>(m, p, grid, stream);
     return pair ? launch<256, 2, kEpiRows>(m, p, grid, stream) : launch<128, 1, kEpiRows>(m, p, grid, stream);
 }
 
@@ -1333,6 +1437,9 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     p.sums = c.loss.sums;
     p.hits = c.loss.hits;
     p.rows = c.loss.rows;
+    p.rests_out = c.loss.rests;
+    p.rests = c.rests;
+    p.f16 = c.type == GEMM_OUT_F16;
     p.eps_v = c.loss.eps_v;
     p.one_eps = c.loss.one_eps;
     p.early = c.early ? 1 : 0;

@@ -45,6 +45,22 @@ struct ProductLoss {
     float *sums = nullptr;     // [part][token]
     float *hits = nullptr;     // [token]: the label's logit
     const float4 *rows = nullptr;   // [token]: lse in base 2, three coefficients (loss.cu)
+    float *rests = nullptr;         // [token]: what rounding took from the label's gradient
+};
+
+// The label entries of d are by far its largest, so their rounding would be nearly all
+// of the gradients' error.  What it took (`rests`) is added back in FP32 where the
+// products that read d are written: to dH the token's rest times its label's row of W,
+// to dW the rests of the tokens that have the label times their rows of H.
+struct ProductRests {
+    int kind = 0;                   // 1: lanes are tokens; 2: lanes, 3: columns are the vocabulary
+    const float *rests = nullptr;
+    const void *m = nullptr;        // kind 1: the piece of W; else H
+    int64_t ld = 0;
+    int m_major = 0;                // kind 1: as w_major
+    int64_t cols = 0;               // kind 1: entries of the piece
+    const int32_t *labels = nullptr, *tokens = nullptr;     // kinds 2, 3: ascending labels, whose they are
+    int64_t count = 0;
 };
 
 enum ProductMode : int {
@@ -53,7 +69,8 @@ enum ProductMode : int {
     kModeLow = 2,              // low = tokens x adapters^T, masked (swapped)
     kModeGradient = 3          // one product per adapter over the tokens that take it (swapped)
 };
-enum ProductEpilogue : int { kEpiSwapped = 0, kEpiRows = 1, kEpiStats = 2, kEpiDlogits = 3 };
+enum ProductEpilogue : int { kEpiSwapped = 0, kEpiRows = 1, kEpiStats = 2, kEpiDlogits = 3,
+                            kEpiRests = 4 /* kEpiRows with ProductRests */ };
 
 // Columns of the tile, CTAs of it, its K ranges within a cluster (swapped) or through
 // memory (row-wise).
@@ -71,6 +88,7 @@ struct ProductCall {
     ProductPlan plan;
     ProductAdapters ad;
     ProductLoss loss;
+    ProductRests rests;
     void *C = nullptr;                     // swapped: C's columns are the lanes
     int64_t ldc = 0;
     int64_t c_stride = 0;                  // kModeGradient: between adapters' results
