@@ -21,6 +21,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kFinishWarps = 16;
+constexpr int kPlaces = 4;
 
 __device__ __forceinline__ bool counted(const void *labels, int label_bytes, int64_t t, int64_t V) {
     const int64_t y = label_bytes == 8 ? __ldg(static_cast<const long long *>(labels) + t)
@@ -117,54 +118,108 @@ loss_scale(int64_t T, int64_t V, const float *__restrict__ grad, int64_t grad_st
 // labels (ties in the order of the tokens, tokens that do not count last), by counting
 // the labels before its own; and H's row, at a pitch TMA can address, zero for a token
 // that does not count, so that nothing it holds (padding may be anything) reaches dW as
-// 0 x NaN.  A warp takes EACH tokens, so that a label read is compared with as many.
+// 0 x NaN.  With W (held D x V): its label's column of it, as a row.  A block takes EACH
+// tokens, so that a label read is compared with as many.
 template <int ACCESS, int EACH, typename E>
 __global__ void __launch_bounds__(256)
 loss_rows(int T, int64_t V, int D, const E *__restrict__ H, int64_t ldh, E *__restrict__ out, int64_t ldo,
           const float *__restrict__ grad, int64_t grad_stride, const float *__restrict__ lse, const void *labels,
-          int label_bytes, float z_loss, const float *scale, float4 *rows, int32_t *sorted, int32_t *tokens) {
+          int label_bytes, float z_loss, const float *scale, float4 *rows, int32_t *sorted, int32_t *tokens, int32_t *index,
+          const E *__restrict__ W, int64_t ldw, E *__restrict__ mine_of_w) {
     pdl_enter();
-    const int per = (D + 7) / 8, lane = threadIdx.x & 31;
+    __shared__ uint32_t count[EACH];
+    const int per = (D + 7) / 8;
     const float f = scale ? __ldg(scale) : 1.f;
     auto key = [&](int t) -> int {
         const int64_t y = label_bytes == 8 ? __ldg(static_cast<const long long *>(labels) + t)
                                            : (int64_t)__ldg(static_cast<const int32_t *>(labels) + t);
         return y >= 0 && y < V ? (int)y : (int)V;
     };
-    for (int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * EACH; t0 < T; t0 += (int64_t)gridDim.x * 8 * EACH) {
-        int mine[EACH], before[EACH];
+    for (int64_t t0 = (int64_t)blockIdx.x * EACH; t0 < T; t0 += (int64_t)gridDim.x * EACH) {
+        int mine[EACH];
 #pragma unroll
-        for (int k = 0; k < EACH; ++k) {
-            mine[k] = t0 + k < T ? key((int)t0 + k) : -1;
-            before[k] = 0;
-        }
+        for (int k = 0; k < EACH; ++k) mine[k] = t0 + k < T ? key((int)t0 + k) : -1;
         if (sorted) {
+            // (at most 65536 tokens: the labels before, and the same ones before, in 16 bits each)
+            uint32_t before[EACH];
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) before[k] = 0u;
+            __syncthreads();
+            if (threadIdx.x < EACH) count[threadIdx.x] = 0u;
+            __syncthreads();
 #pragma unroll 4
-            for (int s = lane; s < T; s += 32) {
+            for (int s = threadIdx.x; s < T; s += 256) {
                 const int y = key(s);
 #pragma unroll
-                for (int k = 0; k < EACH; ++k) before[k] += y < mine[k] || (y == mine[k] && s < (int)t0 + k) ? 1 : 0;
+                for (int k = 0; k < EACH; ++k)
+                    before[k] += y < mine[k] ? 1u : y == mine[k] && s < (int)t0 + k ? 0x10001u : 0u;
             }
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) {
+                const uint32_t n = __reduce_add_sync(0xffffffffu, before[k]);
+                if ((threadIdx.x & 31) == 0) atomicAdd(&count[k], n);
+            }
+            __syncthreads();
         }
 #pragma unroll
         for (int k = 0; k < EACH; ++k) {
             const int64_t t = t0 + k;
             if (t >= T) break;
             const bool has = mine[k] < (int)V;
-            if (sorted) {
-                const int place = __reduce_add_sync(0xffffffffu, before[k]);
-                if (lane == 0) {
+            const int place = sorted ? (int)(count[k] & 0xffffu) : 0;
+            if (threadIdx.x == 0) {
+                if (sorted) {
                     sorted[place] = mine[k];
                     tokens[place] = (int)t;
+                    if (has && count[k] >> 16 == 0) index[mine[k]] = place;
                 }
-            }
-            if (lane == 0) {
                 const float l = __ldg(lse + t), g = f * __ldg(grad + t * grad_stride);
-                rows[t] = has ? make_float4(l * kLog2e, g * fmaf(2.f * z_loss, l, 1.f), g, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+                rows[t] = has ? make_float4(l * kLog2e, g * fmaf(2.f * z_loss, l, 1.f), g, __int_as_float(place + 1))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            for (int c = lane; c < per; c += 32)
+            if (W && has)
+                for (int c = threadIdx.x; c < D; c += 256) mine_of_w[t * ldo + c] = W[c * ldw + mine[k]];
+            for (int c = threadIdx.x; c < per; c += 256)
                 op_store8<true>(out + t * ldo + 8 * c, op_load8<ACCESS>(H + t * ldh + 8 * c, has ? min(8, D - 8 * c) : 0), 8);
         }
+    }
+}
+
+// For each label in [first, first + cols) that a token has: the sum of the rests times
+// the rows of H over its tokens, in their order, in the row of its first place.  Two
+// columns a thread, so that a frequent label's tokens are as many blocks' work; kPlaces
+// places a block, for most are another piece's.
+template <typename E>
+__global__ void __launch_bounds__(128)
+loss_rests(int T, int64_t first, int64_t cols, int D, const int32_t *__restrict__ sorted, const int32_t *__restrict__ tokens,
+           const float *__restrict__ rests, const E *__restrict__ H, int64_t ldh, float *__restrict__ sums) {
+    pdl_enter();
+    const int c = (blockIdx.y * 128 + threadIdx.x) * 2;
+    if (c >= D) return;
+    const E *column = H + c;                     // (rows are padded to eight, with zeros)
+    for (int k0 = blockIdx.x * kPlaces; k0 < min(T, ((int)blockIdx.x + 1) * kPlaces); ++k0) {
+        const int y = __ldg(sorted + k0);
+        if (y < first || y >= first + cols || (k0 > 0 && __ldg(sorted + k0 - 1) == y)) continue;
+        float a = 0.f, b = 0.f;
+        bool more = true;
+        for (int k = k0; more; k += 8) {
+            uint32_t w[8];
+            float f[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                // (in order: the first that is not the label's ends it)
+                more = k + q < T && __ldg(sorted + (k + q < T ? k + q : k0)) == y;
+                f[q] = more ? __ldg(rests + k + q) : 0.f;
+                w[q] = more ? __ldg(reinterpret_cast<const uint32_t *>(column + __ldg(tokens + k + q) * ldh)) : 0u;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const E *pair = reinterpret_cast<const E *>(&w[q]);
+                a = fmaf(f[q], OpType<E>::up(pair[0]), a);
+                b = fmaf(f[q], OpType<E>::up(pair[1]), b);
+            }
+        }
+        *reinterpret_cast<float2 *>(sums + k0 * ldh + c) = make_float2(a, b);
     }
 }
 
@@ -431,19 +486,24 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
     const int64_t part_rows = op_round_up(T, 256);
     const bool join = h_plan.parts > 1;
     Workspace ws;
-    const uint64_t at_rests = ws.add((uint64_t)T * 4), at_sorted = ws.add((uint64_t)T * 4), at_tokens = ws.add((uint64_t)T * 4);
+    // Ordering the labels takes T^2 comparisons: 0.02 ms for 8192 tokens, 1 for 65536.
+    // Beyond, dW is without the rests (dH is not).
+    const bool order = dW && T <= 65536;
+    const uint64_t at_index = ws.add(order ? (uint64_t)V * 4 : 0), at_sums = ws.add(order ? (uint64_t)T * h_pitch * 4 : 0);
+    const uint64_t at_rests = ws.add((uint64_t)T * 4), at_ordered = ws.add((uint64_t)T * 4),
+                   at_label_w = ws.add(dH && w_major ? (uint64_t)T * h_pitch * 2 : 0), at_sorted = ws.add((uint64_t)T * 4), at_tokens = ws.add((uint64_t)T * 4);
     const uint64_t at_rows = ws.add((uint64_t)T * 16), at_scale = ws.add(8), at_h = ws.add((uint64_t)T * h_pitch * 2),
                    at_d = ws.add((uint64_t)T * d_pitch * 2), at_w = ws.add((uint64_t)packed_w_bytes(a, piece)),
                    at_acc = ws.add(!dH ? 0 : join ? (uint64_t)h_plan.parts * part_rows * acc_pitch * 4 : pieces > 1 ? (uint64_t)T * acc_pitch * 4 : 0);
     if ((rc = ws.make(stream))) return rc;
     float4 *rows = reinterpret_cast<float4 *>(ws.base + at_rows);
-    // Ordering the labels takes T^2 comparisons: 0.02 ms for 8192 tokens, 1 for 65536.
-    // Beyond, dW is without the rests (as dH is not).
-    const bool order = dW && T <= 65536;
+    int32_t *index = reinterpret_cast<int32_t *>(ws.base + at_index);
+    float *sums = reinterpret_cast<float *>(ws.base + at_sums);
+    if (order) rc = op_launched("cudaMemsetAsync", cudaMemsetAsync(index, 0xff, (size_t)V * 4, stream));
     int32_t *sorted = order ? reinterpret_cast<int32_t *>(ws.base + at_sorted) : nullptr, *tokens = reinterpret_cast<int32_t *>(ws.base + at_tokens);
-    float *rests = reinterpret_cast<float *>(ws.base + at_rests);
+    float *rests = reinterpret_cast<float *>(ws.base + at_rests), *ordered = reinterpret_cast<float *>(ws.base + at_ordered);
     float *scale = reinterpret_cast<float *>(ws.base + at_scale), *acc = reinterpret_cast<float *>(ws.base + at_acc);
-    if (f16)
+    if (f16 && rc == GEMM_OK)
         rc = op_launched("loss scale", launch_pdl(loss_scale, dim3(1), dim3(1024), 0, stream, T, V, grad, grad_stride, lse, labels,
                                                   label_bytes, a.how.z_loss, scale));
     const bool wide = op_wide(H, a.ldh, 2) && D % 8 == 0;
@@ -455,15 +515,17 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
                 constexpr int kEach = decltype(each)::value;
                 return op_launched("loss rows",
                                    launch_pdl(loss_rows<decltype(acc_kind)::value, kEach, E>,
-                                              dim3((unsigned)std::min<int64_t>(op_cdiv(T, 8 * kEach), sms * 8)), dim3(256), 0, stream,
+                                              dim3((unsigned)std::min<int64_t>(op_cdiv(T, kEach), 0x7fffffff)), dim3(256), 0, stream,
                                               (int)T, V, (int)D, static_cast<const E *>(H), a.ldh,
                                               reinterpret_cast<E *>(ws.base + at_h), h_pitch, grad, grad_stride, lse, labels,
-                                              label_bytes, a.how.z_loss, (const float *)(f16 ? scale : nullptr), rows, sorted, tokens));
+                                              label_bytes, a.how.z_loss, (const float *)(f16 ? scale : nullptr), rows, sorted, tokens, index,
+                                              static_cast<const E *>(dH && w_major ? W : nullptr), a.ldw,
+                                              reinterpret_cast<E *>(ws.base + at_label_w)));
             };
             using One = std::integral_constant<int, 1>;
-            using Four = std::integral_constant<int, 4>;
-            if (f16) return T <= 2048 ? go(__half(), One()) : go(__half(), Four());
-            return T <= 2048 ? go(__nv_bfloat16(), One()) : go(__nv_bfloat16(), Four());
+            using Eight = std::integral_constant<int, 8>;
+            if (f16) return T <= 2048 ? go(__half(), One()) : go(__half(), Eight());
+            return T <= 2048 ? go(__nv_bfloat16(), One()) : go(__nv_bfloat16(), Eight());
         });
     const ProductOperand h_rows = {ws.base + at_h, T, h_pitch, 0}, h_cols = {ws.base + at_h, D, h_pitch, 1};
     int64_t n = 0;
@@ -489,6 +551,7 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
         d.loss.first = v;
         d.loss.rows = rows;
         d.loss.rests = rests;
+        d.loss.rests_ordered = order ? ordered : nullptr;
         if ((rc = product_launch(d, sms, stream))) break;
         if (dH) {
             ProductCall c;
@@ -497,9 +560,9 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
             c.loss.first = v;
             c.rests.kind = 1;
             c.rests.rests = rests;
-            c.rests.m = w.p;
-            c.rests.ld = w.ld;
-            c.rests.m_major = w_major;
+            c.rests.w = w_major ? ws.base + at_label_w : w.p;
+            c.rests.ld = w_major ? h_pitch : w.ld;
+            c.rests.by_token = w_major;
             c.rests.cols = cols;
             c.type = et;
             c.I = T;
@@ -523,15 +586,22 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
         if (dW) {
             const ProductOperand d_cols = {ws.base + at_d, cols, d_pitch, 1};
             ProductCall c;
+            if (order) {
+                auto go = [&](auto e) {
+                    using E = decltype(e);
+                    return op_launched("loss rests",
+                                       launch_pdl(loss_rests<E>, dim3((unsigned)op_cdiv(T, kPlaces), (unsigned)op_cdiv(D, 256)), dim3(128), 0, stream, (int)T, v, cols, (int)D,
+                                                  (const int32_t *)sorted, (const int32_t *)tokens, (const float *)ordered,
+                                                  reinterpret_cast<const E *>(ws.base + at_h), h_pitch, sums));
+                };
+                if ((rc = f16 ? go(__half()) : go(__nv_bfloat16()))) break;
+            }
             c.epilogue = order ? kEpiRests : kEpiRows;
             c.loss.first = v;
             c.rests.kind = w_major ? 3 : 2;
-            c.rests.rests = rests;
-            c.rests.m = ws.base + at_h;
+            c.rests.index = index;
+            c.rests.sums = sums;
             c.rests.ld = h_pitch;
-            c.rests.labels = sorted;
-            c.rests.tokens = tokens;
-            c.rests.count = T;
             c.type = et;
             c.I = w_major ? D : cols;
             c.J = w_major ? cols : D;

@@ -90,7 +90,7 @@ struct ProductParams {
     float2 *parts;
     float *sums, *hits;
     const float4 *rows;
-    float *rests_out;
+    float *rests_out, *rests_ordered;
     ProductRests rests;
     int f16;                   // the operands' type
     int early, debug_stall;
@@ -518,25 +518,17 @@ __device__ __forceinline__ void add_eight(const ProductParams &p, const uint4 &w
     }
 }
 
-// The first of p.rests.count ascending labels that is not below y.
-__device__ __forceinline__ int first_label(const ProductParams &p, int64_t y) {
-    int lo = 0, hi = (int)p.rests.count;
-    while (lo < hi) {
-        const int mid = (int)(((unsigned)lo + (unsigned)hi) >> 1);
-        if (__ldg(p.rests.labels + mid) < y) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // What rounding took from the label entries of d (ProductRests), on 64 columns from j
 // on of row i.
 __device__ __forceinline__ void add_rests(const ProductParams &p, const Tile &T, int64_t i, int64_t j, int lane, float (&v)[64]) {
     const ProductRests &r = p.rests;
-    const uint16_t *m = static_cast<const uint16_t *>(r.m);
-    const int have = (int)(T.j1 - j < 64 ? T.j1 - j : 64);
-    // eight columns at a time of a row on 16 bytes; what is left of it one by one
-    auto add_row = [&](const uint16_t *at, float f) {
+    const int have = (int)(T.j1 - j < 64 ? T.j1 - j : 64), type = p.f16 ? GEMM_OUT_F16 : GEMM_OUT_BF16;
+    if (r.kind == 1) {
+        const int64_t y = i < T.i1 ? label_column(p, i) : -1;
+        if (y < 0 || y >= r.cols) return;
+        const float f = __ldg(r.rests + i);
+        const uint16_t *at = static_cast<const uint16_t *>(r.w) + (r.by_token ? i : y) * r.ld + j;
+        // eight columns at a time (rows start on 16 bytes); what is left one by one
 #pragma unroll
         for (int c = 0; c < 64; c += 8) {
             if (c + 8 <= have) {
@@ -545,53 +537,41 @@ __device__ __forceinline__ void add_rests(const ProductParams &p, const Tile &T,
 #pragma unroll
                 for (int k = 0; k < 7; ++k) {
                     float lo = 0.f, hi;
-                    if (c + k < have) epi_unpack2(p.f16 ? GEMM_OUT_F16 : GEMM_OUT_BF16, __ldg(at + c + k), lo, hi);
+                    if (c + k < have) epi_unpack2(type, __ldg(at + c + k), lo, hi);
                     v[c + k] = fmaf(f, lo, v[c + k]);
                 }
             }
         }
-    };
-    if (r.kind == 1) {
-        const int64_t y = i < T.i1 ? label_column(p, i) : -1;
-        if (y < 0 || y >= r.cols) return;
-        const float f = __ldg(r.rests + i);
-        if (r.m_major == 0) {
-            add_row(m + y * r.ld + j, f);
-        } else {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                float lo = 0.f, hi;
-                if (c < have) epi_unpack2(p.f16 ? GEMM_OUT_F16 : GEMM_OUT_BF16, __ldg(m + (j + c) * r.ld + y), lo, hi);
-                v[c] = fmaf(f, lo, v[c]);
-            }
-        }
     } else if (r.kind == 2) {
-        if (i >= T.i1) return;
-        const int64_t y = p.first + i;
-        for (int k = first_label(p, y); k < r.count && __ldg(r.labels + k) == y; ++k) {
-            const int t = __ldg(r.tokens + k);
-            add_row(m + (int64_t)t * r.ld + j, __ldg(r.rests + t));
+        const int k = i < T.i1 ? __ldg(r.index + p.first + i) : -1;
+        if (k < 0) return;
+        const float *at = r.sums + k * r.ld + j;             // (on 16 bytes, with room for the row's last four)
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+            if (c >= have) break;
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(at + c));
+            v[c] += x.x;
+            v[c + 1] += x.y;
+            v[c + 2] += x.z;
+            v[c + 3] += x.w;
         }
     } else {
-        // (columns j + lane and j + 32 + lane; each column's tokens are the same for all rows)
-        int from[2], count[2];
+        int k[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) k[h] = 32 * h + lane < have ? __ldg(r.index + p.first + j + 32 * h + lane) : -1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t y = p.first + j + 32 * h + lane;
-            from[h] = 32 * h + lane < have ? first_label(p, y) : 0;
-            count[h] = 32 * h + lane < have ? first_label(p, y + 1) - from[h] : 0;
-        }
-        if (!__any_sync(0xffffffffu, count[0] + count[1] > 0)) return;
+            if (!__any_sync(0xffffffffu, k[h] >= 0)) continue;
+            // (all loads before the first sum: one after the other the 60 labels among the
+            // first 64 entries cost a tile 40 us)
+            float x[32];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-            const int k0 = __shfl_sync(0xffffffffu, from[c >> 5], c & 31), n = __shfl_sync(0xffffffffu, count[c >> 5], c & 31);
-#pragma unroll 1
-            for (int k = k0; k < k0 + n; ++k) {
-                const int t = __ldg(r.tokens + k);
-                float lo = 0.f, hi;
-                if (i < T.i1) epi_unpack2(p.f16 ? GEMM_OUT_F16 : GEMM_OUT_BF16, __ldg(m + (int64_t)t * r.ld + i), lo, hi);
-                v[c] = fmaf(__ldg(r.rests + t), lo, v[c]);
+            for (int c = 0; c < 32; ++c) {
+                const int64_t row = __shfl_sync(0xffffffffu, k[h], c);
+                x[c] = row >= 0 && i < T.i1 ? __ldg(r.sums + row * r.ld + i) : 0.f;
             }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[32 * h + c] += x[c];
         }
     }
 }
@@ -1107,7 +1087,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 if constexpr (EPI == kEpiDlogits) {
                     if (steps && i < T.i1) {
                         info = __ldg(p.rows + i);
-                        if (info.w != 0.f) label = label_column(p, i);
+                        if (__float_as_int(info.w) != 0) label = label_column(p, i);
                     }
                 }
 #pragma unroll 1
@@ -1124,9 +1104,9 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                     if constexpr (EPI == kEpiDlogits) {
                         const int64_t rel = label - j;
                         // (a row without a label gives nothing, whatever its logits are)
-                        if (__any_sync(0xffffffffu, info.w != 0.f))
+                        if (__any_sync(0xffffffffu, __float_as_int(info.w) != 0))
                             take_gradient(p, v, info, rel >= 0 && rel < 64 ? (int)rel : -1);
-                        if (info.w == 0.f) {
+                        if (__float_as_int(info.w) == 0) {
 #pragma unroll
                             for (int c = 0; c < 64; ++c) v[c] = 0.f;
                         }
@@ -1134,7 +1114,9 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                             float d = 0.f;
 #pragma unroll
                             for (int c = 0; c < 64; ++c) d = c == (int)rel ? v[c] : d;
-                            p.rests_out[i] = d - (p.f16 ? __half2float(__float2half_rn(d)) : __bfloat162float(__float2bfloat16_rn(d)));
+                            d -= p.f16 ? __half2float(__float2half_rn(d)) : __bfloat162float(__float2bfloat16_rn(d));
+                            p.rests_out[i] = d;
+                            if (p.rests_ordered) p.rests_ordered[__float_as_int(info.w) - 1] = d;
                         }
                     } else {
                         if constexpr (EPI == kEpiRests) {
@@ -1438,6 +1420,7 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     p.hits = c.loss.hits;
     p.rows = c.loss.rows;
     p.rests_out = c.loss.rests;
+    p.rests_ordered = c.loss.rests_ordered;
     p.rests = c.rests;
     p.f16 = c.type == GEMM_OUT_F16;
     p.eps_v = c.loss.eps_v;

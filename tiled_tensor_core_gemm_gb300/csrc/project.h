@@ -44,23 +44,28 @@ struct ProductLoss {
     float2 *parts = nullptr;   // [part][token]: maximum (in base 2) and sum of the exponentials
     float *sums = nullptr;     // [part][token]
     float *hits = nullptr;     // [token]: the label's logit
-    const float4 *rows = nullptr;   // [token]: lse in base 2, three coefficients (loss.cu)
+    const float4 *rows = nullptr;   // [token]: lse in base 2, two factors (loss.cu), and as bits 0 for one
+                                    // that does not count, else its place in the order of the labels + 1
     float *rests = nullptr;         // [token]: what rounding took from the label's gradient
+    float *rests_ordered = nullptr; // the same by place, or nullptr
 };
 
 // The label entries of d are by far its largest, so their rounding would be nearly all
 // of the gradients' error.  What it took (`rests`) is added back in FP32 where the
 // products that read d are written: to dH the token's rest times its label's row of W,
-// to dW the rests of the tokens that have the label times their rows of H.
+// to dW the sum over the tokens that have the label of their rests times their rows of
+// H (loss.cu: loss_rests).
 struct ProductRests {
     int kind = 0;                   // 1: lanes are tokens; 2: lanes, 3: columns are the vocabulary
-    const float *rests = nullptr;
-    const void *m = nullptr;        // kind 1: the piece of W; else H
     int64_t ld = 0;
-    int m_major = 0;                // kind 1: as w_major
-    int64_t cols = 0;               // kind 1: entries of the piece
-    const int32_t *labels = nullptr, *tokens = nullptr;     // kinds 2, 3: ascending labels, whose they are
-    int64_t count = 0;
+    // kind 1: by token, and rows of W by label or by token (of the piece, `cols` entries)
+    const float *rests = nullptr;
+    const void *w = nullptr;
+    int by_token = 0;
+    int64_t cols = 0;
+    // kinds 2, 3: the row of `sums` of each entry of the vocabulary, -1 without a token
+    const int32_t *index = nullptr;
+    const float *sums = nullptr;
 };
 
 enum ProductMode : int {
