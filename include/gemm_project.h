@@ -112,9 +112,10 @@ typedef struct {
  *     C[t] = act(X[t] . W + scales[i] (X[t] . A_i^T) . B_i + bias)
  *
  * and without the middle term for a token that takes none.  The rank-wide
- * X[t] . A_i^T is scaled and rounded to `dtype` once; everything else is FP32 up to
- * the one rounding of C.  The workspace is T x min(256, count) x the rank rounded up
- * to 16, 32, 64 or 128, in 16 bits.
+ * X[t] . A_i^T is scaled and rounded to `dtype` once (up to 32 tokens: to two numbers
+ * of `dtype`, the second what the first left); everything else is FP32 up to the one
+ * rounding of C.  The workspace is T x min(256, count) x the rank rounded up to 16,
+ * 32, 64 or 128, in 16 bits (twice that up to 32 tokens, four times for the gradients).
  *
  *   X            T x K, pitch ldx >= K
  *   W            w_major 0: K rows of N values, pitch ldw >= N; 1: N rows of K,
@@ -134,6 +135,8 @@ GEMM_API int gemm_adapters(int64_t T, int64_t N, int64_t K, int dtype, const voi
  *     dX[t]  = dY[t] . W^T + scales[i] (dY[t] . B_i^T) . A_i
  *     dA_i   = sum_t (scales[i] dY[t] . B_i^T)^T X[t]      over the tokens of i
  *     dB_i   = sum_t (scales[i] X[t] . A_i^T)^T dY[t]
+ *
+ * In dA and dB the rank-wide factors are two numbers of `dtype` each, as above.
  *
  *   plan         made with backward = 1
  *   dX           T x K, pitch lddx, or NULL

@@ -384,6 +384,29 @@ def test_adapters_of_every_rank(T, rank, dtype):
     check_adapters(X, W, A, B, ids, s, randn(T, 136, seed=98).to(dtype))
 
 
+@pytest.mark.parametrize("dtype", (BF16, F16))
+@pytest.mark.parametrize("T,rank,L", [(1, 1, 1), (2, 16, 2), (16, 3, 4), (32, 128, 3), (33, 1, 1), (90, 8, 30), (600, 1, 1), (600, 100, 3)])
+def test_adapters_gradients_and_few_tokens_are_as_exact_as_their_result(T, rank, L, dtype):
+    # low is two numbers of the type, together within u^2 / 2 relative (fp16: or 2^-25, half its smallest step) of the
+    # sum in FP32: the bounds above with that for u
+    X, W, A, B, ids, s = made_adapters(T, 136, 200, rank, L, dtype, seed=rank)
+    dY = randn(T, 200, seed=97).to(dtype)
+    plan = tg.adapter_plan(ids, L, backward=True)
+    C = tg.gemm_adapters(X, W, A, B, plan, s)
+    dX, dA, dB = tg.gemm_adapters_backward(dY, X, W, A, B, plan, s)
+    u = U[dtype]
+    try:
+        U[dtype] = u * u
+        want = exact_adapters(X, W, A, B, ids, s, dY)
+    finally:
+        U[dtype] = u
+    pairs = [(dA, "dA", X), (dB, "dB", dY)] + ([(C, "C", B), (dX, "dX", A)] if T <= 32 else [])
+    for got, name, other in pairs:
+        v, e = want[name]
+        floor = TINY[dtype] * (1 + float(other.abs().max()) * (T if name in ("dA", "dB") else rank))
+        within(got, v, e * (1 + u) + u * v.abs() + floor, name)
+
+
 @pytest.mark.parametrize("order", ("mixed", "sorted", "none", "one"))
 @pytest.mark.parametrize("T,L", [(1, 1), (64, 300), (100, 2), (700, 40), (1100, 600)])
 def test_adapters_in_any_order(T, L, order):

@@ -195,6 +195,7 @@ int run_low(int64_t T, int type, const Side &x, const Stack &stack, ProductAdapt
     ad.cols = stack.cols;
     ad.ld = stack.ld;
     ad.stride = stack.stride;
+    ad.low = low;
     c.ad = ad;
     c.C = low;
     c.ldc = ad.ld_low;
@@ -239,14 +240,15 @@ int run_add(int64_t T, int64_t cols, int type, const Side &x, const void *W, int
 int run_gradient(int64_t T, int type, const Side &x, ProductAdapters ad, void *low, void *out, int sms, cudaStream_t stream) {
     ProductCall c;
     c.mode = kModeGradient;
-    c.epilogue = kEpiSwapped;
+    c.epilogue = kEpiGradient;
     c.type = type;
     c.I = x.cols;
     c.J = ad.rank;
     c.K = T;
     c.plan = product_plan_gradient(ad.pitch, ad.count, x.cols, T, sms);
     c.p = {x.p, x.cols, x.ld, 1};
-    c.q = {low, ad.ld_low, ad.ld_low, 1};
+    c.q.mn = 1;                                   // (low, from its own map)
+    ad.low = low;
     c.ad = ad;
     c.C = out;
     c.ldc = x.cols;
@@ -351,7 +353,9 @@ int gemm_adapters(int64_t T, int64_t N, int64_t K, int dtype, const void *X, int
     cudaGetDevice(&dev);
     ProductAdapters pa = adapters_of(ad, plan, l);
     Side x = {"X", X, K, ldx, false, 0, 0, 0};
-    uint64_t bytes = ((uint64_t)T * pa.ld_low * 2 + 255) / 256 * 256;
+    // Few tokens do not average low's rounding out, and their tiles have room for the rests.
+    if (T <= 32) pa.rest = T * pa.ld_low;
+    uint64_t bytes = ((uint64_t)T * pa.ld_low * (pa.rest ? 4 : 2) + 255) / 256 * 256;
     if ((rc = plan_side(&x, T, dev, &bytes))) return rc;
     void *ws = nullptr;
     if ((rc = workspace(&ws, bytes, dev, stream))) return rc;
@@ -400,7 +404,8 @@ int gemm_adapters_backward(int64_t T, int64_t N, int64_t K, int dtype, const voi
     ProductAdapters pa = adapters_of(ad, plan, l);
     Side x = {"X", X, K, ldx, false, 0, 0, 0}, g = {"dY", dY, N, ldy, false, 0, 0, 0};
     const bool want_up = (dX && K > 0) || da, want_low = db != 0;
-    const uint64_t low_bytes = ((uint64_t)T * pa.ld_low * 2 + 255) / 256 * 256;
+    pa.rest = T * pa.ld_low;
+    const uint64_t low_bytes = ((uint64_t)T * pa.ld_low * 4 + 255) / 256 * 256;
     uint64_t bytes = low_bytes * ((want_up ? 1 : 0) + (want_low ? 1 : 0));
     if (bytes == 0) return GEMM_OK;
     if ((rc = plan_side(&g, T, dev, &bytes))) return rc;

@@ -19,6 +19,10 @@
 //              are 64 tokens each of the granules on the adapter's list, and the
 //              zeros in `low` drop the other tokens.
 //
+// `low` in 16 bits would be most of the gradients' error, and of a result of few tokens,
+// so what its rounding took is kept in 16 bits too and multiplied along there: it rides
+// in the ring slot of the first (more MMAs, no more slots).
+//
 // and four epilogues: C written with its columns on the lanes ("swapped": few
 // tokens, so that the lanes carry the weights' rows and a tile is only as wide as
 // the tokens are), C row by row, the statistics of a softmax over the columns, and
@@ -81,6 +85,7 @@ struct ProductParams {
     const int32_t *slots, *counts, *slot_of, *lists, *list_counts;
     int64_t granules;
     const float *scales;
+    int64_t rest;              // elements from low to what its rounding took (0: not kept)
     // loss
     const void *labels;
     int label_bytes;
@@ -99,7 +104,7 @@ struct ProductParams {
 
 template <int BN, int CG, int EPI, int PROWS>
 struct Cfg {
-    static constexpr bool SWAPPED = EPI == kEpiSwapped;
+    static constexpr bool SWAPPED = EPI == kEpiSwapped || EPI == kEpiGradient;
     static constexpr int EW = BN <= 32 ? 4 : 8;            // epilogue warps
     static constexpr int ROWS = kLanes * CG;
     static constexpr int COLS = BN / (EW / 4);             // columns of a thread
@@ -115,7 +120,11 @@ struct Cfg {
     // which nobody looks at: few tokens stream W through a ring that is nearly all W's.
     static constexpr int P_BYTES = PROWS * 128;
     static constexpr int Q_ROWS = BN / CG;                 // each CTA of a pair loads half of Q's rows
-    static constexpr int Q_BYTES = (Q_ROWS < 64 ? 64 : Q_ROWS) * 128;
+    // (an N-major chunk has at least 64 columns; the gradient has as much again for low's
+    // rests, and few tokens have room for theirs)
+    static constexpr int Q_ONE = (Q_ROWS < 64 ? 64 : Q_ROWS) * 128;
+    static constexpr int Q_BYTES = EPI == kEpiGradient ? 2 * Q_ONE : Q_ONE;
+    static constexpr bool ADD_RESTS = EPI == kEpiSwapped && Q_ROWS <= 32;
     static constexpr int Q_CHUNKS = Q_ROWS < 64 ? 1 : Q_ROWS / 64;
     static constexpr int BLOCK = P_BYTES + Q_BYTES;
     static_assert(PROWS == kLanes || (EPI == kEpiStats && Q_BYTES + P_BYTES >= kLanes * 128), "P's rows");
@@ -129,7 +138,7 @@ struct Cfg {
     static constexpr int FIT = (kSmemMax - FIXED) / STAGE;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
-    static_assert(STAGES >= 3 && SMEM <= kSmemMax, "ring");
+    static_assert(STAGES >= 2 && SMEM <= kSmemMax, "ring");
     static_assert((2 * STAGES + 4) * 8 + 16 <= kCtrlBytes, "barrier area");
     static_assert(2 * BN <= 512, "two accumulators");
     static_assert(!SWAPPED || kLanes * BN * 4 <= STAGES * STAGE, "a tile's partial sums fit in the ring");
@@ -281,6 +290,14 @@ __device__ __forceinline__ void write_four(const ProductParams &p, const Tile &T
         const bool mine = __ldg(p.slot_of + cr) == (int)(cc >> p.pitch_log2);
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = mine ? y[k] * side[k] : 0.f;
+        if (p.rest) {
+            float z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                z[k] = y[k] - (p.f16 ? __half2float(__float2half_rn(y[k])) : __bfloat162float(__float2bfloat16_rn(y[k])));
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + p.rest + cr * p.ldc + cc) =
+                make_uint2(epi_pack2(p.epi.out, z[0], z[1]), epi_pack2(p.epi.out, z[2], z[3]));
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = finish(p.epi, y[k], side[k]);
@@ -659,7 +676,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                const __grid_constant__ CUtensorMap tmLow, const __grid_constant__ CUtensorMap tmAd,
                const __grid_constant__ CUtensorMap tmC, const ProductParams p) {
     using Cf = Cfg<BN, CG, EPI, PROWS>;
-    constexpr bool kPair = CG == 2, kSwapped = Cf::SWAPPED;
+    constexpr bool kPair = CG == 2, kSwapped = Cf::SWAPPED, kGradient = EPI == kEpiGradient;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -693,8 +710,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
         *abort_flag = 0;
         ptx::fence_mbar_init();
         if (p.num_kb > 0) {
-            ptx::prefetch_tensormap(&tmP);
-            ptx::prefetch_tensormap(&tmQ);
+            if (p.mode != kModeLow) ptx::prefetch_tensormap(&tmP);
+            if (!kGradient) ptx::prefetch_tensormap(&tmQ);
         }
         if (p.tma_store) ptx::prefetch_tensormap(&tmC);
     }
@@ -747,7 +764,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 ++issued;
                 return true;
             };
-            if (kSwapped && p.mode == kModeLow) {
+            if (EPI == kEpiSwapped && p.mode == kModeLow) {
                 // the adapters of the tile's lanes: at most eight boxes of `pitch` rows
                 const int pitch = 1 << p.pitch_log2, boxes = min(kLanes, T.i1 - T.i0) >> p.pitch_log2;
                 const int s = (T.i0 >> p.pitch_log2) + (int)lane;
@@ -774,7 +791,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 }
                 continue;
             }
-            if (kSwapped && p.mode == kModeGradient) {
+            if constexpr (kGradient) {
                 // 64 tokens of a granule on the list at a time, and the adapter's slot in it
                 const int log2_blocks = 31 - __clz(p.granule_blocks);
                 WarpList list = {p.lists + T.e * p.granules, (T.kb1 + p.granule_blocks - 1) >> log2_blocks};
@@ -796,8 +813,11 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                             ptx::tma_load_2d(sp + s * Cf::BLOCK, &tmP, fb, i0, k0[s]);
                             ptx::tma_load_2d(sp + s * Cf::BLOCK + kChunkBytes, &tmP, fb, i0 + 64, k0[s]);
 #pragma unroll
-                            for (int c = 0; c < Cf::Q_CHUNKS; ++c)
-                                ptx::tma_load_2d(sq + (uint32_t)(s * Cf::BLOCK + c * kChunkBytes), &tmQ, fb, jx[s] + 64 * c, k0[s]);
+                            for (int c = 0; c < Cf::Q_CHUNKS; ++c) {
+                                const uint32_t to_q = sq + (uint32_t)(s * Cf::BLOCK + c * kChunkBytes);
+                                ptx::tma_load_3d<1>(to_q, &tmLow, fb, jx[s] + 64 * c, k0[s], 0);
+                                ptx::tma_load_3d<1>(to_q + Cf::Q_ONE, &tmLow, fb, jx[s] + 64 * c, k0[s], 1);
+                            }
                         }
                     }
                     __syncwarp();
@@ -853,13 +873,15 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                     }
                     if (!next_slot()) break;
                     if (ptx::elect_one()) {
-                        constexpr int kLow = kSwapped ? Cf::Q_ROWS * 128 : Cf::P_BYTES;
+                        constexpr int kLow = !kSwapped ? Cf::P_BYTES : Cf::ADD_RESTS ? 2 * Cf::Q_ROWS * 128 : Cf::Q_ROWS * 128;
                         if (rank == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)(all * box * 128 * kAddChunks + n * kLow) * CG);
 #pragma unroll
                         for (int s = 0; s < kSlotBlocks; ++s) {
                             if (s >= n) break;
                             const int row0 = (kb + s - p.num_kb) * kBlockK;
-                            ptx::tma_load_2d_cg<CG>((kSwapped ? sq : sp) + s * Cf::BLOCK, &tmLow, to, row0, kSwapped ? j0 : i0);
+                            ptx::tma_load_3d<CG>((kSwapped ? sq : sp) + s * Cf::BLOCK, &tmLow, to, row0, kSwapped ? j0 : i0, 0);
+                            if (Cf::ADD_RESTS)
+                                ptx::tma_load_3d<CG>(sq + s * Cf::BLOCK + Cf::Q_ROWS * 128, &tmLow, to, row0, j0, 1);
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
                                 if (u < boxes[s]) {
@@ -938,9 +960,13 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                             for (int k = kb; k < next; ++k) {
                                 const int steps = min(4, ((T.slots << p.pitch_log2) - (k - p.num_kb) * kBlockK) / 16);
                                 const uint32_t at_block = (uint32_t)((k - kb) * (Cf::BLOCK / 16));
-                                for (int kk = 0; kk < steps; ++kk)
+                                for (int kk = 0; kk < steps; ++kk) {
                                     ptx::mma_f16_sw128<CG>(d, pd + at_block + ps * (uint32_t)kk, qd + at_block + qs * (uint32_t)kk,
                                                            p.idesc_add, kk != 0 || k != kb ? 1u : first);
+                                    if (Cf::ADD_RESTS)
+                                        ptx::mma_f16_sw128<CG>(d, pd + at_block + ps * (uint32_t)kk,
+                                                               qd + at_block + qs * (uint32_t)kk + Cf::Q_ROWS * 128 / 16, p.idesc_add, 1u);
+                                }
                             }
                         } else {
                             const uint32_t pd = sp | p_lead, qd = sq | q_lead;
@@ -952,6 +978,12 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                                 for (int kk = 0; kk < 4; ++kk)
                                     ptx::mma_f16_sw128<CG>(d, pd + at_block + p_step * kk, qd + at_block + q_step * kk, p.idesc,
                                                            kk != 0 || s != 0 ? 1u : first);
+                                if constexpr (kGradient) {
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        ptx::mma_f16_sw128<CG>(d, pd + at_block + p_step * kk, qd + at_block + q_step * kk + Cf::Q_ONE / 16,
+                                                               p.idesc, 1u);
+                                }
                             }
                         }
                         if (kPair) ptx::mma_commit_pair(empty(at.slot), 0x3);
@@ -1255,6 +1287,12 @@ int launch(const Maps &m, const ProductParams &p, int grid, cudaStream_t stream)
 }
 
 int launch_plan(const ProductPlan &pl, int epilogue, const Maps &m, const ProductParams &p, int grid, cudaStream_t stream) {
+    if (epilogue == kEpiGradient) {
+        if (pl.bn == 16) return launch<16, 1, kEpiGradient>(m, p, grid, stream);
+        if (pl.bn == 32) return launch<32, 1, kEpiGradient>(m, p, grid, stream);
+        if (pl.bn == 64) return launch<64, 1, kEpiGradient>(m, p, grid, stream);
+        return launch<128, 1, kEpiGradient>(m, p, grid, stream);
+    }
     if (epilogue == kEpiSwapped) {
         if (pl.bn == 16) return launch<16, 1, kEpiSwapped>(m, p, grid, stream);
         if (pl.bn == 32) return launch<32, 1, kEpiSwapped>(m, p, grid, stream);
@@ -1368,7 +1406,7 @@ ProductPlan product_plan_gradient(int64_t pitch, int64_t adapters, int64_t cols,
 int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     const int64_t kMax = 0x7fffffffLL - 512;
     const ProductPlan &pl = c.plan;
-    const bool swapped = c.epilogue == kEpiSwapped;
+    const bool swapped = c.epilogue == kEpiSwapped || c.epilogue == kEpiGradient;
     ProductParams p = {};
     p.mode = c.mode;
     p.I = (int)c.I;
@@ -1409,6 +1447,7 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     p.list_counts = ad.list_counts;
     p.granules = ad.granules;
     p.scales = ad.scales;
+    p.rest = ad.rest;
     p.labels = c.loss.labels;
     p.label_bytes = c.loss.label_bytes;
     p.first = c.loss.first;
@@ -1433,17 +1472,20 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     Maps m;
     std::memset(&m, 0, sizeof m);
     int rc = GEMM_OK;
-    if (c.mode == kModeGradient || p.num_kb > 0) {
+    const int64_t low_cols = (int64_t)ad.max_slots * ad.pitch, both = ad.rest ? 2 : 1;
+    if (c.mode == kModeGradient) {
+        rc = encode_operand(&m.p, c.p, c.type, c.K, kLanes);
+        if (rc == GEMM_OK) rc = encode(&m.low, ad.low, c.type, c.K, low_cols, ad.ld_low, 64, both, ad.rest);
+    } else if (p.num_kb > 0) {
         if (c.mode != kModeLow) rc = encode_operand(&m.p, c.p, c.type, c.K, pl.p_rows);
         if (rc == GEMM_OK) rc = encode_operand(&m.q, c.q, c.type, c.K, p.width / pl.cg);
     }
-    const int64_t low_cols = (int64_t)ad.max_slots * ad.pitch;
     if (rc == GEMM_OK && c.mode == kModeLow && p.num_kb > 0)
         rc = encode(&m.ad, ad.p, c.type, ad.rank, ad.cols, ad.ld, ad.pitch, ad.count, ad.stride);
     if (rc == GEMM_OK && c.mode == kModeAdd) {
         rc = encode(&m.ad, ad.p, c.type, ad.rank, ad.cols, ad.ld, std::min(ad.pitch, kBlockK), ad.count, ad.stride);
         if (rc == GEMM_OK)
-            rc = encode(&m.low, ad.low, c.type, swapped ? c.J : c.I, low_cols, ad.ld_low, swapped ? pl.bn : kLanes);
+            rc = encode(&m.low, ad.low, c.type, swapped ? c.J : c.I, low_cols, ad.ld_low, swapped ? pl.bn : kLanes, both, ad.rest);
     }
     if (rc) return rc;
     if (c.epilogue != kEpiStats) {

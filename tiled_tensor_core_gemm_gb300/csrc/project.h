@@ -30,7 +30,8 @@ struct ProductAdapters {
     int64_t granules = 0;
     const float *scales = nullptr;       // [adapter] or nullptr
     void *low = nullptr;                 // tokens x (max_slots * pitch): the rank-wide activations,
-    int64_t ld_low = 0;                  // zero in the slots that are not a token's
+    int64_t ld_low = 0;                  // zero in the slots that are not a token's; and, with
+    int64_t rest = 0;                    // `rest` != 0, that many elements on, what their rounding took
 };
 
 // What the loss epilogues take and give, per token (lane).
@@ -75,7 +76,8 @@ enum ProductMode : int {
     kModeGradient = 3          // one product per adapter over the tokens that take it (swapped)
 };
 enum ProductEpilogue : int { kEpiSwapped = 0, kEpiRows = 1, kEpiStats = 2, kEpiDlogits = 3,
-                            kEpiRests = 4 /* kEpiRows with ProductRests */ };
+                            kEpiRests = 4 /* kEpiRows with ProductRests */,
+                            kEpiGradient = 5 /* kEpiSwapped of kModeGradient */ };
 
 // Columns of the tile, CTAs of it, its K ranges within a cluster (swapped) or through
 // memory (row-wise).
