@@ -28,6 +28,14 @@
 // the tokens are), C row by row, the statistics of a softmax over the columns, and
 // the gradient of its logits.
 //
+// What bounds it (GB300): with many tokens the tensor cores, which a 256 x 256 pair keeps
+// 86% busy with the loss statistics of 2048 x 16384 x 4096 (91% of active cycles; 543 to
+// 573 us for 65536 columns = 1.92 to 2.0 PFLOP/s) and 71 to 78% with its gradients'
+// products (few rounds); over a step of 8192 x 131072 x 4096 the power cap does, at 0.97 to
+// 1.0 of the sustained rate.  With few, the stream of the weights: 5 x 50021 x 2048 at
+// 5.4 TB/s; 64 x 4096 x 12288 at 4.3 from 96 of 152 SMs.  In between, a K-block's 0.18 us
+// in small tiles (of which the MMAs' issue is about half) and 8 us around them.
+//
 // Roles as in scaled.cu: warp 0 issues the TMA loads into a ring, warp 1 the MMAs
 // (K = 64 a ring slot, one 128-byte swizzle row), and from warp 4 on the epilogue
 // warps, which read one of two accumulators while the MMAs fill the other.  Either
@@ -37,6 +45,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -280,14 +289,14 @@ __device__ __forceinline__ float finish(const EpiParams &e, float acc, float bia
 }
 
 // Four neighbouring columns of row cr of C.  `side`: the bias of each, or (low)
-// the factor of their slot's adapter.
+// the factor of their slot's adapter; `slot`: (low) the token's.
 __device__ __forceinline__ void write_four(const ProductParams &p, const Tile &T, int64_t cr, int64_t cc, float4 v,
-                                           const float (&side)[4]) {
+                                           const float (&side)[4], int slot) {
     float y[4] = {v.x, v.y, v.z, v.w};
     if (p.mode == kModeLow) {
         // a token keeps the columns of its own slot (selected, not multiplied: what
         // another slot's product held, a NaN included, goes)
-        const bool mine = __ldg(p.slot_of + cr) == (int)(cc >> p.pitch_log2);
+        const bool mine = slot == (int)(cc >> p.pitch_log2);
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = mine ? y[k] * side[k] : 0.f;
         if (p.rest) {
@@ -333,12 +342,10 @@ __device__ __forceinline__ void side_of(const ProductParams &p, const Tile &T, i
 // columns, through 2 KB of shared memory, 16 rows of C at a time: eight lanes
 // then hold 32 neighbouring elements of a row.
 template <int COLS>
-__device__ __forceinline__ void write_swapped(const ProductParams &p, const Tile &T, int row0, int col0,
-                                              float (&acc)[COLS], uint32_t buf, int lane) {
+__device__ __forceinline__ void write_swapped(const ProductParams &p, const Tile &T, int row0, int col0, float (&acc)[COLS],
+                                              const float (&side)[4], int (&own)[COLS / 4], uint32_t buf, int lane) {
     const int u = lane & 7;
     const int64_t cc = (int64_t)T.i0 + row0 + 4 * u;
-    float side[4];
-    side_of(p, T, cc, side);
 #pragma unroll 1
     for (int c0 = 0; c0 < COLS; c0 += 16) {
         const int64_t r0 = (int64_t)T.j0 + col0 + c0;
@@ -347,13 +354,27 @@ __device__ __forceinline__ void write_swapped(const ProductParams &p, const Tile
 #pragma unroll
         for (int c = 0; c < 16; ++c) ptx::st_shared_f(buf + 4u * (uint32_t)(c * 32 + lane), acc[c]);
         __syncwarp();
-#pragma unroll 1
-        for (int r = lane >> 3; r < 16 && r0 + r < T.j1; r += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = (lane >> 3) + 4 * k;
             const float4 v = ptx::ld_shared_v4f(buf + 128u * (uint32_t)r + 16u * (uint32_t)u);
-            if (cc < T.i1) write_four(p, T, r0 + r, cc, v, side);
+            if (cc < T.i1 && r0 + r < T.j1) write_four(p, T, r0 + r, cc, v, side, own[k]);
         }
 #pragma unroll
         for (int c = 0; c + 16 < COLS; ++c) acc[c] = acc[c + 16];
+#pragma unroll
+        for (int k = 0; k + 4 < COLS / 4; ++k) own[k] = own[k + 4];
+    }
+}
+
+// The slots (low) of the rows of C that a lane writes in write_swapped, looked up while
+// the MMAs run (with the factors likewise: one token's two launches 21 -> 17 us by graph).
+template <int COLS>
+__device__ __forceinline__ void slots_of_rows(const ProductParams &p, const Tile &T, int col0, int lane, int (&own)[COLS / 4]) {
+#pragma unroll
+    for (int k = 0; k < COLS / 4; ++k) {
+        const int r = T.j0 + col0 + 4 * k + (lane >> 3);
+        own[k] = p.mode == kModeLow && r < T.j1 ? __ldg(p.slot_of + r) : -1;
     }
 }
 
@@ -1072,6 +1093,14 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 }
                 continue;
             }
+            float side[4] = {0.f, 0.f, 0.f, 0.f};
+            int own[kSwapped ? Cf::COLS / 4 : 1] = {};
+            if constexpr (kSwapped) {
+                if (p.splits == 1) {
+                    side_of(p, T, (int64_t)T.i0 + (int)(quarter * 32) + 4 * (int)(lane & 7), side);
+                    slots_of_rows<Cf::COLS>(p, T, col0, (int)lane, own);
+                }
+            }
             if (have && !wait_warp(accf(acc.slot), acc.lap, bounds, kRoleEpilogue, t)) break;
             ptx::tc_fence_after();
             const uint32_t src = tbase + (uint32_t)(acc.slot * BN), back = acce_to + 8u * (uint32_t)acc.slot;
@@ -1107,7 +1136,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                     for (int c = 0; c < Cf::COLS; ++c) part[(col0 + c) * kLanes + row] = v[c];
                     break;                                   // one tile a cluster
                 }
-                write_swapped<Cf::COLS>(p, T, (int)(quarter * 32), col0, v, out_buf, (int)lane);
+                write_swapped<Cf::COLS>(p, T, (int)(quarter * 32), col0, v, side, own, out_buf, (int)lane);
             } else {
                 const int64_t i0 = (int64_t)T.i0 + (int)(rank * kLanes + quarter * 32), i = i0 + lane;
                 const int64_t j0 = (int64_t)T.j0 + col0;
@@ -1172,30 +1201,36 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
     // of them, in their order, and writes it: rows of C, four neighbouring
     // elements a thread and step, two steps' loads in flight.
     if (kSwapped && p.splits > 1) {
+        const bool writes = warp >= 4 && unit < p.num_tiles;
+        Tile T = {};
+        float side[4] = {0.f, 0.f, 0.f, 0.f};
+        int64_t cc = 0;                                  // (a warp's lanes take a whole row of the tile)
+        if (writes) {
+            T = tile_at<BN, Cf::ROWS, kSwapped>(p, unit, crank);
+            cc = (int64_t)T.i0 + 4 * (int)lane;
+            side_of(p, T, cc, side);
+        }
         __syncwarp();
         ptx::cluster_sync();
-        if (warp >= 4 && unit < p.num_tiles && *abort_flag == 0) {
-            const Tile T = tile_at<BN, Cf::ROWS, kSwapped>(p, unit, crank);
-            if (!T.none) {
-                const int c0 = BN * crank / p.splits, quads = (BN * (crank + 1) / p.splits - c0) * (kLanes / 4);
-                constexpr int kStep = Cf::EW * 32;
-                const int64_t cc = (int64_t)T.i0 + 4 * (int)lane;          // (a warp's lanes take a whole row of the tile)
-                float side[4];
-                side_of(p, T, cc, side);
-                for (int q = (int)threadIdx.x - 128; q < quads; q += 2 * kStep) {
-                    const int c = c0 + q / 32, d = c0 + min(q + kStep, quads - 1) / 32;
-                    const uint32_t at0 = ring0 + 4u * (uint32_t)(c * kLanes + 4 * (int)lane);
-                    const uint32_t at1 = ring0 + 4u * (uint32_t)(d * kLanes + 4 * (int)lane);
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
-                    for (int s = 0; s < p.splits; ++s) {
-                        const float4 x = ptx::ld_cluster_v4f(ptx::mapa_shared(at0, (uint32_t)s));
-                        const float4 y = ptx::ld_cluster_v4f(ptx::mapa_shared(at1, (uint32_t)s));
-                        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
-                        w = make_float4(w.x + y.x, w.y + y.y, w.z + y.z, w.w + y.w);
-                    }
-                    if (T.j0 + c < T.j1 && cc < T.i1) write_four(p, T, (int64_t)T.j0 + c, cc, v, side);
-                    if (q + kStep < quads && T.j0 + d < T.j1 && cc < T.i1) write_four(p, T, (int64_t)T.j0 + d, cc, w, side);
+        if (writes && !T.none && *abort_flag == 0) {
+            const int c0 = BN * crank / p.splits, quads = (BN * (crank + 1) / p.splits - c0) * (kLanes / 4);
+            constexpr int kStep = Cf::EW * 32;
+            for (int q = (int)threadIdx.x - 128; q < quads; q += 2 * kStep) {
+                const int c = c0 + q / 32, d = c0 + min(q + kStep, quads - 1) / 32;
+                const bool first = T.j0 + c < T.j1 && cc < T.i1, second = q + kStep < quads && T.j0 + d < T.j1 && cc < T.i1;
+                const int own_c = p.mode == kModeLow && first ? __ldg(p.slot_of + T.j0 + c) : -1;
+                const int own_d = p.mode == kModeLow && second ? __ldg(p.slot_of + T.j0 + d) : -1;
+                const uint32_t at0 = ring0 + 4u * (uint32_t)(c * kLanes + 4 * (int)lane);
+                const uint32_t at1 = ring0 + 4u * (uint32_t)(d * kLanes + 4 * (int)lane);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
+                for (int s = 0; s < p.splits; ++s) {
+                    const float4 x = ptx::ld_cluster_v4f(ptx::mapa_shared(at0, (uint32_t)s));
+                    const float4 y = ptx::ld_cluster_v4f(ptx::mapa_shared(at1, (uint32_t)s));
+                    v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+                    w = make_float4(w.x + y.x, w.y + y.y, w.z + y.z, w.w + y.w);
                 }
+                if (first) write_four(p, T, (int64_t)T.j0 + c, cc, v, side, own_c);
+                if (second) write_four(p, T, (int64_t)T.j0 + d, cc, w, side, own_d);
             }
         }
         __syncwarp();
@@ -1260,8 +1295,6 @@ template <int BN, int CG, int EPI, int PROWS = kLanes>
 int launch(const Maps &m, const ProductParams &p, int grid, cudaStream_t stream) {
     using Cf = Cfg<BN, CG, EPI, PROWS>;
     auto kern = product_kernel<BN, CG, EPI, PROWS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
-    if (e != cudaSuccess) return op_launched("cudaFuncSetAttribute", e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(Cf::THREADS, 1, 1);
@@ -1283,7 +1316,26 @@ int launch(const Maps &m, const ProductParams &p, int grid, cudaStream_t stream)
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return op_launched("product launch", cudaLaunchKernelEx(&cfg, kern, m.p, m.q, m.low, m.ad, m.c, p));
+    // The shared memory a kernel may have is set once a device, and again should a launch
+    // find it unset (after a device reset): setting it takes 0.5 us of a 25 us call.
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    for (int again = 0;; ++again) {
+        if (again || !(set.load(std::memory_order_relaxed) & bit)) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
+            if (e != cudaSuccess) return op_launched("cudaFuncSetAttribute", e);
+            set.fetch_or(bit, std::memory_order_relaxed);
+            again = 1;
+        }
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m.p, m.q, m.low, m.ad, m.c, p);
+        if (e == cudaErrorInvalidValue && !again) {
+            cudaGetLastError();
+            continue;
+        }
+        return op_launched("product launch", e);
+    }
 }
 
 int launch_plan(const ProductPlan &pl, int epilogue, const Maps &m, const ProductParams &p, int grid, cudaStream_t stream) {
@@ -1391,8 +1443,8 @@ ProductPlan product_plan_tokens(int64_t tokens, int64_t cols, int64_t K, int sms
     return plan_splits(bn, op_cdiv(cols, kLanes) * op_cdiv(tokens, bn), op_cdiv(K, kBlockK), sms);
 }
 
-// The rank-wide activations: 64 tokens a tile, so that a prompt's tiles fill the
-// SMs although each has few slots.
+// The rank-wide activations: 64 tokens a tile, so that a prompt's tiles fill the SMs
+// although each has few slots (8192 x 4096: 20 us; tiles of 128 in 2 K ranges 24).
 ProductPlan product_plan_low(int64_t tokens, int64_t lanes, int64_t K, int sms) {
     const int bn = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
     return plan_splits(bn, op_cdiv(lanes, kLanes) * op_cdiv(tokens, bn), op_cdiv(K, kBlockK), sms);
