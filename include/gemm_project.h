@@ -113,7 +113,8 @@ typedef struct {
  *
  * and without the middle term for a token that takes none.  The rank-wide
  * X[t] . A_i^T is scaled and rounded to `dtype` once (up to 32 tokens: to two numbers
- * of `dtype`, the second what the first left); everything else is FP32 up to the one
+ * of `dtype`, the second what the first left; in FP16 it has to stay below 65504);
+ * everything else is FP32 up to the one
  * rounding of C.  The workspace is T x min(256, count) x the rank rounded up to 16,
  * 32, 64 or 128, in 16 bits (twice that up to 32 tokens, four times for the gradients).
  *

@@ -90,7 +90,7 @@ struct ProductParams {
     const float *old;
     int64_t ld_old;
     // adapters
-    int pitch_log2, granule, granule_blocks, max_slots;
+    int pitch_log2, granule, granule_blocks, max_slots, adapters;
     const int32_t *slots, *counts, *slot_of, *lists, *list_counts;
     int64_t granules;
     const float *scales;
@@ -217,6 +217,9 @@ struct Tile {
     __device__ __forceinline__ int slot_blocks(int kb) const { return min(kSlotBlocks, (kb < own ? own : kb1) - kb); }
 };
 
+// The slots of a granule (within what a plan can hold, whatever the buffer given as one does).
+__device__ __forceinline__ int slots_of(const ProductParams &p, int g) { return min(max(__ldg(p.counts + g), 0), p.max_slots); }
+
 template <int BN, int ROWS, bool SWAPPED>
 __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank) {
     Tile T;
@@ -231,14 +234,14 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank
         T.i0 = ti * ROWS;
         T.j0 = (t - ti * p.tiles_j) * BN;
         T.g = T.j0 / p.granule;
-        T.slots = __ldg(p.counts + T.g);
+        T.slots = slots_of(p, T.g);
         T.i1 = T.slots << p.pitch_log2;
         T.none = T.i0 >= T.i1;
     } else if (p.mode == kModeGradient) {
         T.e = t / p.tiles_i;
         T.i0 = (t - T.e * p.tiles_i) * ROWS;
         T.j0 = 0;
-        total = __ldg(p.list_counts + T.e) * p.granule_blocks;
+        total = min(max(__ldg(p.list_counts + T.e), 0), (int)p.granules) * p.granule_blocks;
     } else {
         if (!SWAPPED && p.k_parts > 1) {
             const int tiles = p.tiles_i * p.tiles_j;
@@ -255,7 +258,7 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank
         T.j1 = min(p.J, T.j0 + p.width);
         if (p.mode == kModeAdd) {
             T.g = (SWAPPED ? T.j0 : T.i0) / p.granule;
-            T.slots = __ldg(p.counts + T.g);
+            T.slots = slots_of(p, T.g);
             total += ((T.slots << p.pitch_log2) + kBlockK - 1) / kBlockK;
         }
     }
@@ -329,7 +332,8 @@ __device__ __forceinline__ void write_four(const ProductParams &p, const Tile &T
 __device__ __forceinline__ void side_of(const ProductParams &p, const Tile &T, int64_t cc, float (&side)[4]) {
     if (p.mode == kModeLow) {
         const int s = (int)(cc >> p.pitch_log2);
-        const float f = p.scales && cc < T.i1 ? __ldg(p.scales + __ldg(p.slots + (int64_t)T.g * p.max_slots + s)) : 1.f;
+        const int ad = p.scales && cc < T.i1 ? __ldg(p.slots + (int64_t)T.g * p.max_slots + s) : -1;
+        const float f = (unsigned)ad < (unsigned)p.adapters ? __ldg(p.scales + ad) : 1.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) side[k] = f;
     } else {
@@ -1492,6 +1496,7 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     p.granule = ad.granule;
     p.granule_blocks = ad.granule < kBlockK ? 1 : ad.granule / kBlockK;
     p.max_slots = ad.max_slots;
+    p.adapters = (int)ad.count;
     p.slots = ad.slots;
     p.counts = ad.counts;
     p.slot_of = ad.slot_of;
