@@ -682,6 +682,12 @@ def test_the_example_runs_them_together():
     assert all(v < 0.01 for v in found.values()), found
 
 
+@pytest.mark.parametrize("T", (65536, 70000))           # statistics 65536 tokens at a time; dW without the rests beyond
+def test_loss_of_many_tokens(T):
+    H, W, y = made_loss(T, 320, 72, BF16, seed=21)
+    check_loss(H[:, :65], W[:, :65], y, torch.full((1,), 1.0 / T, device="cuda").expand(T), smoothing=0.1)
+
+
 def test_loss_past_32_bits():
     # W and dW pass 2^31 elements; labels at both ends
     T, V, D = 3, 530000, 4104

@@ -10,7 +10,9 @@
 // Backward, the vocabulary in pieces: the piece's logits again with the gradient of
 // the softmax as epilogue (16 bits, to a workspace), then dH += d W and dW = d^T H,
 // the latter reading d and H as they lie (both MN-major).  6 T V D flops; dH's sums
-// are read and written once a piece in FP32.
+// are read and written once a piece in FP32 (or kept as K ranges, where it has few
+// tiles).  What rounding d took from its label entries is added back in FP32
+// (project.h: ProductRests).
 #include <algorithm>
 
 #include "gemm_project.h"
@@ -396,51 +398,59 @@ int gemm_project_loss(int64_t T, int64_t V, int64_t D, int dtype, const void *H,
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     // in one piece, unless W has to be copied (256 MB at a time)
     const int64_t piece = piece_columns(V, a.pack_w ? (1LL << 27) / std::max<int64_t>(D, 1) : V + 256);
-    const ProductPlan plan = product_plan_stats(T, std::min(piece, V), D, !a.w_major, sms);
+    // the tokens 65536 at a time, which bounds the memory of their parts (half a GB at V = 131072)
+    const int64_t most = std::min<int64_t>(T, 65536);
+    const ProductPlan plan = product_plan_stats(most, std::min(piece, V), D, !a.w_major, sms);
     int64_t parts = 0;
     for (int64_t v = 0; v < V; v += piece) parts += product_parts(plan, std::min(piece, V - v));
     if (parts > 0x7fffffffLL) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
     const int64_t h_pitch = a.pack_h ? op_round_up(D, 8) : a.ldh;
+    const bool smooth = a.how.smoothing != 0.f;
     Workspace ws;
-    const uint64_t at_parts = ws.add((uint64_t)parts * T * 8), at_sums = ws.add(a.how.smoothing != 0.f ? (uint64_t)parts * T * 4 : 0),
-                   at_hits = ws.add((uint64_t)T * 4), at_h = ws.add(a.pack_h ? (uint64_t)T * h_pitch * 2 : 0),
+    const uint64_t at_parts = ws.add((uint64_t)parts * most * 8), at_sums = ws.add(smooth ? (uint64_t)parts * most * 4 : 0),
+                   at_hits = ws.add((uint64_t)most * 4), at_h = ws.add(a.pack_h ? (uint64_t)T * h_pitch * 2 : 0),
                    at_w = ws.add((uint64_t)packed_w_bytes(a, piece));
     if ((rc = ws.make(stream))) return rc;
-    ProductCall c;
-    c.epilogue = kEpiStats;
-    c.type = a.type;
-    c.I = T;
-    c.K = D;
-    c.plan = plan;
-    c.p = {H, T, h_pitch, 0};
+    const void *h = H;
     if (a.pack_h) {
-        c.p.p = ws.base + at_h;
+        h = ws.base + at_h;
         rc = op_launched("operand pack", pack_rows_launch(H, a.ldh, ws.base + at_h, h_pitch, T, D, 2, a.h_lo, a.h_hi, stream));
     }
-    c.loss = loss_of(a);
-    c.loss.hits = reinterpret_cast<float *>(ws.base + at_hits);
-    int64_t part = 0;
-    for (int64_t v = 0; rc == GEMM_OK && v < V; v += piece) {
-        c.J = std::min(piece, V - v);
-        rc = piece_of_w(a, v, c.J, ws.base + at_w, &c.q, stream);
+    float2 *const part_of = reinterpret_cast<float2 *>(ws.base + at_parts);
+    float *const sum_of = reinterpret_cast<float *>(ws.base + at_sums), *const hits = reinterpret_cast<float *>(ws.base + at_hits);
+    for (int64_t t = 0; rc == GEMM_OK && t < T; t += most) {
+        const int64_t n = std::min(most, T - t);
+        const void *mine = static_cast<const uint8_t *>(labels) + t * label_bytes;
+        ProductCall c;
+        c.epilogue = kEpiStats;
+        c.type = a.type;
+        c.I = n;
+        c.K = D;
+        c.plan = plan;
+        c.p = {static_cast<const uint16_t *>(h) + t * h_pitch, n, h_pitch, 0};
+        c.loss = loss_of(a);
+        c.loss.labels = mine;
+        c.loss.hits = hits;
+        int64_t part = 0;
+        for (int64_t v = 0; v < V; v += piece) {
+            c.J = std::min(piece, V - v);
+            if ((rc = piece_of_w(a, v, c.J, ws.base + at_w, &c.q, stream))) break;
+            c.loss.first = v;
+            c.loss.parts = part_of + part * n;
+            c.loss.sums = sum_of + part * n;
+            part += product_parts(plan, c.J);
+            if ((rc = product_launch(c, sms, stream))) break;
+        }
         if (rc) break;
-        c.loss.first = v;
-        c.loss.parts = reinterpret_cast<float2 *>(ws.base + at_parts) + part * T;
-        c.loss.sums = reinterpret_cast<float *>(ws.base + at_sums) + part * T;
-        part += product_parts(plan, c.J);
-        rc = product_launch(c, sms, stream);
-    }
-    if (rc == GEMM_OK) {
         auto finish = [&](auto tokens) {
             constexpr int kTokens = decltype(tokens)::value;
-            return op_launched("loss", launch_pdl(loss_finish<kTokens>, dim3((unsigned)op_cdiv(T, kTokens)), dim3(32 * kFinishWarps), 0,
-                                                  stream, T, V, (int)parts, reinterpret_cast<const float2 *>(ws.base + at_parts),
-                                                  a.how.smoothing != 0.f ? reinterpret_cast<const float *>(ws.base + at_sums) : nullptr,
-                                                  reinterpret_cast<const float *>(ws.base + at_hits), labels, label_bytes, a.how,
-                                                  loss, lse));
+            return op_launched("loss", launch_pdl(loss_finish<kTokens>, dim3((unsigned)op_cdiv(n, kTokens)), dim3(32 * kFinishWarps), 0,
+                                                  stream, n, V, (int)parts, (const float2 *)part_of,
+                                                  (const float *)(smooth ? sum_of : nullptr), (const float *)hits, mine, label_bytes,
+                                                  a.how, loss ? loss + t : nullptr, lse + t));
         };
-        if (T <= 256) rc = finish(std::integral_constant<int, 1>());
-        else if (T <= 2048) rc = finish(std::integral_constant<int, 8>());
+        if (n <= 256) rc = finish(std::integral_constant<int, 1>());
+        else if (n <= 2048) rc = finish(std::integral_constant<int, 8>());
         else rc = finish(std::integral_constant<int, 32>());
     }
     return ws.done(rc, stream);
