@@ -180,8 +180,17 @@ ProductAdapters adapters_of(const gemm_adapters_t *ad, const int32_t *plan, cons
     return a;
 }
 
-// low = scale * x . stack_i^T, in the slot of each token's adapter.
-int run_low(int64_t T, int type, const Side &x, const Stack &stack, ProductAdapters ad, void *low, int sms, cudaStream_t stream) {
+// low = scale * x . stack_i^T, in the slot of each token's adapter; with x2 the same of
+// it and stack2 to low2, in the same launch.
+int run_low(int64_t T, int type, const Side &x, const Stack &stack, ProductAdapters ad, void *low, const Side *x2, const Stack *stack2,
+            void *low2, int sms, cudaStream_t stream) {
+    auto with = [](ProductAdapters a, const Stack &s) {
+        a.p = s.p;
+        a.cols = s.cols;
+        a.ld = s.ld;
+        a.stride = s.stride;
+        return a;
+    };
     ProductCall c;
     c.mode = kModeLow;
     c.epilogue = kEpiSwapped;
@@ -189,16 +198,19 @@ int run_low(int64_t T, int type, const Side &x, const Stack &stack, ProductAdapt
     c.I = ad.ld_low;
     c.J = T;
     c.K = x.cols;
-    c.plan = product_plan_low(T, ad.ld_low, x.cols, sms);
+    c.plan = product_plan_low(T, x2 ? 2 * op_round_up(ad.ld_low, 128) : ad.ld_low, x2 ? std::min(x.cols, x2->cols) : x.cols, sms);
     c.q = {x.p, T, x.ld, 0};
-    ad.p = stack.p;
-    ad.cols = stack.cols;
-    ad.ld = stack.ld;
-    ad.stride = stack.stride;
-    ad.low = low;
-    c.ad = ad;
+    c.ad = with(ad, stack);
     c.C = low;
     c.ldc = ad.ld_low;
+    if (x2) {
+        c.two = true;
+        c.second = {x2->p, T, x2->ld, 0};
+        c.second_k = x2->cols;
+        c.ad2 = with(ad, *stack2);
+        c.C2 = low2;
+        c.ldc2 = ad.ld_low;
+    }
     c.epi.active = 1;
     c.epi.out = type;
     return product_launch(c, sms, stream);
@@ -236,23 +248,36 @@ int run_add(int64_t T, int64_t cols, int type, const Side &x, const void *W, int
     return product_launch(c, sms, stream);
 }
 
-// For each adapter low^T . x over its tokens: rank x cols.
-int run_gradient(int64_t T, int type, const Side &x, ProductAdapters ad, void *low, void *out, int sms, cudaStream_t stream) {
+// For each adapter low^T . x over its tokens, rank x cols: dA from up and X, dB from low
+// and dY, in one launch where both are wanted.
+int run_gradients(int64_t T, int type, ProductAdapters ad, const Side &x, void *up, void *dA, const Side &g, void *low, void *dB,
+                  int sms, cudaStream_t stream) {
+    const Side &one = dA ? x : g;
     ProductCall c;
     c.mode = kModeGradient;
     c.epilogue = kEpiGradient;
     c.type = type;
-    c.I = x.cols;
+    c.I = one.cols;
     c.J = ad.rank;
     c.K = T;
-    c.plan = product_plan_gradient(ad.pitch, ad.count, x.cols, T, sms);
-    c.p = {x.p, x.cols, x.ld, 1};
+    c.plan = product_plan_gradient(ad.pitch, ad.count, one.cols + (dA && dB ? op_round_up(g.cols, 128) : 0), T, sms);
+    c.p = {one.p, one.cols, one.ld, 1};
     c.q.mn = 1;                                   // (low, from its own map)
-    ad.low = low;
     c.ad = ad;
-    c.C = out;
-    c.ldc = x.cols;
-    c.c_stride = ad.rank * x.cols;
+    c.ad.low = dA ? up : low;
+    c.C = dA ? dA : dB;
+    c.ldc = one.cols;
+    c.c_stride = ad.rank * one.cols;
+    if (dA && dB) {
+        c.two = true;
+        c.second = {g.p, g.cols, g.ld, 1};
+        c.second_k = g.cols;
+        c.ad2 = ad;
+        c.ad2.low = low;
+        c.C2 = dB;
+        c.ldc2 = g.cols;
+        c.c_stride2 = ad.rank * g.cols;
+    }
     c.epi.active = 1;
     c.epi.out = type;
     return product_launch(c, sms, stream);
@@ -361,7 +386,7 @@ int gemm_adapters(int64_t T, int64_t N, int64_t K, int dtype, const void *X, int
     if ((rc = workspace(&ws, bytes, dev, stream))) return rc;
     rc = pack_side(&x, T, static_cast<uint8_t *>(ws), stream);
     const Stack a = {"A", ad->A, K, ad->lda, ad->a_stride}, b = {"B", ad->B, N, ad->ldb, ad->b_stride};
-    if (rc == GEMM_OK) rc = run_low(T, type, x, a, pa, ws, sms, stream);
+    if (rc == GEMM_OK) rc = run_low(T, type, x, a, pa, ws, nullptr, nullptr, nullptr, sms, stream);
     if (rc == GEMM_OK) rc = run_add(T, N, type, x, W, ldw, w_major != 0, b, pa, ws, C, ldc, epi, sms, stream);
     const cudaError_t e = cudaFreeAsync(ws, stream);
     return rc ? rc : op_launched("cudaFreeAsync", e);
@@ -416,16 +441,19 @@ int gemm_adapters_backward(int64_t T, int64_t N, int64_t K, int dtype, const voi
     const Stack a = {"A", ad->A, K, ad->lda, ad->a_stride}, b = {"B", ad->B, N, ad->ldb, ad->b_stride};
     rc = pack_side(&g, T, base, stream);
     if (rc == GEMM_OK) rc = pack_side(&x, T, base, stream);
-    if (rc == GEMM_OK && want_up) rc = run_low(T, type, g, b, pa, up, sms, stream);
+    if (rc == GEMM_OK) {
+        if (want_up && want_low) rc = run_low(T, type, g, b, pa, up, &x, &a, low, sms, stream);
+        else rc = want_up ? run_low(T, type, g, b, pa, up, nullptr, nullptr, nullptr, sms, stream)
+                          : run_low(T, type, x, a, pa, low, nullptr, nullptr, nullptr, sms, stream);
+    }
     if (rc == GEMM_OK && dX && K > 0) {
         EpiParams epi;
         epi.active = 1;
         epi.out = type;
         rc = run_add(T, K, type, g, W, ldw, w_major == 0, a, pa, up, dX, lddx, epi, sms, stream);
     }
-    if (rc == GEMM_OK && da) rc = run_gradient(T, type, x, pa, up, dA, sms, stream);
-    if (rc == GEMM_OK && want_low) rc = run_low(T, type, x, a, pa, low, sms, stream);
-    if (rc == GEMM_OK && want_low) rc = run_gradient(T, type, g, pa, low, dB, sms, stream);
+    if (rc == GEMM_OK && (da || want_low))
+        rc = run_gradients(T, type, pa, x, up, da ? dA : nullptr, g, low, want_low ? dB : nullptr, sms, stream);
     const cudaError_t e = cudaFreeAsync(ws, stream);
     return rc ? rc : op_launched("cudaFreeAsync", e);
 }

@@ -84,6 +84,11 @@ struct ProductParams {
     uint32_t idesc, idesc_add; // of the operands, and of low x adapters
     void *C;
     int64_t ldc, c_stride;
+    // a second product (low, gradient): tiles from tiles_first on
+    int tiles_first, I2, num_kb2, tiles_i2;
+    void *C2;
+    int64_t ldc2, c_stride2;
+    int wide2;
     int wide, tma_store;       // C's rows start on 16 bytes; and end on them
     EpiParams epi;
     const float *alpha;
@@ -213,6 +218,7 @@ struct Tile {
     int kb0, kb1;
     int own;                   // where the operands' own K-blocks end and the adapters' begin
     bool none;                 // nothing to do: no slot reaches these lanes
+    bool second;               // of the launch's second product
     // K-blocks of the ring slot that begins with kb (never of both kinds).
     __device__ __forceinline__ int slot_blocks(int kb) const { return min(kSlotBlocks, (kb < own ? own : kb1) - kb); }
 };
@@ -225,9 +231,11 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank
     Tile T;
     T.e = T.g = T.slots = T.down = 0;
     T.none = false;
-    T.i1 = p.I;
+    T.second = SWAPPED && t >= p.tiles_first;
+    if (T.second) t -= p.tiles_first;
+    T.i1 = T.second ? p.I2 : p.I;
     T.j1 = p.J;
-    int total = p.num_kb, ranges = p.splits, range = crank;
+    int total = T.second ? p.num_kb2 : p.num_kb, ranges = p.splits, range = crank;
     if (p.mode == kModeLow) {
         // (the first lanes of every token tile first: most granules have few slots)
         const int ti = t / p.tiles_j;
@@ -238,8 +246,9 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int t, int crank
         T.i1 = T.slots << p.pitch_log2;
         T.none = T.i0 >= T.i1;
     } else if (p.mode == kModeGradient) {
-        T.e = t / p.tiles_i;
-        T.i0 = (t - T.e * p.tiles_i) * ROWS;
+        const int tiles_i = T.second ? p.tiles_i2 : p.tiles_i;
+        T.e = t / tiles_i;
+        T.i0 = (t - T.e * tiles_i) * ROWS;
         T.j0 = 0;
         total = min(max(__ldg(p.list_counts + T.e), 0), (int)p.granules) * p.granule_blocks;
     } else {
@@ -296,6 +305,8 @@ __device__ __forceinline__ float finish(const EpiParams &e, float acc, float bia
 __device__ __forceinline__ void write_four(const ProductParams &p, const Tile &T, int64_t cr, int64_t cc, float4 v,
                                            const float (&side)[4], int slot) {
     float y[4] = {v.x, v.y, v.z, v.w};
+    void *const C = T.second ? p.C2 : p.C;
+    const int64_t ldc = T.second ? p.ldc2 : p.ldc;
     if (p.mode == kModeLow) {
         // a token keeps the columns of its own slot (selected, not multiplied: what
         // another slot's product held, a NaN included, goes)
@@ -307,24 +318,24 @@ __device__ __forceinline__ void write_four(const ProductParams &p, const Tile &T
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 z[k] = y[k] - (p.f16 ? __half2float(__float2half_rn(y[k])) : __bfloat162float(__float2bfloat16_rn(y[k])));
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + p.rest + cr * p.ldc + cc) =
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(C) + p.rest + cr * ldc + cc) =
                 make_uint2(epi_pack2(p.epi.out, z[0], z[1]), epi_pack2(p.epi.out, z[2], z[3]));
         }
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = finish(p.epi, y[k], side[k]);
     }
-    const int64_t at = T.e * p.c_stride + cr * p.ldc + cc;
-    if (p.wide && cc + 4 <= T.i1) {
+    const int64_t at = T.e * (T.second ? p.c_stride2 : p.c_stride) + cr * ldc + cc;
+    if ((T.second ? p.wide2 : p.wide) && cc + 4 <= T.i1) {
         if (p.epi.out != GEMM_OUT_F32)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(C) + at) =
                 make_uint2(epi_pack2(p.epi.out, y[0], y[1]), epi_pack2(p.epi.out, y[2], y[3]));
         else
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4 *>(static_cast<float *>(C) + at) = make_float4(y[0], y[1], y[2], y[3]);
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (cc + k < T.i1) epi_store(p.C, at + k, p.epi.out, y[k]);
+            if (cc + k < T.i1) epi_store(C, at + k, p.epi.out, y[k]);
     }
 }
 
@@ -798,6 +809,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
 #pragma unroll
                 for (int u = 0; u < 8; ++u) ad[u] = __shfl_sync(0xffffffffu, mine, u);
                 const uint32_t bytes = (uint32_t)((boxes << p.pitch_log2) * 128 + Cf::Q_ROWS * 128);
+                // (the second product's maps are where this mode has no other use for them)
+                const CUtensorMap *const mq = T.second ? &tmP : &tmQ, *const ma = T.second ? &tmC : &tmAd;
                 for (int kb = T.kb0; kb < T.kb1 && next_slot(); kb += kSlotBlocks) {
                     const int n = T.slot_blocks(kb);
                     if (ptx::elect_one()) {
@@ -806,10 +819,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                         for (int s = 0; s < kSlotBlocks; ++s) {
                             if (s >= n) break;
                             const int k0 = (kb + s) * kBlockK;
-                            ptx::tma_load_2d(sq + s * Cf::BLOCK, &tmQ, fb, k0, j0);
+                            ptx::tma_load_2d(sq + s * Cf::BLOCK, mq, fb, k0, j0);
 #pragma unroll
                             for (int u = 0; u < 8; ++u)
-                                if (u < boxes) ptx::tma_load_3d<1>(sp + (uint32_t)(s * Cf::BLOCK + u * pitch * 128), &tmAd, fb, k0, 0, ad[u]);
+                                if (u < boxes) ptx::tma_load_3d<1>(sp + (uint32_t)(s * Cf::BLOCK + u * pitch * 128), ma, fb, k0, 0, ad[u]);
                         }
                     }
                     __syncwarp();
@@ -819,6 +832,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
             if constexpr (kGradient) {
                 // 64 tokens of a granule on the list at a time, and the adapter's slot in it
                 const int log2_blocks = 31 - __clz(p.granule_blocks);
+                const CUtensorMap *const mp = T.second ? &tmQ : &tmP, *const ml = T.second ? &tmAd : &tmLow;
                 WarpList list = {p.lists + T.e * p.granules, (T.kb1 + p.granule_blocks - 1) >> log2_blocks};
                 for (int kb = T.kb0; kb < T.kb1; kb += kSlotBlocks) {
                     const int n = T.slot_blocks(kb);
@@ -835,13 +849,13 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
 #pragma unroll
                         for (int s = 0; s < kSlotBlocks; ++s) {
                             if (s >= n) break;
-                            ptx::tma_load_2d(sp + s * Cf::BLOCK, &tmP, fb, i0, k0[s]);
-                            ptx::tma_load_2d(sp + s * Cf::BLOCK + kChunkBytes, &tmP, fb, i0 + 64, k0[s]);
+                            ptx::tma_load_2d(sp + s * Cf::BLOCK, mp, fb, i0, k0[s]);
+                            ptx::tma_load_2d(sp + s * Cf::BLOCK + kChunkBytes, mp, fb, i0 + 64, k0[s]);
 #pragma unroll
                             for (int c = 0; c < Cf::Q_CHUNKS; ++c) {
                                 const uint32_t to_q = sq + (uint32_t)(s * Cf::BLOCK + c * kChunkBytes);
-                                ptx::tma_load_3d<1>(to_q, &tmLow, fb, jx[s] + 64 * c, k0[s], 0);
-                                ptx::tma_load_3d<1>(to_q + Cf::Q_ONE, &tmLow, fb, jx[s] + 64 * c, k0[s], 1);
+                                ptx::tma_load_3d<1>(to_q, ml, fb, jx[s] + 64 * c, k0[s], 0);
+                                ptx::tma_load_3d<1>(to_q + Cf::Q_ONE, ml, fb, jx[s] + 64 * c, k0[s], 1);
                             }
                         }
                     }
@@ -1476,10 +1490,23 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     p.width = pl.width ? pl.width : pl.bn;
     int64_t ti = op_cdiv(c.I, kLanes * pl.cg), tj = op_cdiv(c.J, p.width);
     if (c.mode == kModeGradient) tj = ad.count;      // (an adapter's rank is one tile wide)
-    if (ti * tj * pl.splits * p.k_parts > kMax || (int64_t)p.k_parts * p.part_rows > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
+    p.tiles_first = 0x7fffffff;
+    int64_t more = 0;                                // tiles of the second product
+    if (c.two) {
+        p.tiles_first = (int)std::min<int64_t>(ti * tj, kMax);
+        p.num_kb2 = (int)op_cdiv(c.second_k, kBlockK);
+        p.I2 = (int)(c.mode == kModeLow ? c.I : c.second_k);
+        p.tiles_i2 = (int)op_cdiv(p.I2, kLanes);
+        p.C2 = c.C2;
+        p.ldc2 = c.ldc2;
+        p.c_stride2 = c.c_stride2;
+        p.wide2 = op_wide(c.C2, c.ldc2, 2) && (c.c_stride2 * 2) % 16 == 0;
+        more = p.tiles_i2 * tj;
+    }
+    if ((ti * tj * p.k_parts + more) * pl.splits > kMax || (int64_t)p.k_parts * p.part_rows > kMax) return api_error(GEMM_ERR_INVALID_ARG, "too many tiles");
     p.tiles_i = (int)ti;
     p.tiles_j = (int)tj;
-    p.num_tiles = (int)(ti * tj * p.k_parts);
+    p.num_tiles = (int)(ti * tj * p.k_parts + more);
     if (p.num_tiles == 0) return GEMM_OK;
     p.p_mn = c.p.mn;
     p.q_mn = c.q.mn;
@@ -1533,12 +1560,20 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     if (c.mode == kModeGradient) {
         rc = encode_operand(&m.p, c.p, c.type, c.K, kLanes);
         if (rc == GEMM_OK) rc = encode(&m.low, ad.low, c.type, c.K, low_cols, ad.ld_low, 64, both, ad.rest);
+        if (rc == GEMM_OK && more) {
+            rc = encode_operand(&m.q, c.second, c.type, c.K, kLanes);
+            if (rc == GEMM_OK) rc = encode(&m.ad, c.ad2.low, c.type, c.K, low_cols, ad.ld_low, 64, both, ad.rest);
+        }
     } else if (p.num_kb > 0) {
         if (c.mode != kModeLow) rc = encode_operand(&m.p, c.p, c.type, c.K, pl.p_rows);
         if (rc == GEMM_OK) rc = encode_operand(&m.q, c.q, c.type, c.K, p.width / pl.cg);
     }
     if (rc == GEMM_OK && c.mode == kModeLow && p.num_kb > 0)
         rc = encode(&m.ad, ad.p, c.type, ad.rank, ad.cols, ad.ld, ad.pitch, ad.count, ad.stride);
+    if (rc == GEMM_OK && c.mode == kModeLow && c.two && p.num_kb2 > 0) {
+        rc = encode_operand(&m.p, c.second, c.type, c.second_k, pl.bn);
+        if (rc == GEMM_OK) rc = encode(&m.c, c.ad2.p, c.type, ad.rank, c.ad2.cols, c.ad2.ld, ad.pitch, ad.count, c.ad2.stride);
+    }
     if (rc == GEMM_OK && c.mode == kModeAdd) {
         rc = encode(&m.ad, ad.p, c.type, ad.rank, ad.cols, ad.ld, std::min(ad.pitch, kBlockK), ad.count, ad.stride);
         if (rc == GEMM_OK)

@@ -106,6 +106,15 @@ struct ProductCall {
     const float *old = nullptr;            // FP32 sums to add (row-wise epilogue), pitch ld_old
     int64_t ld_old = 0;
     const float *alpha = nullptr;          // a factor on the device, on top of epi.alpha
+    // kModeLow and kModeGradient: a second product of the same kind in the same launch (the
+    // two sides of a backward pass): tokens' activations `second`, their width `second_k`;
+    // low: the adapters' other stack, `ad2.p`; both: C2 and its pitches.
+    bool two = false;
+    ProductOperand second;
+    int64_t second_k = 0;
+    ProductAdapters ad2;
+    void *C2 = nullptr;
+    int64_t ldc2 = 0, c_stride2 = 0;
     bool early = false;                    // the launch before this one, on this stream and from
                                            // the same entry, only makes `low`
 };
