@@ -62,7 +62,8 @@ GEMM_API int gemm_project_loss(int64_t T, int64_t V, int64_t D, int dtype, const
  * The vocabulary is taken in pieces: a piece's logits are computed again, their
  * gradient d is rounded to `dtype` (with FP16 scaled by a power of two so that the
  * largest fits and the small ones keep their digits) and goes into both products;
- * dH is summed over the pieces in FP32.  A token without a label adds nothing,
+ * dH is summed over the pieces in FP32.  What rounding takes from a row's largest
+ * entry, the label's, is added back in FP32 (to dW for up to 65536 tokens).  A token without a label adds nothing,
  * whatever H[t] and grad[t] hold, and gets a zero row in dH (W must be finite).
  *
  *   grad         T floats, grad_stride (0: one value for all, or 1) apart

@@ -151,7 +151,7 @@ def check_loss(H, W, y, grad=None, **how):
 
 @pytest.mark.parametrize("dtype", (BF16, F16))
 @pytest.mark.parametrize("layout", ("vd", "dv", "padded"))
-@pytest.mark.parametrize("T,V,D", [(1, 1, 8), (1, 1000, 64), (2, 129, 1), (17, 257, 72), (33, 1000, 77), (64, 64, 64),
+@pytest.mark.parametrize("T,V,D", [(1, 1, 8), (1, 1000, 64), (1, 300, 77), (2, 129, 1), (17, 257, 72), (33, 1000, 77), (64, 64, 64),
                                    (127, 513, 130), (130, 255, 520), (300, 1111, 263), (257, 2049, 1032)])
 def test_loss_and_its_gradients(T, V, D, layout, dtype):
     H, W, y = made_loss(T, V, D, dtype, layout, seed=T)
@@ -184,9 +184,12 @@ def test_loss_variants(how, dtype):
     check_loss(H, W, y, randn(200, seed=8), **how)
 
 
+@pytest.mark.parametrize("layout", ("vd", "dv"))
+@pytest.mark.parametrize("bn", (0, 128))
 @pytest.mark.parametrize("T", (1, 3, 8, 16, 31, 32, 33, 200))       # few tokens: tiles of any width
-def test_loss_of_few_tokens(T):
-    H, W, y = made_loss(T, 50021, 320, BF16, seed=T)
+def test_loss_of_few_tokens(T, bn, layout):
+    tg.gemm_set_option("product_bn", bn)
+    H, W, y = made_loss(T, 50021, 320, BF16, layout, seed=T)
     check_loss(H, W, y)
 
 
@@ -415,7 +418,7 @@ def test_adapters_in_any_order(T, L, order):
 
 
 @pytest.mark.parametrize("K,N", [(1, 1), (1, 300), (300, 1), (63, 65), (77, 129), (1001, 130), (130, 1001)])
-@pytest.mark.parametrize("T", (3, 130, 530))
+@pytest.mark.parametrize("T", (1, 3, 130, 530))
 def test_adapters_of_odd_sizes(T, K, N):
     X, W, A, B, ids, s = made_adapters(T, K, N, 12, 3, F16, seed=K)
     check_adapters(X, W, A, B, ids, s, randn(T, N, seed=96).to(F16))

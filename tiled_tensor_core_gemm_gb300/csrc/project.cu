@@ -1402,8 +1402,8 @@ int64_t product_parts(const ProductPlan &plan, int64_t cols) {
 // Tile of a product with the tokens (or whatever else there is much of) on the
 // lanes, and (most_parts > 1) into how many K ranges its tiles go, by the rounds of
 // tiles and a tile's pace, in us: 0.27 a K-block of a 256 x 256 pair (its MMAs) and
-// 0.3 of 128 x 128 (its operands from L2), and what does not overlap at a tile's
-// ends.  K ranges are for few tiles over a long K; their FP32 sums are written and
+// 0.3 of 128 x 128 (its operands from L2), and 7 and 4 around the first and last tile
+// (1000 x 1016 x 2056: 20.4 us in 16 pair tiles, 64 of 128 x 128 finish earlier).  K ranges are for few tiles over a long K; their FP32 sums are written and
 // read again.
 ProductPlan product_plan_rows(int64_t I, int64_t J, int64_t K, int sms, int most_parts) {
     const int64_t kb = op_cdiv(K, kBlockK);
@@ -1416,7 +1416,7 @@ ProductPlan product_plan_rows(int64_t I, int64_t J, int64_t K, int sms, int most
         for (int parts = 1; parts <= most_parts; ++parts) {
             if (parts > 1 && (kb < 8 * parts || (double)parts * I * J > 3.2e7)) break;
             const double rounds = (double)op_cdiv(tiles * parts, sms / cg);
-            const double cost = rounds * (op_cdiv(kb, parts) * (cg == 2 ? 0.27 : 0.3) + (cg == 2 ? 2. : 1.5)) +
+            const double cost = rounds * (op_cdiv(kb, parts) * (cg == 2 ? 0.27 : 0.3) + 0.4) + (cg == 2 ? 7. : 4.) +
                                 (parts > 1 ? 4. + (double)parts * I * J * 8. / 5e6 : 0.);
             if (best.bn && cost >= least) continue;
             least = cost;
@@ -1433,11 +1433,17 @@ ProductPlan product_plan_rows(int64_t I, int64_t J, int64_t K, int sms, int most
 // columns on 76 pairs are 2.6 rounds run as 3; of 224 columns 2.9).
 ProductPlan product_plan_stats(int64_t tokens, int64_t vocab, int64_t K, bool any, int sms) {
     ProductPlan pl = product_plan_rows(tokens, vocab, K, sms);
+    const int forced = options_snapshot().product_bn;
+    if (tokens <= 32 && forced != 128) {
+        // (their ring holds nearly nothing but W: 5 x 50021 x 2048 42 us, in 128 columns 58)
+        pl.bn = 256;
+        pl.cg = 2;
+        pl.p_rows = 32;
+    }
     if (!any || tokens > 256) return pl;
     const int64_t units = sms / pl.cg, rounds = op_cdiv(op_cdiv(vocab, pl.bn), units);
     const int64_t width = op_round_up(op_cdiv(vocab, rounds * units), 32);
     pl.width = (int)std::min<int64_t>(std::max<int64_t>(width, pl.bn / 2 + 32), pl.bn);
-    if (tokens <= 32 && pl.cg == 2) pl.p_rows = 32;
     return pl;
 }
 
