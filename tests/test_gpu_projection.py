@@ -548,10 +548,11 @@ def test_adapters_small_integers_are_exact():
         assert torch.equal(got.double(), want)
 
 
-def test_adapters_past_32_bits():
-    # C and the rank-wide activations pass 2^31 elements
-    T, N, L, r = 70000, 31000, 260, 128
-    X, W, A, B, ids, s = made_adapters(T, 64, N, r, L, BF16, seed=13)
+@pytest.mark.parametrize("K,N", [(64, 31000), (22000, 64)])
+def test_adapters_past_32_bits(K, N):
+    # C and the rank-wide activations pass 2^31 elements; a wide K makes the latter long work, whose end is waited for
+    T, L, r = 70000, 260, 128
+    X, W, A, B, ids, s = made_adapters(T, K, N, r, L, BF16, seed=13)
     plan = tg.adapter_plan(ids, L)
     C = tg.gemm_adapters(X, W, A, B, plan, s)
     at = torch.tensor([0, 1, 255, 256, 34634, 34635, 69275, 69999], device="cuda")

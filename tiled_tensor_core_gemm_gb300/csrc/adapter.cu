@@ -244,7 +244,9 @@ int run_add(int64_t T, int64_t cols, int type, const Side &x, const void *W, int
     c.C = C;
     c.ldc = ldc;
     c.epi = epi;
-    c.early = true;
+    // (where low takes long its end is waited for first: the waits behind an early start
+    // are bounded)
+    c.early = (double)T * (double)ad.ld_low * (double)x.cols < 5e13;
     return product_launch(c, sms, stream);
 }
 
