@@ -712,3 +712,20 @@ def test_loss_past_32_bits():
     exact = d[:, at].t() @ H.double()
     bound = (U[BF16] * 2 + 1.5e-3) * (d[:, at].abs().t() @ H.double().abs()) + U[BF16] * exact.abs()
     within(dW[at], exact, bound, "dW")
+
+
+@pytest.mark.parametrize("dtype", (BF16, F16))
+@pytest.mark.parametrize("T", (1, 20, 32, 33, 200))
+def test_adapters_of_a_token_with_an_infinity_are_infinite(T, dtype):
+    # every factor positive: inf and nothing that could cancel it, whichever way low is held
+    X, W, A, B, ids, s = made_adapters(T, 72, 88, 16, 3, dtype, seed=61)
+    X, W, A, B, ids = X.abs() + 0.1, W.abs() + 0.01, A.abs() + 0.01, B.abs() + 0.01, ids.clamp_min(0)
+    dY = randn(T, 88, seed=62).abs().to(dtype) + 0.1
+    plan = tg.adapter_plan(ids, 3, backward=True)
+    want = tg.gemm_adapters(X, W, A, B, plan, s), tg.gemm_adapters_backward(dY, X, W, A, B, plan, s, want_adapters=False)[0]
+    t = min(T - 1, 5)
+    X[t, 3], dY[t, 7] = float("inf"), float("inf")
+    got = tg.gemm_adapters(X, W, A, B, plan, s), tg.gemm_adapters_backward(dY, X, W, A, B, plan, s, want_adapters=False)[0]
+    keep = torch.arange(T, device="cuda") != t
+    for g, w in zip(got, want):
+        assert bool((g[t] == float("inf")).all()) and torch.equal(g[keep], w[keep])

@@ -300,6 +300,13 @@ __device__ __forceinline__ float finish(const EpiParams &e, float acc, float bia
     return y;
 }
 
+// What rounding x to the operands' type takes from it; nothing where the rounded value is
+// not finite (an infinity has no rest: inf - inf would make its row NaN).
+__device__ __forceinline__ float rest_of(const ProductParams &p, float x) {
+    const float r = x - (p.f16 ? __half2float(__float2half_rn(x)) : __bfloat162float(__float2bfloat16_rn(x)));
+    return fabsf(r) < INFINITY ? r : 0.f;
+}
+
 // Four neighbouring columns of row cr of C.  `side`: the bias of each, or (low)
 // the factor of their slot's adapter; `slot`: (low) the token's.
 __device__ __forceinline__ void write_four(const ProductParams &p, const Tile &T, int64_t cr, int64_t cc, float4 v,
@@ -316,8 +323,7 @@ __device__ __forceinline__ void write_four(const ProductParams &p, const Tile &T
         if (p.rest) {
             float z[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                z[k] = y[k] - (p.f16 ? __half2float(__float2half_rn(y[k])) : __bfloat162float(__float2bfloat16_rn(y[k])));
+            for (int k = 0; k < 4; ++k) z[k] = rest_of(p, y[k]);
             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(C) + p.rest + cr * ldc + cc) =
                 make_uint2(epi_pack2(p.epi.out, z[0], z[1]), epi_pack2(p.epi.out, z[2], z[3]));
         }
@@ -1193,7 +1199,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                             float d = 0.f;
 #pragma unroll
                             for (int c = 0; c < 64; ++c) d = c == (int)rel ? v[c] : d;
-                            d -= p.f16 ? __half2float(__float2half_rn(d)) : __bfloat162float(__float2bfloat16_rn(d));
+                            d = rest_of(p, d);
                             p.rests_out[i] = d;
                             if (p.rests_ordered) p.rests_ordered[__float_as_int(info.w) - 1] = d;
                         }
