@@ -729,3 +729,20 @@ def test_adapters_of_a_token_with_an_infinity_are_infinite(T, dtype):
     keep = torch.arange(T, device="cuda") != t
     for g, w in zip(got, want):
         assert bool((g[t] == float("inf")).all()) and torch.equal(g[keep], w[keep])
+
+
+def test_adapters_with_a_short_limit_on_waits():
+    # low alone takes more than the limit (7e11 multiply-adds over the slots in use, 1.6 ms and more): the
+    # projection's waits must not begin before it ends
+    X, W, A, B, ids, s = made_adapters(8192, 4096, 256, 128, 256, BF16, seed=64)
+    plan = tg.adapter_plan(ids, 256)
+    want = tg.gemm_adapters(X, W, A, B, plan, s)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert tg.gemm_get_status(stream) == tg.GEMM_OK
+    assert tg.gemm_set_option("wait_timeout_ms", 1) == 0
+    try:
+        got = tg.gemm_adapters(X, W, A, B, plan, s)
+        assert tg.gemm_get_status(stream) == tg.GEMM_OK, tg.gemm_last_error()
+    finally:
+        tg.gemm_set_option("wait_timeout_ms", 2000)
+    assert torch.equal(got, want)

@@ -216,9 +216,10 @@ int run_low(int64_t T, int type, const Side &x, const Stack &stack, ProductAdapt
     return product_launch(c, sms, stream);
 }
 
-// C = act(x . W + low x stack + bias).  w_k_major: W's rows are the columns of C.
+// C = act(x . W + low x stack + bias).  w_k_major: W's rows are the columns of C.  low_k: what
+// the launch that makes low sums over, its two products' lengths together.
 int run_add(int64_t T, int64_t cols, int type, const Side &x, const void *W, int64_t ldw, bool w_k_major, const Stack &stack,
-            ProductAdapters ad, void *low, void *C, int64_t ldc, const EpiParams &epi, int sms, cudaStream_t stream) {
+            ProductAdapters ad, void *low, int64_t low_k, void *C, int64_t ldc, const EpiParams &epi, int sms, cudaStream_t stream) {
     ProductCall c;
     c.mode = kModeAdd;
     c.type = type;
@@ -244,9 +245,10 @@ int run_add(int64_t T, int64_t cols, int type, const Side &x, const void *W, int
     c.C = C;
     c.ldc = ldc;
     c.epi = epi;
-    // (where low takes long its end is waited for first: the waits behind an early start
-    // are bounded)
-    c.early = (double)T * (double)ad.ld_low * (double)x.cols < 5e13;
+    // Where low may take long its end is waited for first: the MMAs' wait for a slot of it is
+    // bounded by the option.  At 64 x 128 x 64 multiply-adds in 0.18 us an SM (project.cu) the
+    // rule gives low's launch a seventeenth of the limit.
+    c.early = (double)T * (double)ad.ld_low * (double)low_k < 2.5e10 * options_snapshot().wait_timeout_ms;
     return product_launch(c, sms, stream);
 }
 
@@ -389,7 +391,7 @@ int gemm_adapters(int64_t T, int64_t N, int64_t K, int dtype, const void *X, int
     rc = pack_side(&x, T, static_cast<uint8_t *>(ws), stream);
     const Stack a = {"A", ad->A, K, ad->lda, ad->a_stride}, b = {"B", ad->B, N, ad->ldb, ad->b_stride};
     if (rc == GEMM_OK) rc = run_low(T, type, x, a, pa, ws, nullptr, nullptr, nullptr, sms, stream);
-    if (rc == GEMM_OK) rc = run_add(T, N, type, x, W, ldw, w_major != 0, b, pa, ws, C, ldc, epi, sms, stream);
+    if (rc == GEMM_OK) rc = run_add(T, N, type, x, W, ldw, w_major != 0, b, pa, ws, K, C, ldc, epi, sms, stream);
     const cudaError_t e = cudaFreeAsync(ws, stream);
     return rc ? rc : op_launched("cudaFreeAsync", e);
 }
@@ -452,7 +454,7 @@ int gemm_adapters_backward(int64_t T, int64_t N, int64_t K, int dtype, const voi
         EpiParams epi;
         epi.active = 1;
         epi.out = type;
-        rc = run_add(T, K, type, g, W, ldw, w_major == 0, a, pa, up, dX, lddx, epi, sms, stream);
+        rc = run_add(T, K, type, g, W, ldw, w_major == 0, a, pa, up, N + (want_low ? K : 0), dX, lddx, epi, sms, stream);
     }
     if (rc == GEMM_OK && (da || want_low))
         rc = run_gradients(T, type, pa, x, up, da ? dA : nullptr, g, low, want_low ? dB : nullptr, sms, stream);
