@@ -746,3 +746,105 @@ def test_adapters_with_a_short_limit_on_waits():
     finally:
         tg.gemm_set_option("wait_timeout_ms", 2000)
     assert torch.equal(got, want)
+
+
+# What the rounding of d takes from its label entries and the products give back.  In the inputs below it is all
+# there is: W's rows are alike within groups of 1 / p entries, the logits far lower outside a token's own group
+# (sums exact in FP32: multiples of 2^-5 below 2^8), so d is grad p, exact in the type, but for the label's
+# -grad (1 - p), and dH is 0.  Tokens come in pairs of one label, H = 1.5 h with grad = c and H = h with
+# grad = -1.5 c, c a power of two: dW is 0 too.  1 - p has as many digits as the type, 1.5 (1 - p) one and a half
+# more: a quarter of a step of its last digit goes, 2^-9 c (bf16) or 2^-12 c (fp16).
+GROUP = {BF16: 256, F16: 2048}
+
+
+def made_cancelling(runs, dtype, layout, seed, tokens=None):
+    """Pairs by label, in a random order; tokens beyond them (up to `tokens`) do not count.  runs: pairs of each label."""
+    size, groups, content = GROUP[dtype], 4, 24
+    V, n = size * groups, len(runs)
+    of = torch.arange(V, device="cuda") // size
+    own = randint(0, 2, groups * content, seed=seed).view(groups, content) * 2 - 1
+    W = torch.zeros(V, content + groups, device="cuda")
+    W[:, :content] = (own * (0.5 + 0.5 * randint(0, 2, groups * content, seed=seed + 1).view(groups, content)))[of]
+    W[torch.arange(V, device="cuda"), content + of] = 1.0
+    labels = torch.randperm(V, generator=torch.Generator().manual_seed(seed))[:n].cuda()
+    pair_label = labels.repeat_interleave(torch.tensor(runs, device="cuda"))
+    pairs = len(pair_label)
+    h = torch.zeros(pairs, content + groups, device="cuda")
+    h[:, :content] = randint(-8, 9, pairs * content, seed=seed + 2).view(pairs, content) / 8.0
+    h[torch.arange(pairs, device="cuda"), content + of[pair_label]] = 64.0
+    c = 2.0 ** -randint(0, 3, pairs, seed=seed + 3).float()
+    T = max(tokens or 0, 2 * pairs)
+    H, g, y = torch.full((T, h.shape[1]), float("nan"), device="cuda"), torch.ones(T, device="cuda"), torch.full((T,), -100, device="cuda")
+    at = torch.randperm(T, generator=torch.Generator().manual_seed(seed + 1))[:2 * pairs].cuda()
+    H[at], g[at], y[at] = torch.cat((1.5 * h, h)), torch.cat((c, -1.5 * c)), torch.cat((pair_label, pair_label))
+    W = W.to(dtype)
+    return H.to(dtype), W.t().contiguous().t() if layout == "dv" else W, y, g
+
+
+def check_cancelling(H, W, y, g):
+    """dH and dW against 0, within FP32's error (a logit is exact, lse off by 2^-20 + 4 * 2^-24 |lse|, so p by
+    twice that; d at the label by 2^-22 |grad| besides; products 1e-5 of the sum of magnitudes); and that the same
+    without the labels' rests would be outside."""
+    dtype = H.dtype
+    _, lse = tg.project_loss(H, W, y)
+    dH, dW = tg.project_loss_backward(g, H, W, y, lse)
+    at = (y >= 0).nonzero()[:, 0]
+    assert not bool(dH[y < 0].any())
+    h, w, gg, yy, n = H[at].double(), W.double(), g[at].double(), y[at], torch.arange(len(at), device="cuda")
+    dH_off, dW_off, dW_bound, dW_without = dH[at].double(), dW.double(), torch.zeros_like(w), torch.zeros_like(w)
+    caught, tokens = 0, 0
+    for s in range(0, len(at), 4096):
+        m = slice(s, s + 4096)
+        i = n[:len(yy[m])]
+        z = h[m] @ w.t()
+        l64 = torch.logsumexp(z, 1)
+        p = torch.exp(z - l64[:, None])
+        d = gg[m, None] * p
+        d[i, yy[m]] -= gg[m]
+        rounded = d.to(dtype).double() if dtype is BF16 else (d * 2.0 ** 12).to(dtype).double() * 2.0 ** -12
+        e = gg[m].abs() * (2.0 ** -22 + p[i, yy[m]] * (2.0 ** -19 + 2.0 ** -21 * l64.abs()))
+        beyond = torch.where(torch.arange(len(w), device="cuda") // GROUP[dtype] == (yy[m] // GROUP[dtype])[:, None], 0.0, 2 * d.abs())
+        bound = e[:, None] * w[yy[m]].abs() + 1e-5 * (d.abs() @ w.abs()) + beyond @ w.abs() + TINY[dtype]
+        assert float((dH_off[m].abs() - bound).max()) <= 0, "dH"
+        wide = (gg[m] < 0)[:, None] & (w[yy[m]] != 0)
+        caught += int(((rounded @ w).abs() > bound)[wide].sum())
+        tokens += int(wide.sum())
+        dW_bound += 1e-5 * (d.abs().t() @ h[m].abs()) + beyond.t() @ h[m].abs()
+        dW_bound.index_add_(0, yy[m], e[:, None] * h[m].abs())
+        dW_without += rounded.t() @ h[m]
+    assert caught == tokens
+    dW_bound += TINY[dtype]
+    assert float((dW_off.abs() - dW_bound).max()) <= 0, "dW"
+    used = torch.unique(yy)
+    # (rows of several pairs may cancel in a column by chance)
+    outside = (dW_without.abs() > dW_bound)[used].any(1)
+    assert bool(outside.all())
+
+
+@pytest.mark.parametrize("columns", (0, 512))
+@pytest.mark.parametrize("layout", ("vd", "dv"))
+@pytest.mark.parametrize("dtype", (BF16, F16))
+def test_loss_gradients_lose_nothing_of_their_label_entries(dtype, layout, columns):
+    tg.gemm_set_option("loss_columns", columns)
+    check_cancelling(*made_cancelling([1] * 60 + list(range(2, 40)), dtype, layout, seed=70))
+
+
+@pytest.mark.parametrize("layout", ("vd", "dv"))
+@pytest.mark.parametrize("dtype", (BF16, F16))
+@pytest.mark.parametrize("pairs", (1, 15, 16, 17, 40, 3000, 20000))
+def test_loss_gradients_where_all_tokens_have_one_label(pairs, dtype, layout):
+    check_cancelling(*made_cancelling([pairs], dtype, layout, seed=71))
+
+
+def test_loss_gradient_of_the_tokens_past_32_bits():
+    # dH passes 2^31 elements, W's rows are gathered by label for its rests; checked at both ends and in the middle
+    T, V, D = 65600, 300, 33000
+    H, W = torch.empty((T, D), dtype=BF16, device="cuda"), (randn(V, D, seed=1) * D ** -0.5).to(BF16)
+    for t in range(0, T, 8200):
+        H[t:t + 8200] = randn(8200, D, seed=t)
+    y, g = randint(0, V, T, seed=2), randn(T, seed=3)
+    _, lse = tg.project_loss(H, W, y)
+    dH, _ = tg.project_loss_backward(g, H, W, y, lse, want_W=False)
+    at = torch.tensor([0, 1, 32800, 65074, 65075, 65076, T - 2, T - 1], device="cuda")
+    want = exact_loss(H[at], W, y[at], g[at])["dH"]
+    within(dH[at], *want, "dH")
