@@ -109,7 +109,7 @@ struct ProductParams {
     float2 *parts;
     float *sums, *hits;
     const float4 *rows;
-    float *rests_out, *rests_ordered;
+    float *rests_out;
     ProductRests rests;
     int f16;                   // the operands' type
     int early, debug_stall;
@@ -1172,7 +1172,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                 if constexpr (EPI == kEpiDlogits) {
                     if (steps && i < T.i1) {
                         info = __ldg(p.rows + i);
-                        if (__float_as_int(info.w) != 0) label = label_column(p, i);
+                        if (info.w != 0.f) label = label_column(p, i);
                     }
                 }
 #pragma unroll 1
@@ -1189,9 +1189,9 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                     if constexpr (EPI == kEpiDlogits) {
                         const int64_t rel = label - j;
                         // (a row without a label gives nothing, whatever its logits are)
-                        if (__any_sync(0xffffffffu, __float_as_int(info.w) != 0))
+                        if (__any_sync(0xffffffffu, info.w != 0.f))
                             take_gradient(p, v, info, rel >= 0 && rel < 64 ? (int)rel : -1);
-                        if (__float_as_int(info.w) == 0) {
+                        if (info.w == 0.f) {
 #pragma unroll
                             for (int c = 0; c < 64; ++c) v[c] = 0.f;
                         }
@@ -1201,7 +1201,6 @@ product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
                             for (int c = 0; c < 64; ++c) d = c == (int)rel ? v[c] : d;
                             d = rest_of(p, d);
                             p.rests_out[i] = d;
-                            if (p.rests_ordered) p.rests_ordered[__float_as_int(info.w) - 1] = d;
                         }
                     } else {
                         if constexpr (EPI == kEpiRests) {
@@ -1555,7 +1554,6 @@ int product_launch(const ProductCall &c, int sms, cudaStream_t stream) {
     p.hits = c.loss.hits;
     p.rows = c.loss.rows;
     p.rests_out = c.loss.rests;
-    p.rests_ordered = c.loss.rests_ordered;
     p.rests = c.rests;
     p.f16 = c.type == GEMM_OUT_F16;
     p.eps_v = c.loss.eps_v;

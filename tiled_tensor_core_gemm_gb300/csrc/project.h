@@ -45,17 +45,16 @@ struct ProductLoss {
     float2 *parts = nullptr;   // [part][token]: maximum (in base 2) and sum of the exponentials
     float *sums = nullptr;     // [part][token]
     float *hits = nullptr;     // [token]: the label's logit
-    const float4 *rows = nullptr;   // [token]: lse in base 2, two factors (loss.cu), and as bits 0 for one
-                                    // that does not count, else its place in the order of the labels + 1
+    const float4 *rows = nullptr;   // [token]: lse in base 2, two factors (loss.cu), and 0 for one that
+                                    // does not count, else 1
     float *rests = nullptr;         // [token]: what rounding took from the label's gradient
-    float *rests_ordered = nullptr; // the same by place, or nullptr
 };
 
 // The label entries of d are by far its largest, so their rounding would be nearly all
 // of the gradients' error.  What it took (`rests`) is added back in FP32 where the
 // products that read d are written: to dH the token's rest times its label's row of W,
 // to dW the sum over the tokens that have the label of their rests times their rows of
-// H (loss.cu: loss_rests).
+// H (loss.cu: loss_rests, loss_rests_join).
 struct ProductRests {
     int kind = 0;                   // 1: lanes are tokens; 2: lanes, 3: columns are the vocabulary
     int64_t ld = 0;
