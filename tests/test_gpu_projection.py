@@ -818,7 +818,9 @@ def check_cancelling(H, W, y, g):
     used = torch.unique(yy)
     # (rows of several pairs may cancel in a column by chance)
     outside = (dW_without.abs() > dW_bound)[used].any(1)
-    assert bool(outside.all())
+    # Of 70000 tokens that count a group has 17500, whose p of 2^-8 make the bound 1e-5 * 17500 * 1.25 * 2^-8 |h| =
+    # 8.5e-4 |h|: a single pair's rest, 2^-9 c |h|, is outside for c = 1, a third of them.
+    assert bool(outside.all()) if len(at) <= 40000 else float(outside.double().mean()) > 0.25
 
 
 @pytest.mark.parametrize("columns", (0, 512))
@@ -855,6 +857,37 @@ def test_loss_gradient_takes_no_longer_where_all_tokens_have_one_label():
         return min(took)
     mixed = least(y)
     assert least(one) < 2 * mixed
+
+
+@pytest.mark.parametrize("labels", (torch.int64, torch.int32))
+@pytest.mark.parametrize("tokens,pairs", [(4096, 2000), (4097, 2000), (70000, 4000), (70001, 35000), (200000, 900)])
+def test_loss_gradients_lose_nothing_with_many_tokens(tokens, pairs, labels):
+    # most of them do not count; labels of one pair and of many
+    runs = [1] * 400 + [pairs // 4] + [2] * 100 + [pairs - 600 - pairs // 4]
+    H, W, y, g = made_cancelling(runs, BF16, "vd", seed=73, tokens=tokens)
+    check_cancelling(H, W, y.to(labels), g)
+
+
+def test_loss_gradients_of_many_tokens_do_not_depend_on_how_they_are_ordered():
+    # 4096 tokens are ordered by comparisons, with one more that does not count by passes over the labels' bits
+    # (over a vocabulary of three such passes)
+    T, V, D = 4096, 66000, 40
+    H, W, y = made_loss(T, V, D, BF16, seed=74)
+    y[::3] = 7
+    g = randn(T, seed=75)
+    _, lse = tg.project_loss(H, W, y)
+    want = tg.project_loss_backward(g, H, W, y, lse)[1]
+    more = lambda t, v: torch.cat((t[:100], t.new_full((1, *t.shape[1:]), v), t[100:]))       # noqa: E731
+    H2, y2, g2, lse2 = more(H, 1.0), more(y, -1), more(g, 1.0), more(lse, 0.0)
+    got = tg.project_loss_backward(g2, H2, W, y2, lse2)[1]
+    # FP32 sums in another grouping (1e-5 of their magnitudes, over all 4096 tokens under 1e-5 * 4096 * |H|), and
+    # one rounding: half a step of the larger
+    off = (got.double() - want.double()).abs()
+    p = torch.exp(H.double() @ W[:64].double().t() - lse.double()[:, None])
+    p[torch.arange(T, device="cuda"), y.clamp(0, 63)] += ((y >= 0) & (y < 64)).double()
+    d = torch.where((y >= 0)[:, None], g.double().abs()[:, None] * p, 0.0)
+    bound = 2 * (1e-5 * (d.t() @ H.double().abs()) + U[BF16] * torch.maximum(got[:64].abs(), want[:64].abs()).double())
+    assert float((off[:64] - bound).max()) <= 0
 
 
 def test_loss_gradient_of_the_tokens_past_32_bits():

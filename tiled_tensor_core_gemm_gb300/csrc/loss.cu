@@ -23,13 +23,24 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kFinishWarps = 16;
+// Up to here loss_rows orders the tokens by their labels in T^2 comparisons, beyond order_place
+// does in passes over the labels' bits.  A whole dW of 8 columns over 8000 labels (two passes),
+// comparing and in passes: 2048 tokens 54 and 64 us, 4096 80 and 81, 8192 137 and 128, 65536
+// 2641 and 1605; over 131072 labels (three) 4096 take 711 and 712.
+constexpr int64_t kCountTokens = 4096;
+constexpr int kOrderBlocks = 128;
 constexpr int kRun = 32;         // places in the order of the labels that a block of loss_rests takes
 constexpr int kJoinRuns = 8;     // blocks of loss_rests that one of loss_rests_join looks at
 
-__device__ __forceinline__ bool counted(const void *labels, int label_bytes, int64_t t, int64_t V) {
+// Token t's label, V for one that does not count.
+__device__ __forceinline__ int label_key(const void *labels, int label_bytes, int64_t t, int64_t V) {
     const int64_t y = label_bytes == 8 ? __ldg(static_cast<const long long *>(labels) + t)
                                        : (int64_t)__ldg(static_cast<const int32_t *>(labels) + t);
-    return y >= 0 && y < V;
+    return y >= 0 && y < V ? (int)y : (int)V;
+}
+
+__device__ __forceinline__ bool counted(const void *labels, int label_bytes, int64_t t, int64_t V) {
+    return label_key(labels, label_bytes, t, V) < (int)V;
 }
 
 // Joins a row's (maximum, sum) with another's.
@@ -116,10 +127,83 @@ loss_scale(int64_t T, int64_t V, const float *__restrict__ grad, int64_t grad_st
     }
 }
 
+// The tokens in the order of their labels, where counting takes too many comparisons: eight
+// bits of the labels at a time from the lowest, each pass stable.  A block takes `per`
+// neighbouring tokens.  order_count: how many of them have each digit.
+struct OrderKeys {
+    const void *labels;            // the first pass: the labels themselves
+    int label_bytes;
+    int64_t V;
+    const int32_t *keys, *tokens;  // or what the last pass left
+    __device__ __forceinline__ int key(int64_t k) const { return keys ? __ldg(keys + k) : label_key(labels, label_bytes, k, V); }
+};
+
+__global__ void __launch_bounds__(256)
+order_count(int64_t T, int64_t per, int shift, OrderKeys in, int32_t *counts) {
+    pdl_enter();
+    __shared__ int count[256];
+    count[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t end = min(T, (blockIdx.x + 1) * per);
+    for (int64_t k = blockIdx.x * per + threadIdx.x; k < end; k += 256) atomicAdd(&count[in.key(k) >> shift & 255], 1);
+    __syncthreads();
+    counts[blockIdx.x * 256 + threadIdx.x] = count[threadIdx.x];
+}
+
+// A token's place: behind those of lower digits, those of its digit in blocks before, and
+// those before it in its own block, 256 tokens at a time.
+__global__ void __launch_bounds__(256)
+order_place(int64_t T, int64_t per, int shift, OrderKeys in, const int32_t *__restrict__ counts, int32_t *keys_out, int32_t *tokens_out) {
+    pdl_enter();
+    __shared__ int seen[8][256], sums[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int all = 0, next = 0;                       // with this thread's digit: everywhere; then the place of the next
+#pragma unroll 16
+    for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int n = __ldg(counts + b * 256 + (int)threadIdx.x);
+        all += n;
+        next += b < (int)blockIdx.x ? n : 0;
+    }
+    int up = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, up, d);
+        if (lane >= d) up += x;
+    }
+    if (lane == 31) sums[warp] = up;
+    __syncthreads();
+    next += up - all;
+    for (int w = 0; w < warp; ++w) next += sums[w];
+    const int64_t end = min(T, (blockIdx.x + 1) * per);
+    for (int64_t k0 = blockIdx.x * per; k0 < end; k0 += 256) {
+        const int64_t k = k0 + threadIdx.x;
+        const bool live = k < end;
+        const int key = live ? in.key(k) : 0, digit = live ? key >> shift & 255 : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        for (int d = lane; d < 256; d += 32) seen[warp][d] = 0;
+        __syncwarp();
+        if (live && rank == 0) seen[warp][digit] = __popc(same);
+        __syncthreads();
+        for (int w = 0; w < 8; ++w) {
+            const int n = seen[w][threadIdx.x];
+            seen[w][threadIdx.x] = next;
+            next += n;
+        }
+        __syncthreads();
+        if (live) {
+            const int at = seen[warp][digit] + rank;
+            keys_out[at] = key;
+            tokens_out[at] = in.tokens ? __ldg(in.tokens + k) : (int)k;
+        }
+        __syncwarp();
+    }
+}
+
 // Per token: what the logits' gradient takes (project.cu: take_gradient): lse in base 2,
-// grad (1 + 2 a lse), grad, and whether the token counts; the tokens in the order of the
-// labels (ties in the order of the tokens, tokens that do not count last), each by counting
-// the labels before its own, with `index` cleared; and H's row, at a pitch TMA can address, zero for a token
+// grad (1 + 2 a lse), grad, and whether the token counts; with `sorted` the tokens in
+// the order of the labels (ties in the order of the tokens, tokens that do not count last),
+// each by counting the labels before its own; `index` cleared; and H's row, at a pitch TMA can address, zero for a token
 // that does not count, so that nothing it holds (padding may be anything) reaches dW as
 // 0 x NaN.  With W (held D x V): its label's column of it, as a row.  A block takes EACH
 // tokens, so that a label read is compared with as many.
@@ -132,14 +216,10 @@ loss_rows(int T, int64_t V, int D, const E *__restrict__ H, int64_t ldh, E *__re
     pdl_enter();
     __shared__ int count[EACH];
     const int per = (D + 7) / 8;
-    if (sorted)
+    if (index)
         for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < V; v += (int64_t)gridDim.x * 256) index[v] = -1;
     const float f = scale ? __ldg(scale) : 1.f;
-    auto key = [&](int t) -> int {
-        const int64_t y = label_bytes == 8 ? __ldg(static_cast<const long long *>(labels) + t)
-                                           : (int64_t)__ldg(static_cast<const int32_t *>(labels) + t);
-        return y >= 0 && y < V ? (int)y : (int)V;
-    };
+    auto key = [&](int t) { return label_key(labels, label_bytes, t, V); };
     for (int64_t t0 = (int64_t)blockIdx.x * EACH; t0 < T; t0 += (int64_t)gridDim.x * EACH) {
         int mine[EACH];
 #pragma unroll
@@ -565,16 +645,17 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
     const int64_t part_rows = op_round_up(T, 256);
     const bool join = h_plan.parts > 1;
     Workspace ws;
-    // Ordering the labels takes T^2 comparisons: 0.02 ms for 8192 tokens, 1 for 65536.
-    // Beyond, dW is without the rests (dH is not).
-    const bool order = dW && T <= 65536;
+    // dW takes the label entries' rests by label, so the tokens are put in the order of their labels.
+    const bool order = dW != nullptr, passes = order && T > kCountTokens;
     const bool by_label = piece < T;
     const int64_t blocks = op_cdiv(T, kRun);
     const uint64_t at_index = ws.add(order ? (uint64_t)V * 4 : 0),
                    at_sums = ws.add(order ? (uint64_t)std::min(T, piece) * h_pitch * 4 : 0),
                    at_heads = ws.add(order ? (uint64_t)blocks * h_pitch * 4 : 0);
     const uint64_t at_rests = ws.add((uint64_t)T * 4),
-                   at_label_w = ws.add(dH && w_major ? (uint64_t)T * h_pitch * 2 : 0), at_sorted = ws.add((uint64_t)T * 4), at_tokens = ws.add((uint64_t)T * 4);
+                   at_label_w = ws.add(dH && w_major ? (uint64_t)T * h_pitch * 2 : 0), at_sorted = ws.add((uint64_t)T * 4), at_tokens = ws.add((uint64_t)T * 4),
+                   at_keys = ws.add(passes ? (uint64_t)T * 4 : 0), at_places = ws.add(passes ? (uint64_t)T * 4 : 0),
+                   at_counts = ws.add(passes ? kOrderBlocks * 256 * 4 : 0);
     const uint64_t at_rows = ws.add((uint64_t)T * 16), at_scale = ws.add(8), at_h = ws.add((uint64_t)T * h_pitch * 2),
                    at_d = ws.add((uint64_t)T * d_pitch * 2), at_w = ws.add((uint64_t)packed_w_bytes(a, piece)),
                    at_acc = ws.add(!dH ? 0 : join ? (uint64_t)h_plan.parts * part_rows * acc_pitch * 4 : pieces > 1 ? (uint64_t)T * acc_pitch * 4 : 0);
@@ -582,12 +663,29 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
     float4 *rows = reinterpret_cast<float4 *>(ws.base + at_rows);
     int32_t *index = reinterpret_cast<int32_t *>(ws.base + at_index);
     float *sums = reinterpret_cast<float *>(ws.base + at_sums);
-    int32_t *sorted = order ? reinterpret_cast<int32_t *>(ws.base + at_sorted) : nullptr, *tokens = reinterpret_cast<int32_t *>(ws.base + at_tokens);
+    int32_t *sorted = reinterpret_cast<int32_t *>(ws.base + at_sorted), *tokens = reinterpret_cast<int32_t *>(ws.base + at_tokens);
     float *rests = reinterpret_cast<float *>(ws.base + at_rests), *heads = reinterpret_cast<float *>(ws.base + at_heads);
     float *scale = reinterpret_cast<float *>(ws.base + at_scale), *acc = reinterpret_cast<float *>(ws.base + at_acc);
     if (f16 && rc == GEMM_OK)
         rc = op_launched("loss scale", launch_pdl(loss_scale, dim3(1), dim3(1024), 0, stream, T, V, grad, grad_stride, lse, labels,
                                                   label_bytes, a.how.z_loss, scale));
+    if (passes) {
+        const int64_t per = op_round_up(op_cdiv(T, kOrderBlocks), 256);
+        const dim3 grid((unsigned)op_cdiv(T, per));
+        int32_t *keys = reinterpret_cast<int32_t *>(ws.base + at_keys), *places = reinterpret_cast<int32_t *>(ws.base + at_places),
+                *counts = reinterpret_cast<int32_t *>(ws.base + at_counts);
+        OrderKeys in = {labels, label_bytes, V, nullptr, nullptr};
+        for (int shift = 0; rc == GEMM_OK && (V >> shift) > 0; shift += 8) {          // (keys are at most V)
+            rc = op_launched("label counts", launch_pdl(order_count, grid, dim3(256), 0, stream, T, per, shift, in, counts));
+            if (rc) break;
+            rc = op_launched("label order", launch_pdl(order_place, grid, dim3(256), 0, stream, T, per, shift, in,
+                                                       (const int32_t *)counts, keys, places));
+            std::swap(keys, sorted);
+            std::swap(places, tokens);
+            in.keys = sorted;
+            in.tokens = tokens;
+        }
+    }
     const bool wide = op_wide(H, a.ldh, 2) && D % 8 == 0;
     const int access = op_access(wide, &spans[0], 1);
     if (rc == GEMM_OK)
@@ -601,7 +699,8 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
                                               0, stream,
                                               (int)T, V, (int)D, static_cast<const E *>(H), a.ldh,
                                               reinterpret_cast<E *>(ws.base + at_h), h_pitch, grad, grad_stride, lse, labels,
-                                              label_bytes, a.how.z_loss, (const float *)(f16 ? scale : nullptr), rows, sorted, tokens, index,
+                                              label_bytes, a.how.z_loss, (const float *)(f16 ? scale : nullptr), rows,
+                                              order && !passes ? sorted : nullptr, tokens, order ? index : nullptr,
                                               static_cast<const E *>(dH && w_major ? W : nullptr), a.ldw,
                                               reinterpret_cast<E *>(ws.base + at_label_w)));
             };
