@@ -29,8 +29,9 @@ constexpr int kFinishWarps = 16;
 // 2641 and 1605; over 131072 labels (three) 4096 take 711 and 712.
 constexpr int64_t kCountTokens = 4096;
 constexpr int kOrderBlocks = 128;
-constexpr int kRun = 32;         // places in the order of the labels that a block of loss_rests takes
-constexpr int kJoinRuns = 8;     // blocks of loss_rests that one of loss_rests_join looks at
+constexpr int kRestWarps = 16;   // of loss_rests, at most
+constexpr int kWalk = 32;        // places in the order of the labels that each of them takes: one a thread to look up
+constexpr int kJoinBlocks = 8;   // blocks of loss_rests that one of loss_rests_join looks at
 
 // Token t's label, V for one that does not count.
 __device__ __forceinline__ int label_key(const void *labels, int label_bytes, int64_t t, int64_t V) {
@@ -267,89 +268,116 @@ loss_rows(int T, int64_t V, int D, const E *__restrict__ H, int64_t ldh, E *__re
 }
 
 // For each label in [first, first + cols) that a token has: the sum of the rests times
-// the rows of H over its tokens, in their order.  A block takes kRun places in the order of
-// the labels, two columns a thread, whatever labels they have; what it sums of a label that
-// begins in it goes to the label's row of `sums`, which `index` then names (by_label: the
-// label's own, else that of its first place), and what it sums of one that began before to
-// its row of `heads`, for loss_rests_join.  So a label that all tokens have takes no longer
-// than many: the gradients of 65536 x 8000 x 512 take 3.3 ms with one label for all and 3.5
-// with labels at random; a block a label took 17.5 and 3.9.
+// the rows of H over its tokens, in their order.  A warp takes kWalk places in the order of
+// the labels for 64 columns, whatever labels they have.  What it sums of a label that begins
+// there goes to the label's row of `sums`, which `index` then names (by_label: the label's
+// own, else that of its first place), together with what the warps behind sum of the same
+// label; and what a block sums of a label that began before it to its row of `heads`, for
+// loss_rests_join.  So a label that all tokens have takes no longer than many: the gradients
+// of 65536 x 8000 x 512 take 2.3 ms with one label for all and 2.5 with labels at random; a
+// block a label took 17.5 and 3.9.
 template <typename E>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kRestWarps)
 loss_rests(int T, int64_t first, int64_t cols, int D, int col_blocks, const int32_t *__restrict__ sorted,
            const int32_t *__restrict__ tokens, const float *__restrict__ rests, const E *__restrict__ H, int64_t ldh,
            int by_label, int32_t *index, float *__restrict__ sums, float *__restrict__ heads) {
     pdl_enter();
-    __shared__ int label[kRun + 1];              // of the place before and of the block's, in the piece (-1: elsewhere)
-    __shared__ int token[kRun];
-    __shared__ float rest[kRun];
-    const int block = blockIdx.x / col_blocks, c = ((int)(blockIdx.x - (unsigned)block * col_blocks) * 128 + (int)threadIdx.x) * 2;
-    const int64_t k0 = (int64_t)block * kRun;
-    int mine = -1;
-    if (threadIdx.x <= kRun) {
-        const int64_t k = k0 - 1 + threadIdx.x;
+    constexpr int kPlaces = kRestWarps * kWalk;
+    __shared__ int label[kPlaces + 1];           // of the place before and of the block's, in the piece (-1: elsewhere)
+    __shared__ int token[kPlaces];
+    __shared__ float rest[kPlaces];
+    __shared__ float2 head[kRestWarps][32];      // what a warp sums of a label that began before it
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, places = warps * kWalk;
+    const int block = blockIdx.x / col_blocks, c = ((int)(blockIdx.x - (unsigned)block * col_blocks) * 32 + lane) * 2;
+    const int64_t k0 = (int64_t)block * places;
+    auto in_piece = [&](int64_t k) {
         const int64_t y = k >= 0 && k < T ? __ldg(sorted + k) - first : -1;
-        mine = y >= 0 && y < cols ? (int)y : -1;
-        label[threadIdx.x] = mine;
-        if (threadIdx.x > 0) {
-            const int t = mine >= 0 ? __ldg(tokens + k) : 0;
-            token[threadIdx.x - 1] = t;
-            rest[threadIdx.x - 1] = mine >= 0 ? __ldg(rests + t) : 0.f;
-        }
-    }
-    if (!__syncthreads_or(threadIdx.x > 0 && mine >= 0) || c >= D) return;
-    const E *column = H + c;                     // (rows are padded to eight, with zeros)
-    float a = 0.f, b = 0.f;
-    int64_t row = -1;                            // of `sums`, or -1: the block's of `heads`
-    auto leave = [&](int y) {
-        if (y >= 0) *reinterpret_cast<float2 *>(row < 0 ? heads + block * ldh + c : sums + row * ldh + c) = make_float2(a, b);
+        return y >= 0 && y < cols ? (int)y : -1;
     };
-    for (int q0 = 0; q0 < kRun; q0 += 16) {
+    const int64_t k = k0 + threadIdx.x;          // (a place a thread)
+    const int before = threadIdx.x == 0 ? in_piece(k0 - 1) : -1, mine = in_piece(k), t = k < T ? __ldg(tokens + k) : 0;
+    if (threadIdx.x == 0) label[0] = before;
+    label[threadIdx.x + 1] = mine;
+    token[threadIdx.x] = t;
+    rest[threadIdx.x] = mine >= 0 ? __ldg(rests + t) : 0.f;
+    if (!__syncthreads_or(mine >= 0)) return;
+    const E *column = H + c;                     // (rows are padded to eight, with zeros)
+    const int q0 = warp * kWalk;
+    float a = 0.f, b = 0.f;
+    bool began = false;                          // the label did in this warp's places
+    int64_t row = 0;                             // its row of `sums`
+    auto store = [&](float *to, int64_t r) {
+        if (c < D) *reinterpret_cast<float2 *>(to + r * ldh + c) = make_float2(a, b);
+    };
+    for (int q1 = q0; q1 < q0 + kWalk; q1 += 16) {
         uint32_t w[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-            w[q] = label[q0 + q + 1] >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(column + token[q0 + q] * ldh)) : 0u;
+            w[q] = label[q1 + q + 1] >= 0 && c < D ? __ldg(reinterpret_cast<const uint32_t *>(column + token[q1 + q] * ldh)) : 0u;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-            const int y = label[q0 + q + 1], was = label[q0 + q];
+            const int y = label[q1 + q + 1], was = label[q1 + q];
             if (y != was) {
-                if (q0 + q > 0) leave(was);
+                if (q1 + q > q0 && was >= 0) {
+                    if (began) store(sums, row);
+                    else head[warp][lane] = make_float2(a, b);
+                }
                 a = b = 0.f;
-                row = by_label ? y : k0 + q0 + q;
+                began = true;
+                row = by_label ? y : k0 + q1 + q;
                 if (y >= 0 && c == 0) index[first + y] = (int32_t)row;
             }
             const E *pair = reinterpret_cast<const E *>(&w[q]);
-            a = fmaf(rest[q0 + q], OpType<E>::up(pair[0]), a);
-            b = fmaf(rest[q0 + q], OpType<E>::up(pair[1]), b);
+            a = fmaf(rest[q1 + q], OpType<E>::up(pair[0]), a);
+            b = fmaf(rest[q1 + q], OpType<E>::up(pair[1]), b);
         }
     }
-    leave(label[kRun]);
+    const int last = label[q0 + kWalk];
+    if (!began) head[warp][lane] = make_float2(a, b);
+    __syncthreads();
+    auto add_heads = [&](int from, int y) {      // of the warps that go on with the label
+        for (int w = from; w < warps && label[w * kWalk + 1] == y; ++w) {
+            a += head[w][lane].x;
+            b += head[w][lane].y;
+        }
+    };
+    if (began && last >= 0) {
+        add_heads(warp + 1, last);
+        store(sums, row);
+    }
+    if (warp == 0 && label[0] >= 0 && label[1] == label[0]) {
+        a = head[0][lane].x;
+        b = head[0][lane].y;
+        if (label[kWalk] == label[0]) add_heads(1, label[0]);
+        store(heads, block);
+    }
 }
 
-// What the labels that go on from one block of loss_rests into the next have in `heads`, added
-// to their rows of `sums`.  A block looks at kJoinRuns of them, for 64 columns; a label's heads
-// are shared out to its warps 16 at a time, and the warps' sums added in their order.
+// What the labels that go on from one block of loss_rests (`places` places) into the next have
+// in `heads`, added to their rows of `sums`.  A block looks at kJoinBlocks of them, for 64
+// columns; a label's heads are shared out to its warps 16 at a time, and the warps' sums added
+// in their order.
 __global__ void __launch_bounds__(256)
-loss_rests_join(int T, int64_t first, int64_t cols, int D, int col_blocks, const int32_t *__restrict__ sorted,
+loss_rests_join(int T, int64_t first, int64_t cols, int D, int col_blocks, int places, const int32_t *__restrict__ sorted,
                 const int32_t *__restrict__ index, const float *__restrict__ heads, int64_t ld, float *__restrict__ sums) {
     pdl_enter();
     __shared__ float2 part[8][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = blockIdx.x / col_blocks, c = ((int)(blockIdx.x - (unsigned)group * col_blocks) * 32 + lane) * 2;
-    const int64_t s0 = 1 + (int64_t)group * kJoinRuns;
+    const int64_t s0 = 1 + (int64_t)group * kJoinBlocks;
     // the first of a label's heads: the label went on into this block, but not into the one before
     bool starts = false;
     int y = -1;
-    if (lane < kJoinRuns && (s0 + lane) * kRun < T) {
-        const int64_t k = (s0 + lane) * kRun;
+    if (lane < kJoinBlocks && (s0 + lane) * places < T) {
+        const int64_t k = (s0 + lane) * places;
         y = __ldg(sorted + k);
-        starts = y >= first && y < first + cols && __ldg(sorted + k - 1) == y && (k == kRun || __ldg(sorted + k - kRun - 1) != y);
+        starts = y >= first && y < first + cols && __ldg(sorted + k - 1) == y && (k == places || __ldg(sorted + k - places - 1) != y);
     }
     for (uint32_t todo = __ballot_sync(0xffffffffu, starts); todo; todo &= todo - 1) {       // (the same in every warp)
         const int u = __ffs(todo) - 1, label = __shfl_sync(0xffffffffu, y, u);
         float a = 0.f, b = 0.f;
         for (int64_t s = s0 + u + warp * 16;; s += 8 * 16) {
-            const bool has = lane < 16 && (s + lane) * kRun < T && __ldg(sorted + (s + lane) * kRun) == label;
+            const bool has = lane < 16 && (s + lane) * places < T && __ldg(sorted + (s + lane) * places) == label;
             const int n = __popc(__ballot_sync(0xffffffffu, has));
             float2 x[16];
 #pragma unroll
@@ -648,7 +676,8 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
     // dW takes the label entries' rests by label, so the tokens are put in the order of their labels.
     const bool order = dW != nullptr, passes = order && T > kCountTokens;
     const bool by_label = piece < T;
-    const int64_t blocks = op_cdiv(T, kRun);
+    const int rest_warps = (int)std::min<int64_t>(kRestWarps, op_cdiv(T, kWalk));
+    const int64_t blocks = op_cdiv(T, rest_warps * kWalk);          // of loss_rests
     const uint64_t at_index = ws.add(order ? (uint64_t)V * 4 : 0),
                    at_sums = ws.add(order ? (uint64_t)std::min(T, piece) * h_pitch * 4 : 0),
                    at_heads = ws.add(order ? (uint64_t)blocks * h_pitch * 4 : 0);
@@ -770,10 +799,10 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
             if (order) {
                 auto go = [&](auto e) {
                     using E = decltype(e);
-                    const int64_t wide = op_cdiv(D, 256);
+                    const int64_t wide = op_cdiv(D, 64);
                     return op_launched("loss rests",
-                                       launch_pdl(loss_rests<E>, dim3((unsigned)(blocks * wide)), dim3(128), 0, stream, (int)T, v, cols,
-                                                  (int)D, (int)wide, (const int32_t *)sorted, (const int32_t *)tokens,
+                                       launch_pdl(loss_rests<E>, dim3((unsigned)(blocks * wide)), dim3(32 * rest_warps), 0, stream,
+                                                  (int)T, v, cols, (int)D, (int)wide, (const int32_t *)sorted, (const int32_t *)tokens,
                                                   (const float *)rests, reinterpret_cast<const E *>(ws.base + at_h), h_pitch,
                                                   by_label ? 1 : 0, index, sums, heads));
                 };
@@ -781,8 +810,8 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
                 if (blocks > 1) {
                     const int64_t wide = op_cdiv(D, 64);
                     rc = op_launched("loss rests join",
-                                     launch_pdl(loss_rests_join, dim3((unsigned)(op_cdiv(blocks - 1, kJoinRuns) * wide)), dim3(256), 0,
-                                                stream, (int)T, v, cols, (int)D, (int)wide, (const int32_t *)sorted,
+                                     launch_pdl(loss_rests_join, dim3((unsigned)(op_cdiv(blocks - 1, kJoinBlocks) * wide)), dim3(256), 0,
+                                                stream, (int)T, v, cols, (int)D, (int)wide, rest_warps * kWalk, (const int32_t *)sorted,
                                                 (const int32_t *)index, (const float *)heads, h_pitch, sums));
                     if (rc) break;
                 }
