@@ -222,3 +222,24 @@ def test_options(lib):
             assert tg.gemm_set_option(key, v) == tg.GEMM_OK and tg.gemm_get_option(key) == v
         for v in bad:
             assert tg.gemm_set_option(key, v) == BAD and tg.gemm_get_option(key) == 0
+
+
+def test_the_series_of_tanh_is_within_a_unit_in_the_last_place():
+    # the kernel's coefficients and steps (fused multiply-adds in FP32) against tanh in 64 bits on (0, 1/2]
+    import numpy as np
+    src = open(os.path.join(ROOT, "tiled_tensor_core_gemm_gb300", "csrc", "project.cu")).read()
+    body = src[src.index("void tanh_64("):]
+    body = body[:body.index("tanhf")]
+    coeffs = [np.float32(np.float32(a) / np.float32(b)) for a, b in re.findall(r"both\((-?\d+)\.f / (\d+)\.f\)", body)]
+    assert "most <= 0.5f" in body and len(coeffs) >= 6
+    x = np.linspace(2.0 ** -12, 0.5, 200001).astype(np.float32)
+
+    def fma(a, b, c):
+        return (a.astype(np.float64) * b + c).astype(np.float32)
+    q = x * x
+    r = np.full_like(x, coeffs[0])
+    for c in coeffs[1:]:
+        r = fma(r, q, np.float64(c))
+    got = fma(r * q, x, x)
+    want = np.tanh(x.astype(np.float64))
+    assert float((np.abs(got - want) / np.spacing(want.astype(np.float32))).max()) <= 1.0
