@@ -431,12 +431,13 @@ __device__ __forceinline__ void add_columns(uint32_t src, float (&v)[COLS]) {
 __device__ __forceinline__ void store_box_plain(const ProductParams &p, const Tile &T, uint32_t buf, int64_t i0,
                                                 int64_t jb, bool half, int lane) {
     const int rows = T.i1 - i0 < 32 ? (int)(T.i1 - i0) : 32;
+    const int64_t row0 = i0 + T.down;
     const int most = half ? 64 : 32;
     const int cols = (int)(T.j1 - jb < most ? T.j1 - jb : most);
 #pragma unroll 2
     for (int r = 0; r < rows; ++r) {
         const uint32_t from = buf + 128u * (uint32_t)r;
-        const int64_t at = (i0 + r) * p.ldc + jb + lane;
+        const int64_t at = (row0 + r) * p.ldc + jb + lane;
         const uint32_t sw = (uint32_t)(r & 7) << 4;
         if (half) {
             uint16_t *d = static_cast<uint16_t *>(p.C) + at;
