@@ -902,3 +902,49 @@ def test_loss_gradient_of_the_tokens_past_32_bits():
     at = torch.tensor([0, 1, 32800, 65074, 65075, 65076, T - 2, T - 1], device="cuda")
     want = exact_loss(H[at], W, y[at], g[at])["dH"]
     within(dH[at], *want, "dH")
+
+
+@pytest.mark.parametrize("layout", ("vd", "dv"))
+@pytest.mark.parametrize("T,V,D,columns", [(4097, 1, 8, 0), (4097, 255, 9, 64), (4100, 256, 1, 0), (5000, 65535, 16, 0), (4500, 65536, 24, 1024),
+                                           (520, 40, 65, 0), (1030, 300, 130, 0)])
+def test_loss_gradients_of_tokens_ordered_by_label(T, V, D, columns, layout):
+    # labels of one, two and three bytes, tokens in several blocks of sums
+    tg.gemm_set_option("loss_columns", columns)
+    H, W, y = made_loss(T, V, D, BF16, layout, seed=80)
+    y[1::2] = torch.where(y[1::2] >= 0, V // 2, y[1::2])
+    g = randn(T, seed=81)
+    _, lse, dH, dW = check_loss(H, W, y, g)
+    again = tg.project_loss_backward(g, H, W, y, lse)
+    assert torch.equal(again[0], dH) and torch.equal(again[1], dW)
+    none = torch.full_like(y, V)
+    dH, dW = tg.project_loss_backward(g, H, W, none, lse)
+    assert not bool(dH.any()) and not bool(dW.any())
+    only = tg.project_loss_backward(g, H, W, y, lse, want_W=False)
+    assert torch.equal(only[0], again[0]) and only[1] is None
+
+
+def test_loss_gradients_of_many_tokens_in_cuda_graphs_that_run_at_once():
+    H, V, y = made_loss(5000, 700, 128, BF16, seed=82)
+    g = randn(5000, seed=83)
+
+    def step():
+        loss, lse = tg.project_loss(H, V, y)
+        return loss, *tg.project_loss_backward(g, H, V, y, lse)
+    step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out, torch.cuda.Stream()))
+    y.copy_(randint(-1, 5, 5000, seed=84))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, _, st in graphs:
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    want = step()
+    for _, out, _ in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
