@@ -63,7 +63,7 @@ GEMM_API int gemm_project_loss(int64_t T, int64_t V, int64_t D, int dtype, const
  * gradient d is rounded to `dtype` (with FP16 scaled by a power of two so that the
  * largest fits and the small ones keep their digits) and goes into both products;
  * dH is summed over the pieces in FP32.  What rounding takes from a row's largest
- * entry, the label's, is added back in FP32 (to dW for up to 65536 tokens).  A token without a label adds nothing,
+ * entry, the label's, is added back in FP32.  A token without a label adds nothing,
  * whatever H[t] and grad[t] hold, and gets a zero row in dH (W must be finite).
  *
  *   grad         T floats, grad_stride (0: one value for all, or 1) apart
@@ -81,7 +81,8 @@ GEMM_API int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dty
  * gemm_adapter_plan -- which tokens take which adapter, in the form the products
  * below read it.  ids: T int32, token t takes adapter ids[t]; values outside
  * [0, adapters) take none.  Tokens may come in any order; the products cost least
- * when neighbours share an adapter.  One plan serves every projection of a step.
+ * when neighbours share an adapter, for the tokens of a granule (16 to 256 neighbours)
+ * take the products of all its adapters.  One plan serves every projection of a step.
  *
  *   plan         gemm_adapter_plan_words(T, adapters, backward) int32 words
  *   backward     1: with what gemm_adapters_backward needs besides

@@ -3,12 +3,14 @@
 // together.
 //
 // C = X W + s (X A_i^T) B_i takes two launches: `low`, the rank-wide activations of
-// every token in the slot of its adapter (one pass over X and over the adapters in
-// use), and the projection, whose K-blocks go on over the slots of the tile's
-// granule.  The projection does not wait for `low` until its own K-blocks are in.
-// What bounds it: the weight stream for few tokens (W, and the adapters in use once
-// each), the tensor cores for many, where the slots add (slots x rank) / K to the
-// flops.
+// every token in the slot of its adapter (X once for every 128 lanes of slots x rank of a
+// tile's tokens, the adapters in use once a tile), and the projection, whose K-blocks go
+// on over the slots of the tile's granule.  The projection does not wait for `low` until
+// its own K-blocks are in.  What bounds it: the weight stream for few tokens (W, and the
+// adapters in use once each), the tensor cores for many, where the slots add
+// (slots x rank) / K to the projection's flops and as many again to low's: 8192 tokens
+// over 64 adapters of rank 64, 4096 x 4096, take 199 us in the adapters' order and 635 in
+// a random one (62 slots a granule).
 #include <algorithm>
 
 #include "gemm_project.h"

@@ -544,7 +544,6 @@ ProductLoss loss_of(const LossArgs &a) {
     ProductLoss l;
     l.labels = a.labels;
     l.label_bytes = a.label_bytes;
-    l.vocab = a.V;
     l.softcap = a.how.softcap;
     l.eps_v = a.how.smoothing / (float)a.V;
     l.one_eps = 1.f - a.how.smoothing;
@@ -664,7 +663,7 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
     if ((rc = plan_packs(&a))) return rc;
     const int et = a.type;
     const bool f16 = et == GEMM_OUT_F16;
-    // A piece's d is at most 256 MB
+    // A piece's d is at most 256 MB, or 256 columns: 512 bytes a token beyond 524288 tokens
     const int64_t piece = piece_columns(V, (1LL << 27) / T);
     const int64_t pieces = op_cdiv(V, piece), d_pitch = op_round_up(piece, 64), h_pitch = op_round_up(D, 8),
                   acc_pitch = op_round_up(D, 64);

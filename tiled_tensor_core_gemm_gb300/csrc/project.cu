@@ -37,7 +37,7 @@
 // in small tiles (of which the MMAs' issue is about half) and 8 us around them.
 //
 // Roles as in scaled.cu: warp 0 issues the TMA loads into a ring, warp 1 the MMAs
-// (K = 64 a ring slot, one 128-byte swizzle row), and from warp 4 on the epilogue
+// (two K-blocks of 64 a ring slot, one 128-byte swizzle row each), and from warp 4 on the epilogue
 // warps, which read one of two accumulators while the MMAs fill the other.  Either
 // operand in either major: K-major as rows of 64 values, MN-major in chunks of 64
 // rows of K by 64 values.  Every wait is bounded; a role that gives up waits,

@@ -38,8 +38,7 @@ struct ProductAdapters {
 struct ProductLoss {
     const void *labels = nullptr;
     int label_bytes = 8;
-    int64_t vocab = 0;         // of the whole projection; `first` is this call's first column
-    int64_t first = 0;
+    int64_t first = 0;         // this call's first column of the whole vocabulary
     float softcap = 0.f, eps_v = 0.f, one_eps = 1.f;   // smoothing / vocab, 1 - smoothing
     int want_sum = 0;          // label smoothing: the sum of the logits too
     float2 *parts = nullptr;   // [part][token]: maximum (in base 2) and sum of the exponentials
