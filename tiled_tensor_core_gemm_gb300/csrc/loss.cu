@@ -202,12 +202,12 @@ order_place(int64_t T, int64_t per, int shift, OrderKeys in, const int32_t *__re
 }
 
 // Per token: what the logits' gradient takes (project.cu: take_gradient): lse in base 2,
-// grad (1 + 2 a lse), grad, and whether the token counts; with `sorted` the tokens in
-// the order of the labels (ties in the order of the tokens, tokens that do not count last),
-// each by counting the labels before its own; `index` cleared; and H's row, at a pitch TMA can address, zero for a token
-// that does not count, so that nothing it holds (padding may be anything) reaches dW as
-// 0 x NaN.  With W (held D x V): its label's column of it, as a row.  A block takes EACH
-// tokens, so that a label read is compared with as many.
+// grad (1 + 2 a lse), grad, and whether the token counts; with `sorted` the tokens in the
+// order of the labels (ties in the order of the tokens, tokens that do not count last), each
+// by counting the labels before its own; `index` cleared; and H's row, at a pitch TMA can
+// address, zero for a token that does not count, so that nothing it holds (padding may be
+// anything) reaches dW as 0 x NaN.  With W (held D x V): its label's column of it, as a row.
+// A block takes EACH tokens, so that a label read is compared with as many.
 template <int ACCESS, int EACH, typename E>
 __global__ void __launch_bounds__(256)
 loss_rows(int T, int64_t V, int D, const E *__restrict__ H, int64_t ldh, E *__restrict__ out, int64_t ldo,
@@ -681,7 +681,8 @@ int gemm_project_loss_backward(int64_t T, int64_t V, int64_t D, int dtype, const
                    at_sums = ws.add(order ? (uint64_t)std::min(T, piece) * h_pitch * 4 : 0),
                    at_heads = ws.add(order ? (uint64_t)blocks * h_pitch * 4 : 0);
     const uint64_t at_rests = ws.add((uint64_t)T * 4),
-                   at_label_w = ws.add(dH && w_major ? (uint64_t)T * h_pitch * 2 : 0), at_sorted = ws.add((uint64_t)T * 4), at_tokens = ws.add((uint64_t)T * 4),
+                   at_label_w = ws.add(dH && w_major ? (uint64_t)T * h_pitch * 2 : 0),
+                   at_sorted = ws.add((uint64_t)T * 4), at_tokens = ws.add((uint64_t)T * 4),
                    at_keys = ws.add(passes ? (uint64_t)T * 4 : 0), at_places = ws.add(passes ? (uint64_t)T * 4 : 0),
                    at_counts = ws.add(passes ? kOrderBlocks * 256 * 4 : 0);
     const uint64_t at_rows = ws.add((uint64_t)T * 16), at_scale = ws.add(8), at_h = ws.add((uint64_t)T * h_pitch * 2),
